@@ -36,6 +36,17 @@ EXPORTS = (
     "dora_compose_bwd_noalloc",
     "dora_norm_bwd_workspace_bytes",
     "dora_norm_bwd",
+    "dora_q8_pack",
+    "dora_q8_pack_weight",
+    "dora_q8_unpack",
+    "dora_q8_linear_workspace_bytes",
+    "dora_q8_linear_fwd",
+    "dora_q8_linear_bwd_workspace_bytes",
+    "dora_q8_linear_bwd",
+    "dora_q8_lora_compose_bwd_workspace_bytes",
+    "dora_q8_lora_compose_bwd",
+    "dora_q8_grad_a_workspace_bytes",
+    "dora_q8_grad_a",
     "dora_last_error",
     "dora_version",
 )
@@ -78,6 +89,22 @@ def _load() -> ctypes.CDLL:
     lib.dora_norm_bwd_workspace_bytes.restype = sz
     lib.dora_norm_bwd.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, f32, i32, vp, vp, vp, sz, vp]
     lib.dora_norm_bwd.restype = i32
+    lib.dora_q8_pack.argtypes = lib.dora_q8_pack_weight.argtypes = [vp, i64, i64, i32, vp, vp, vp]
+    lib.dora_q8_pack.restype = lib.dora_q8_pack_weight.restype = i32
+    lib.dora_q8_unpack.argtypes = [vp, vp, i64, i64, i32, i32, vp, vp]
+    lib.dora_q8_unpack.restype = i32
+    for name in ("dora_q8_linear_workspace_bytes", "dora_q8_linear_bwd_workspace_bytes",
+                 "dora_q8_lora_compose_bwd_workspace_bytes", "dora_q8_grad_a_workspace_bytes"):
+        getattr(lib, name).argtypes = [i64, i64, i64]
+        getattr(lib, name).restype = sz
+    for name in ("dora_q8_linear_fwd", "dora_q8_linear_bwd"):
+        getattr(lib, name).argtypes = [vp, vp, vp, vp, i64, i64, i64, i32, vp, vp, sz, vp]
+        getattr(lib, name).restype = i32
+    lib.dora_q8_lora_compose_bwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, f32, i64, i64, i64, i32, i32, vp, vp, vp, vp,
+                                             vp, vp, sz, vp]
+    lib.dora_q8_lora_compose_bwd.restype = i32
+    lib.dora_q8_grad_a.argtypes = [vp, vp, vp, i64, i64, i64, i32, vp, vp, sz, vp]
+    lib.dora_q8_grad_a.restype = i32
     lib.dora_last_error.argtypes = []
     lib.dora_last_error.restype = ctypes.c_char_p
     lib.dora_version.argtypes = []
@@ -350,3 +377,166 @@ def dora_norm_bwd(W0, A, B, norm, d_norm, s: float, d_A=None, d_B=None, workspac
                              _ptr(d_A), _ptr(d_B), _ptr(workspace), workspace.numel() * workspace.element_size(),
                              _stream(dev)))
     return d_A, d_B
+
+
+# ------------------------------------------------------------ the frozen side in 8 bits
+#
+# A packed matrix is a pair (q, e): torch.float8_e4m3fn values and uint8 exponent
+# bytes in the layout of include/dora.h.  These calls run on the tensors' own
+# device, whatever the current one is.
+
+Q8_BLOCK = 128
+
+
+def q8_row_shapes(rows: int, cols: int):
+    """Shapes of (q, e) for packed rows [rows x cols]."""
+    nb = -(-cols // Q8_BLOCK)
+    return (rows, nb * Q8_BLOCK), (rows, -(-nb // 4) * 4)
+
+
+def q8_weight_shapes(out: int, in_: int):
+    """Shapes of (q, e) for a packed weight [out x in]."""
+    ob = -(-out // Q8_BLOCK)
+    q, e = q8_row_shapes(ob, in_)
+    return (ob * Q8_BLOCK, q[1]), e
+
+
+def _packed(q, e, name, shapes, device):
+    _matrix(q, name, shapes[0], torch.float8_e4m3fn, device)
+    _matrix(e, name + "'s exponents", shapes[1], torch.uint8, device)
+    if q.data_ptr() % 16 or e.data_ptr() % 4:
+        raise ValueError(f"{name} must be 16-byte aligned, its exponents 4-byte")
+
+
+def _dtype_code(dtype) -> int:
+    if dtype not in DTYPE_CODE:
+        raise ValueError(f"unsupported dtype {dtype}; bf16 and fp16 are")
+    return DTYPE_CODE[dtype]
+
+
+def _on_gpu(t, name):
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be on a HIP device")
+    return t.device
+
+
+def _new_packed(shapes, device):
+    return (torch.empty(shapes[0], dtype=torch.float8_e4m3fn, device=device),
+            torch.empty(shapes[1], dtype=torch.uint8, device=device))
+
+
+def _workspace(need: int, device):
+    return torch.empty(max(need, 1), dtype=torch.uint8, device=device)
+
+
+def dora_q8_pack(x):
+    """(q, e): the rows of x [T x K] in blocks of 128 columns."""
+    code = _code(x)
+    rows, cols = x.shape
+    _matrix(x, "x", (rows, cols))
+    with torch.cuda.device(x.device):
+        q, e = _new_packed(q8_row_shapes(rows, cols), x.device)
+        _check(LIB.dora_q8_pack(_ptr(x), rows, cols, code, _ptr(q), _ptr(e), _stream(x.device)))
+    return q, e
+
+
+def dora_q8_pack_weight(W):
+    """(q, e): the weight W [out x in] in blocks of 128 x 128."""
+    code = _code(W)
+    out, in_ = W.shape
+    _matrix(W, "W", (out, in_))
+    with torch.cuda.device(W.device):
+        q, e = _new_packed(q8_weight_shapes(out, in_), W.device)
+        _check(LIB.dora_q8_pack_weight(_ptr(W), out, in_, code, _ptr(q), _ptr(e), _stream(W.device)))
+    return q, e
+
+
+def dora_q8_unpack(q, e, rows: int, cols: int, dtype, weight: bool = False):
+    """The values of packed rows, or of the first rows of a packed weight, in dtype."""
+    code, dev = _dtype_code(dtype), _on_gpu(q, "q")
+    if weight:
+        if not 0 <= rows <= q.shape[0]:
+            raise ValueError(f"rows {rows} out of range of a packed weight of {q.shape[0]}")
+        _packed(q, e, "q", q8_weight_shapes(q.shape[0], cols), dev)
+    else:
+        _packed(q, e, "q", q8_row_shapes(rows, cols), dev)
+    with torch.cuda.device(dev):
+        x = torch.empty((rows, cols), dtype=dtype, device=dev)
+        _check(LIB.dora_q8_unpack(_ptr(q), _ptr(e), rows, cols, int(weight), code, _ptr(x), _stream(dev)))
+    return x
+
+
+def dora_q8_linear_fwd(xq, xe, wq, we, out: int, in_: int, dtype):
+    """y [T x out] = x W^T from packed rows [T x in] and a packed weight [out x in]."""
+    code, dev, T = _dtype_code(dtype), _on_gpu(xq, "xq"), xq.shape[0]
+    _packed(xq, xe, "xq", q8_row_shapes(T, in_), dev)
+    _packed(wq, we, "wq", q8_weight_shapes(out, in_), dev)
+    with torch.cuda.device(dev):
+        y = torch.empty((T, out), dtype=dtype, device=dev)
+        ws = _workspace(int(LIB.dora_q8_linear_workspace_bytes(T, out, in_)), dev)
+        _check(LIB.dora_q8_linear_fwd(_ptr(xq), _ptr(xe), _ptr(wq), _ptr(we), T, out, in_, code, _ptr(y), _ptr(ws),
+                                      ws.numel(), _stream(dev)))
+    return y
+
+
+def dora_q8_linear_bwd(gq, ge, wq, we, out: int, in_: int, dtype):
+    """dx [T x in] = g W from packed rows [T x out] and a packed weight [out x in]."""
+    code, dev, T = _dtype_code(dtype), _on_gpu(gq, "gq"), gq.shape[0]
+    _packed(gq, ge, "gq", q8_row_shapes(T, out), dev)
+    _packed(wq, we, "wq", q8_weight_shapes(out, in_), dev)
+    with torch.cuda.device(dev):
+        dx = torch.empty((T, in_), dtype=dtype, device=dev)
+        ws = _workspace(int(LIB.dora_q8_linear_bwd_workspace_bytes(T, out, in_)), dev)
+        _check(LIB.dora_q8_linear_bwd(_ptr(gq), _ptr(ge), _ptr(wq), _ptr(we), T, out, in_, code, _ptr(dx), _ptr(ws),
+                                      ws.numel(), _stream(dev)))
+    return dx
+
+
+def _aligned(t):
+    """t itself, or a copy where a slice starts off a 16-byte boundary."""
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
+def dora_q8_lora_compose_bwd(dy, bq, be, h, B, mag, norm, s: float, add_base: bool = False, want_d_base: bool = True,
+                             packed: bool = False):
+    """(d_base, d_B, d_mag) of the fused compose with the base from packed rows.
+    d_base is None if not wanted, or with packed the pair (q, e)."""
+    code = _code(dy)
+    T, out = dy.shape
+    r, dev = h.shape[1], dy.device
+    _matrix(dy, "dy", (T, out))
+    _packed(bq, be, "bq", q8_row_shapes(T, out), dev)
+    _matrix(h, "h", (T, r), dy.dtype, dev)
+    _matrix(B, "B", (out, r), dy.dtype, dev)
+    _matrix(mag, "mag", (out,), torch.float32, dev)
+    _matrix(norm, "norm", (out,), torch.float32, dev)
+    dy, h, B = _aligned(dy), _aligned(h), _aligned(B)
+    with torch.cuda.device(dev):
+        d_base = q = e = None
+        if want_d_base and packed:
+            q, e = _new_packed(q8_row_shapes(T, out), dev)
+        elif want_d_base:
+            d_base = torch.empty((T, out), dtype=dy.dtype, device=dev)
+        d_B = torch.empty((out, r), dtype=dy.dtype, device=dev)
+        d_mag = torch.empty(out, dtype=torch.float32, device=dev)
+        ws = _workspace(int(LIB.dora_q8_lora_compose_bwd_workspace_bytes(T, out, r)), dev)
+        _check(LIB.dora_q8_lora_compose_bwd(_ptr(dy), _ptr(bq), _ptr(be), _ptr(h), _ptr(B), _ptr(mag), _ptr(norm),
+                                            float(s), T, out, r, code, int(bool(add_base)), _ptr(d_base), _ptr(q),
+                                            _ptr(e), _ptr(d_B), _ptr(d_mag), _ptr(ws), ws.numel(), _stream(dev)))
+    return (q, e) if q is not None else d_base, d_B, d_mag
+
+
+def dora_q8_grad_a(dh, xq, xe, in_: int):
+    """d_A [r x in] = d_h^T x from packed rows x [T x in]."""
+    code = _code(dh)
+    T, r = dh.shape
+    dev = dh.device
+    _matrix(dh, "dh", (T, r))
+    _packed(xq, xe, "xq", q8_row_shapes(T, in_), dev)
+    dh = _aligned(dh)
+    with torch.cuda.device(dev):
+        d_A = torch.empty((r, in_), dtype=dh.dtype, device=dev)
+        ws = _workspace(int(LIB.dora_q8_grad_a_workspace_bytes(T, in_, r)), dev)
+        _check(LIB.dora_q8_grad_a(_ptr(dh), _ptr(xq), _ptr(xe), T, in_, r, code, _ptr(d_A), _ptr(ws), ws.numel(),
+                                  _stream(dev)))
+    return d_A

@@ -1,13 +1,8 @@
 // C ABI of the DoRA hot path: argument validation, workspace queries, launch
 // selection (16-byte fast path or general path) and the per-thread error string.
 // Every check runs before the first HIP call, so invalid calls touch no device.
-#include <stdarg.h>
-#include <stdio.h>
-#include <string.h>
-
-#include <string>
-
 #include "../../include/dora.h"
+#include "abi_common.hpp"
 #include "compose_kernels.hpp"
 #include "lora_compose_kernels.hpp"
 #include "noalloc_kernels.hpp"
@@ -18,47 +13,9 @@
 #define DORA_VERSION_STRING "0.1.0"
 #endif
 
+using namespace dora::abi;
+
 namespace {
-
-thread_local std::string g_err;
-
-int fail(int status, const char* fmt, ...) {
-  char buf[512];
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(buf, sizeof(buf), fmt, ap);
-  va_end(ap);
-  g_err = buf;
-  return status;
-}
-
-int ok() {
-  g_err.clear();
-  return DORA_OK;
-}
-
-int hip_status(hipError_t e, const char* what) {
-  if (e == hipSuccess) return ok();
-  return fail(DORA_HIP_ERROR, "%s: %s", what, hipGetErrorString(e));
-}
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-// Two byte ranges [p, p + n) and [q, q + m) that overlap without being the same buffer.
-bool partial_overlap(const void* p, size_t n, const void* q, size_t m) {
-  if (!p || !q || n == 0 || m == 0) return false;
-  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
-  if (a == b && n == m) return false;
-  return a < b + m && b < a + n;
-}
-
-bool any_overlap(const void* p, size_t n, const void* q, size_t m) {
-  if (!p || !q || n == 0 || m == 0) return false;
-  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
-  return a < b + m && b < a + n;
-}
-
-bool valid_dtype(int dtype) { return dtype == DORA_BF16 || dtype == DORA_F16; }
 
 // Longest serial chain (T * r products per thread) the slow path of
 // dora_lora_compose_bwd is allowed to run.
@@ -161,7 +118,7 @@ int compose_bwd_call(const char* fn, const void* dy, const void* base, const voi
 
 extern "C" {
 
-const char* dora_last_error(void) { return g_err.c_str(); }
+const char* dora_last_error(void) { return g_err; }
 
 const char* dora_version(void) { return "dora_fine_tuning_amd " DORA_VERSION_STRING " (HIP, gfx950)"; }
 

@@ -26,6 +26,13 @@ This module registers:
   (+ base), g = m / n. Its autograd formula is the fused backward
   ``dora_amd::compose_backward``, which gives the gradients of base, lora and
   the magnitude m.
+* the 8-bit operators: ``q8_pack`` / ``q8_pack_weight`` / ``q8_unpack`` /
+  ``q8_unpack_weight`` (e4m3 blocks of 128 with a power-of-two scale each),
+  ``q8_linear`` and ``q8_linear_backward`` (the frozen layer's product and its
+  gradient of x, on packed operands), ``q8_lora_compose_backward`` (and
+  ``_packed``: the compose's backward from the base kept in 8 bits) and
+  ``q8_grad_a`` (the gradient of A from x kept in 8 bits).  ``q8_layer`` runs
+  them together under autograd.
 * ``DoRALinear`` -- a linear layer with frozen W0 and trainable A, B and m:
   y = x W0^T + compose(x W0^T, x A^T B^T, m, n, s), with n = ||W0 + s*B*A||
   detached by default.  With ``detach_norm=False`` the gradient also flows
@@ -51,6 +58,7 @@ On that path every operator is argument marshalling around the C ABI
 from __future__ import annotations
 
 import math
+from typing import Optional
 
 import numpy as np
 import torch
@@ -354,6 +362,350 @@ lora_compose.register_kernel("cpu")(_eager_lora_compose)
 lora_compose_backward.register_kernel("cpu")(_eager_lora_compose_backward)
 
 
+# ------------------------------------------------------------ the frozen side in 8 bits
+#
+# Packed matrices are pairs (q, e): float8_e4m3fn values in blocks of 128 (of a
+# row, or 128 x 128 of a weight) and uint8 exponent bytes 127 + e, laid out as
+# include/dora.h says.  W0 is frozen and x and base are needed by the backward
+# only inside sums over the tokens, so 8 bits hold them.
+
+_F8 = torch.float8_e4m3fn
+
+
+def _round_up(n: int, k: int) -> int:
+    return -(-n // k) * k
+
+
+def _exp2i(k: Tensor) -> Tensor:
+    """2^k in fp32 for whole k in [-126, 127], by its exponent field (exact on every device)."""
+    return ((k.to(torch.int32) + 127) << 23).view(torch.float32)
+
+
+def _eager_blocks(v: Tensor, dims) -> tuple[Tensor, Tensor]:
+    """(values, exponent bytes) of fp32 blocks that lie along ``dims``."""
+    amax = torch.where(torch.isfinite(v), v.abs(), torch.zeros_like(v)).amax(dim=dims, keepdim=True)
+    bits = amax.view(torch.int32)  # 448 = 1.75 * 2^8
+    e = ((bits >> 23) - 127 - 8 + ((bits & 0x7FFFFF) > 0x600000).to(torch.int32)).clamp(min=-126)
+    q = torch.where(torch.isfinite(v), v * _exp2i(-e), torch.full_like(v, math.nan))
+    return q.to(_F8), (e + 127).to(torch.uint8)
+
+
+def _padded_exponents(e: Tensor) -> Tensor:
+    return F.pad(e, (0, _round_up(e.shape[1], 4) - e.shape[1]), value=127)
+
+
+def _eager_q8_pack(x):
+    T, K = x.shape
+    v = F.pad(x.float(), (0, _round_up(K, 128) - K)).reshape(T, -1, 128)
+    if v.numel() == 0:
+        (qs, es) = binding.q8_row_shapes(T, K)
+        return x.new_empty(qs, dtype=_F8), x.new_empty(es, dtype=torch.uint8)
+    q, e = _eager_blocks(v, (2,))
+    return q.reshape(T, -1), _padded_exponents(e[:, :, 0])
+
+
+def _eager_q8_pack_weight(W):
+    o, i = W.shape
+    if W.numel() == 0:
+        (qs, es) = binding.q8_weight_shapes(o, i)
+        return W.new_empty(qs, dtype=_F8), W.new_empty(es, dtype=torch.uint8)
+    v = F.pad(W.float(), (0, _round_up(i, 128) - i, 0, _round_up(o, 128) - o))
+    q, e = _eager_blocks(v.reshape(v.shape[0] // 128, 128, -1, 128), (1, 3))
+    return q.reshape(v.shape), _padded_exponents(e[:, 0, :, 0])
+
+
+def _values(q, e, cols, weight=False):
+    """The fp32 values of packed rows (or of a packed weight)."""
+    nb = q.shape[1] // 128
+    s = _exp2i(e[:, :nb].to(torch.int32) - 127)
+    s = s.repeat_interleave(128, dim=1)
+    if weight:
+        s = s.repeat_interleave(128, dim=0)
+    return (q.float() * s)[:, :cols]
+
+
+def _held(v, dtype):
+    big = torch.finfo(dtype).max
+    return v.clamp(-big, big).to(dtype)
+
+
+def _eager_q8_unpack(q, e, cols, dtype):
+    return _held(_values(q, e, cols), dtype)
+
+
+def _eager_q8_unpack_weight(q, e, rows, cols, dtype):
+    return _held(_values(q, e, cols, True)[:rows], dtype)
+
+
+def _eager_q8_linear(xq, xe, wq, we, out_features, dtype):
+    return (_values(xq, xe, xq.shape[1]) @ _values(wq, we, wq.shape[1], True)[:out_features].t()).to(dtype)
+
+
+def _eager_q8_linear_backward(gq, ge, wq, we, in_features, dtype):
+    return (_values(gq, ge, gq.shape[1]) @ _values(wq, we, in_features, True)).to(dtype)
+
+
+def _eager_q8_lora_compose_backward(dy, bq, be, h, B, mag, norm, s, add_base, want_base):
+    base = _values(bq, be, dy.shape[1])
+    return _eager_lora_compose_backward(dy, base, h, B, mag, norm, s, add_base, want_base)
+
+
+def _eager_q8_lora_compose_backward_packed(dy, bq, be, h, B, mag, norm, s, add_base):
+    _, d_B, d_mag = _eager_q8_lora_compose_backward(dy, bq, be, h, B, mag, norm, s, add_base, False)
+    g, gm1 = _scales(mag, norm)
+    q, e = _eager_q8_pack((g if add_base else gm1) * dy.float())
+    return q, e, d_B, d_mag
+
+
+def _eager_q8_grad_a(dh, xq, xe, in_features):
+    return (dh.float().t() @ _held(_values(xq, xe, in_features), dh.dtype).float()).to(dh.dtype)
+
+
+@torch.library.custom_op("dora_amd::q8_pack", mutates_args=(), device_types="cuda")
+def q8_pack(x: Tensor) -> tuple[Tensor, Tensor]:
+    """(q, e): the rows of x [T x K] in 8-bit blocks of 128 columns."""
+    if not _kernels_take(x):
+        return _eager_q8_pack(x)
+    return binding.dora_q8_pack(x.contiguous())
+
+
+@q8_pack.register_fake
+def _q8_pack_fake(x):
+    qs, es = binding.q8_row_shapes(x.shape[0], x.shape[1])
+    return x.new_empty(qs, dtype=_F8), x.new_empty(es, dtype=torch.uint8)
+
+
+@torch.library.custom_op("dora_amd::q8_pack_weight", mutates_args=(), device_types="cuda")
+def q8_pack_weight(W: Tensor) -> tuple[Tensor, Tensor]:
+    """(q, e): a weight [out x in] in 8-bit blocks of 128 x 128 (once: it is frozen)."""
+    if not _kernels_take(W):
+        return _eager_q8_pack_weight(W)
+    return binding.dora_q8_pack_weight(W.contiguous())
+
+
+@q8_pack_weight.register_fake
+def _q8_pack_weight_fake(W):
+    qs, es = binding.q8_weight_shapes(W.shape[0], W.shape[1])
+    return W.new_empty(qs, dtype=_F8), W.new_empty(es, dtype=torch.uint8)
+
+
+@torch.library.custom_op("dora_amd::q8_unpack", mutates_args=(), device_types="cuda")
+def q8_unpack(q: Tensor, e: Tensor, cols: int, dtype: torch.dtype) -> Tensor:
+    """The values that packed rows are held as, [T x cols] in dtype."""
+    if dtype not in binding.DTYPE_CODE:
+        return _eager_q8_unpack(q, e, cols, dtype)
+    return binding.dora_q8_unpack(q.contiguous(), e.contiguous(), q.shape[0], cols, dtype)
+
+
+@q8_unpack.register_fake
+def _q8_unpack_fake(q, e, cols, dtype):
+    return q.new_empty((q.shape[0], cols), dtype=dtype)
+
+
+@torch.library.custom_op("dora_amd::q8_unpack_weight", mutates_args=(), device_types="cuda")
+def q8_unpack_weight(q: Tensor, e: Tensor, rows: int, cols: int, dtype: torch.dtype) -> Tensor:
+    """The values of the first ``rows`` rows of a packed weight, [rows x cols] in dtype."""
+    if dtype not in binding.DTYPE_CODE:
+        return _eager_q8_unpack_weight(q, e, rows, cols, dtype)
+    return binding.dora_q8_unpack(q.contiguous(), e.contiguous(), rows, cols, dtype, weight=True)
+
+
+@q8_unpack_weight.register_fake
+def _q8_unpack_weight_fake(q, e, rows, cols, dtype):
+    return q.new_empty((rows, cols), dtype=dtype)
+
+
+@torch.library.custom_op("dora_amd::q8_linear", mutates_args=(), device_types="cuda")
+def q8_linear(xq: Tensor, xe: Tensor, wq: Tensor, we: Tensor, out_features: int, dtype: torch.dtype) -> Tensor:
+    """y [T x out] = x W^T from packed rows and a packed weight."""
+    if dtype not in binding.DTYPE_CODE:
+        return _eager_q8_linear(xq, xe, wq, we, out_features, dtype)
+    return binding.dora_q8_linear_fwd(xq.contiguous(), xe.contiguous(), wq.contiguous(), we.contiguous(),
+                                      out_features, xq.shape[1], dtype)
+
+
+@q8_linear.register_fake
+def _q8_linear_fake(xq, xe, wq, we, out_features, dtype):
+    return xq.new_empty((xq.shape[0], out_features), dtype=dtype)
+
+
+@torch.library.custom_op("dora_amd::q8_linear_backward", mutates_args=(), device_types="cuda")
+def q8_linear_backward(gq: Tensor, ge: Tensor, wq: Tensor, we: Tensor, in_features: int,
+                       dtype: torch.dtype) -> Tensor:
+    """dx [T x in] = g W from packed rows g [T x out] and the same packed weight."""
+    if dtype not in binding.DTYPE_CODE:
+        return _eager_q8_linear_backward(gq, ge, wq, we, in_features, dtype)
+    return binding.dora_q8_linear_bwd(gq.contiguous(), ge.contiguous(), wq.contiguous(), we.contiguous(),
+                                      gq.shape[1], in_features, dtype)
+
+
+@q8_linear_backward.register_fake
+def _q8_linear_backward_fake(gq, ge, wq, we, in_features, dtype):
+    return gq.new_empty((gq.shape[0], in_features), dtype=dtype)
+
+
+def _q8_compose_args(dy, bq, be, h, B, mag, norm, s):
+    return (dy.contiguous(), bq.contiguous(), be.contiguous(), h.contiguous(), B.contiguous(),
+            mag.contiguous().float(), norm.contiguous().float(), s)
+
+
+@torch.library.custom_op("dora_amd::q8_lora_compose_backward", mutates_args=(), device_types="cuda")
+def q8_lora_compose_backward(dy: Tensor, bq: Tensor, be: Tensor, h: Tensor, B: Tensor, mag: Tensor, norm: Tensor,
+                             s: float, add_base: bool, want_base: bool) -> tuple[Tensor, Tensor, Tensor]:
+    """``lora_compose_backward`` with the base from packed rows."""
+    if not _kernels_take(dy, h, B):
+        return _eager_q8_lora_compose_backward(dy, bq, be, h, B, mag, norm, s, add_base, want_base)
+    d_base, d_B, d_mag = binding.dora_q8_lora_compose_bwd(*_q8_compose_args(dy, bq, be, h, B, mag, norm, s), add_base,
+                                                          want_d_base=want_base)
+    return dy.new_empty((0,)) if d_base is None else d_base, d_B, d_mag
+
+
+@q8_lora_compose_backward.register_fake
+def _q8_lora_compose_backward_fake(dy, bq, be, h, B, mag, norm, s, add_base, want_base):
+    d_base = torch.empty_like(dy) if want_base else dy.new_empty((0,))
+    return d_base, torch.empty_like(B), mag.new_empty(mag.shape)
+
+
+@torch.library.custom_op("dora_amd::q8_lora_compose_backward_packed", mutates_args=(), device_types="cuda")
+def q8_lora_compose_backward_packed(dy: Tensor, bq: Tensor, be: Tensor, h: Tensor, B: Tensor, mag: Tensor,
+                                    norm: Tensor, s: float, add_base: bool) -> tuple[Tensor, Tensor, Tensor, Tensor]:
+    """The same with d_base packed straight from fp32: (q, e, d_B, d_mag)."""
+    if not _kernels_take(dy, h, B):
+        return _eager_q8_lora_compose_backward_packed(dy, bq, be, h, B, mag, norm, s, add_base)
+    (q, e), d_B, d_mag = binding.dora_q8_lora_compose_bwd(*_q8_compose_args(dy, bq, be, h, B, mag, norm, s), add_base,
+                                                          packed=True)
+    return q, e, d_B, d_mag
+
+
+@q8_lora_compose_backward_packed.register_fake
+def _q8_lora_compose_backward_packed_fake(dy, bq, be, h, B, mag, norm, s, add_base):
+    q, e = _q8_pack_fake(dy)
+    return q, e, torch.empty_like(B), mag.new_empty(mag.shape)
+
+
+@torch.library.custom_op("dora_amd::q8_grad_a", mutates_args=(), device_types="cuda")
+def q8_grad_a(dh: Tensor, xq: Tensor, xe: Tensor, in_features: int) -> Tensor:
+    """d_A [r x in] = d_h^T x from packed rows x."""
+    if not _kernels_take(dh):
+        return _eager_q8_grad_a(dh, xq, xe, in_features)
+    return binding.dora_q8_grad_a(dh.contiguous(), xq.contiguous(), xe.contiguous(), in_features)
+
+
+@q8_grad_a.register_fake
+def _q8_grad_a_fake(dh, xq, xe, in_features):
+    return dh.new_empty((dh.shape[1], in_features))
+
+
+# The norm of a packed weight: 16-bit values of a slab of rows at a time (32 MiB
+# at 8192 columns), so the weight is never whole in 16 bits.
+_Q8_SLAB = 2048
+
+
+def _slabs(wq, we, out, in_, dtype):
+    for i in range(0, out, _Q8_SLAB):
+        n = min(_Q8_SLAB, out - i)
+        rows = slice(i, _round_up(i + n, 128))
+        blocks = slice(i // 128, -(-(i + n) // 128))
+        yield slice(i, i + n), q8_unpack_weight(wq[rows], we[blocks], n, in_, dtype)
+
+
+@torch.library.custom_op("dora_amd::q8_weight_norm", mutates_args=())
+def q8_weight_norm(wq: Tensor, we: Tensor, A: Tensor, B: Tensor, base_sq: Tensor, s: float) -> Tensor:
+    """``weight_norm_cached`` of a packed weight."""
+    n = torch.empty(B.shape[0], dtype=torch.float32, device=B.device)
+    for rows, W in _slabs(wq, we, B.shape[0], A.shape[1], A.dtype):
+        n[rows] = weight_norm_cached(W, A, B[rows], base_sq[rows], s)
+    return n
+
+
+@q8_weight_norm.register_fake
+def _q8_weight_norm_fake(wq, we, A, B, base_sq, s):
+    return B.new_empty((B.shape[0],), dtype=torch.float32)
+
+
+def _q8_norm_setup(ctx, inputs, output):
+    wq, we, A, B, _, s = inputs
+    ctx.save_for_backward(wq, we, A, B, output)
+    ctx.s = s
+
+
+def _q8_norm_grad(ctx, d_norm):
+    wq, we, A, B, n = ctx.saved_tensors
+    d_A, d_B = torch.zeros(A.shape, dtype=torch.float32, device=A.device), torch.empty_like(B)
+    for rows, W in _slabs(wq, we, B.shape[0], A.shape[1], A.dtype):
+        a, d_B[rows] = weight_norm_backward(W, A, B[rows], n[rows], d_norm[rows], ctx.s)
+        d_A += a
+    need = ctx.needs_input_grad
+    return None, None, d_A.to(A.dtype) if need[2] else None, d_B if need[3] else None, None, None
+
+
+q8_weight_norm.register_autograd(_q8_norm_grad, setup_context=_q8_norm_setup)
+
+
+@torch.library.custom_op("dora_amd::q8_layer", mutates_args=())
+def q8_layer(x: Tensor, A: Tensor, B: Tensor, mag: Tensor, norm: Tensor, weight: Tensor, we: Optional[Tensor],
+             s: float) -> tuple[Tensor, Tensor, Tensor, Tensor, Tensor, Tensor]:
+    """The layer on x [T x in] with 8-bit checkpoints: (y, then what the backward
+    reads: x and base packed, and h).  ``weight`` is W0 [out x in] in 16 bits, or,
+    with its exponents ``we``, packed: then both products with W0 run on packed
+    operands, x's being the checkpoint itself."""
+    xq, xe = q8_pack(x)
+    base = F.linear(x, weight) if we is None else q8_linear(xq, xe, weight, we, B.shape[0], x.dtype)
+    h = F.linear(x, A)
+    y = lora_compose(base, h, B, mag, norm, s, True)
+    bq, be = q8_pack(base)
+    return y, xq, xe, bq, be, h
+
+
+@q8_layer.register_fake
+def _q8_layer_fake(x, A, B, mag, norm, weight, we, s):
+    y = x.new_empty((x.shape[0], B.shape[0]))
+    return (y, *_q8_pack_fake(x), *_q8_pack_fake(y), x.new_empty((x.shape[0], A.shape[0])))
+
+
+def _q8_layer_setup(ctx, inputs, output):
+    x, A, B, mag, norm, weight, we, s = inputs
+    ctx.save_for_backward(A, B, mag, norm, weight, we, *output[1:])
+    ctx.s = s
+
+
+def _q8_layer_grad(ctx, dy, *_):
+    A, B, mag, norm, weight, we, xq, xe, bq, be, h = ctx.saved_tensors
+    need, s, in_ = ctx.needs_input_grad, ctx.s, A.shape[1]
+    dx = None
+    if need[0] and we is not None:
+        dq, de, d_B, d_mag = q8_lora_compose_backward_packed(dy, bq, be, h, B, mag, norm, s, True)
+        dx = q8_linear_backward(dq, de, weight, we, in_, dy.dtype)
+    else:
+        d_base, d_B, d_mag = q8_lora_compose_backward(dy, bq, be, h, B, mag, norm, s, True, bool(need[0]))
+        if need[0]:
+            dx = d_base @ weight
+    d_A = None
+    if need[0] or need[1]:
+        gsB = ((mag / norm) * s)[:, None] * B.float()
+        d_h = dy @ gsB.to(dy.dtype)
+        if need[0]:
+            dx = torch.addmm(dx, d_h, A)
+        if need[1]:
+            d_A = q8_grad_a(d_h, xq, xe, in_)
+    d_norm = -(mag / norm) * d_mag if need[4] else None
+    return dx, d_A, d_B if need[2] else None, d_mag if need[3] else None, d_norm, None, None, None
+
+
+q8_layer.register_autograd(_q8_layer_grad, setup_context=_q8_layer_setup)
+
+
+q8_pack.register_kernel("cpu")(_eager_q8_pack)
+q8_pack_weight.register_kernel("cpu")(_eager_q8_pack_weight)
+q8_unpack.register_kernel("cpu")(_eager_q8_unpack)
+q8_unpack_weight.register_kernel("cpu")(_eager_q8_unpack_weight)
+q8_linear.register_kernel("cpu")(_eager_q8_linear)
+q8_linear_backward.register_kernel("cpu")(_eager_q8_linear_backward)
+q8_lora_compose_backward.register_kernel("cpu")(_eager_q8_lora_compose_backward)
+q8_lora_compose_backward_packed.register_kernel("cpu")(_eager_q8_lora_compose_backward_packed)
+q8_grad_a.register_kernel("cpu")(_eager_q8_grad_a)
+
+
 # -------------------------------------------------------------------------- layer
 
 
@@ -374,11 +726,19 @@ class DoRALinear(torch.nn.Module):
     ``detach_norm`` (default True) treats n as a constant in the backward; with
     False the gradients of A and B also carry the path through n, by the
     factored norm backward.
+
+    ``q8_checkpoint`` keeps x and base, all that the backward needs of size
+    T x in and T x out, in 8-bit blocks instead of 16 bits: half the activation
+    memory.  d_mag and d_A then come from those values, d_B and dx do not change.
+    ``q8_weight`` (which implies it) also holds W0 itself in 8-bit blocks (the
+    buffers ``weight_q``, ``weight_e``; ``weight`` is None) and runs both products
+    with W0 on packed operands.  n is the norm of the values W0 is held as, so the
+    layer still starts out with g = 1.
     """
 
     def __init__(self, in_features: int, out_features: int, r: int, alpha: float = 32.0,
                  weight: Tensor | None = None, dtype: torch.dtype = torch.bfloat16, device=None,
-                 detach_norm: bool = True):
+                 detach_norm: bool = True, q8_weight: bool = False, q8_checkpoint: bool = False):
         super().__init__()
         self.detach_norm = detach_norm
         if dtype not in (torch.bfloat16, torch.float16, torch.float32):
@@ -387,19 +747,37 @@ class DoRALinear(torch.nn.Module):
         self.s = float(np.float32(alpha / math.sqrt(r)))
         if weight is None:
             weight = torch.randn(out_features, in_features, device=device) / math.sqrt(in_features)
-        self.register_buffer("weight", weight.to(device=device, dtype=dtype).contiguous())
+        self.q8_weight, self.q8_checkpoint = q8_weight, q8_weight or q8_checkpoint
+        weight = weight.to(device=device, dtype=dtype).contiguous()
+        if q8_weight:
+            # bytes, so that a change of the module's dtype leaves them alone
+            q, e = q8_pack_weight(weight)
+            self.register_buffer("weight", None)
+            self.register_buffer("weight_q", q.view(torch.uint8))
+            self.register_buffer("weight_e", e)
+            weight = q8_unpack_weight(q, e, out_features, in_features, dtype)
+        else:
+            self.register_buffer("weight", weight)
         self.lora_A = torch.nn.Parameter(
             (torch.randn(r, in_features, device=device) / math.sqrt(in_features)).to(dtype))
         self.lora_B = torch.nn.Parameter(torch.zeros(out_features, r, device=device, dtype=dtype))
-        self.magnitude = torch.nn.Parameter(self.weight.float().norm(dim=1))
+        self.magnitude = torch.nn.Parameter(weight.float().norm(dim=1))
         self.register_buffer("weight_sqnorm", None)
-        if self.weight.is_cuda:
+        if weight.is_cuda:
             self.reset_magnitude()
+
+    def _packed_weight(self) -> tuple[Tensor, Tensor]:
+        return self.weight_q.view(_F8), self.weight_e
 
     @torch.no_grad()
     def refresh_weight_cache(self) -> None:
         """Recompute ||W0_i||^2 (after ``weight`` changed)."""
-        self.weight_sqnorm = row_sqnorm(self.weight)
+        if self.q8_weight:
+            wq, we = self._packed_weight()
+            slabs = _slabs(wq, we, self.out_features, self.in_features, self.lora_A.dtype)
+            self.weight_sqnorm = torch.cat([row_sqnorm(W) for _, W in slabs])
+        else:
+            self.weight_sqnorm = row_sqnorm(self.weight)
 
     @torch.no_grad()
     def reset_magnitude(self) -> None:
@@ -409,18 +787,29 @@ class DoRALinear(torch.nn.Module):
     def weight_norm(self) -> Tensor:
         """n = ||W0 + s*B*A|| per output row (base term from the cache); detached
         unless the layer was built with ``detach_norm=False``."""
-        if self.weight_sqnorm is None or self.weight_sqnorm.device != self.weight.device:
+        if self.weight_sqnorm is None or self.weight_sqnorm.device != self.lora_A.device:
             self.refresh_weight_cache()
         A, B = (self.lora_A.detach(), self.lora_B.detach()) if self.detach_norm else (self.lora_A, self.lora_B)
+        if self.q8_weight:
+            return q8_weight_norm(*self._packed_weight(), A, B, self.weight_sqnorm, self.s)
         return weight_norm_cached(self.weight, A, B, self.weight_sqnorm, self.s)
 
     def forward(self, x: Tensor) -> Tensor:
         lead = x.shape[:-1]
         x2 = x.reshape(-1, self.in_features)
-        base = F.linear(x2, self.weight)
+        weight, we = self._packed_weight() if self.q8_weight else (self.weight, None)
+        n = self.weight_norm()
+        trained = (x2, self.lora_A, self.lora_B, self.magnitude, n)
+        if self.q8_checkpoint and torch.is_grad_enabled() and any(t.requires_grad for t in trained):
+            y = q8_layer(x2, self.lora_A, self.lora_B, self.magnitude, n, weight, we, self.s)[0]
+            return y.reshape(*lead, self.out_features)
+        if self.q8_weight:  # inference: x is packed for the product alone
+            base = q8_linear(*q8_pack(x2), weight, we, self.out_features, x2.dtype)
+        else:
+            base = F.linear(x2, weight)
         h = F.linear(x2, self.lora_A)
         # lora = h B^T is formed inside the compose kernel on both tiers; on the
         # training tier autograd records it and its backward (lora_compose_backward)
         # never forms lora or d_lora either, so nothing T x out is saved for lora
-        y = lora_compose(base, h, self.lora_B, self.magnitude, self.weight_norm(), self.s, True)
+        y = lora_compose(base, h, self.lora_B, self.magnitude, n, self.s, True)
         return y.reshape(*lead, self.out_features)

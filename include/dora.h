@@ -318,6 +318,115 @@ DORA_API int dora_compose_bwd_noalloc(const void* dy, const void* base, const vo
                                       const float* norm, float s, int64_t T, int64_t out, int dtype, int add_base,
                                       void* d_lora, void* d_base, float* d_mag, hipStream_t stream);
 
+/*
+ * ---- The frozen side in 8 bits -------------------------------------------
+ *
+ * W0 is frozen and the backward needs x and base only as operands of sums over
+ * the tokens, so all three can be held in 8 bits: e4m3 values in blocks of 128
+ * with one power-of-two scale 2^e a block.  The entry points below pack and
+ * unpack such matrices, multiply with them, and run the compose's backward and
+ * the gradient of A from them.
+ *
+ * Packed rows (activations, gradients), from [rows x cols]:
+ *   q  bytes [rows x P], P = cols rounded up to 128, zeros behind cols;
+ *   e  bytes [rows x E], E = P / 128 rounded up to 4: byte 127 + e of each block
+ *      of 128 columns, 127 behind the last.
+ * Packed weight, from [out x in]: blocks of 128 x 128,
+ *   q  bytes [out rounded up to 128, x in rounded up to 128], zeros outside;
+ *   e  bytes [out / 128 rounded up, x E], as above.
+ * e is the smallest exponent >= -126 for which the block's largest finite
+ * magnitude is at most 448 * 2^e; the stored value is v * 2^-e rounded once, to
+ * nearest even.  A value that is not finite is stored as NaN and does not count
+ * for e.  A power of two, because the matrix instruction applies such scales
+ * itself, exactly, and because the packed bytes then do not depend on the order
+ * of any arithmetic.  q is 16-byte aligned and e 4-byte.  Only bytes written by
+ * these entry points (1 to 247) are exponents.
+ *
+ * Sizes: fewer than 2^31 rows and at most 2^23 - 128 columns (else
+ * DORA_UNSUPPORTED).  No output may overlap an input or another output.
+ */
+
+/*
+ * Pack x [rows x cols] (device, dtype) into q, e.  One read of x, one write of
+ * q.  Empty sizes are no-ops.
+ */
+DORA_API int dora_q8_pack(const void* x, int64_t rows, int64_t cols, int dtype, void* q, void* e, hipStream_t stream);
+
+/* Pack a weight [out x in] into blocks of 128 x 128 (once: the weight is frozen). */
+DORA_API int dora_q8_pack_weight(const void* W, int64_t out, int64_t in, int dtype, void* q, void* e,
+                                 hipStream_t stream);
+
+/*
+ * The values that packed rows (weight == 0) or the first `rows` rows of a
+ * packed weight (weight != 0) are held as: x [rows x cols] in dtype.  Exact but
+ * for values past the type's range: a block's top rounded up past the largest
+ * finite value is held at that value, and bf16 or fp16 subnormals round once.
+ */
+DORA_API int dora_q8_unpack(const void* q, const void* e, int64_t rows, int64_t cols, int weight, int dtype, void* x,
+                            hipStream_t stream);
+
+/* Bytes of device workspace dora_q8_linear_fwd needs (fp32 tiles of a split contraction, often 0). */
+DORA_API size_t dora_q8_linear_workspace_bytes(int64_t T, int64_t out, int64_t in);
+
+/*
+ * y [T x out] = x W0^T from packed rows x [T x in] and a packed weight
+ * [out x in]: y_tj = sum over the blocks of 2^(e_x + e_W) * (sum of the block's
+ * products), in fp32, rounded once to dtype.  The frozen layer's base product
+ * of the training and the inference tier; for few rows (T <= 64, as when single
+ * tokens are generated) the weight is streamed once and the rows share it.
+ * in == 0 gives y = 0.  A NaN in a row of x gives NaN in that row of y alone.
+ * ws: 16-byte aligned, at least dora_q8_linear_workspace_bytes bytes.
+ */
+DORA_API int dora_q8_linear_fwd(const void* xq, const void* xe, const void* wq, const void* we, int64_t T, int64_t out,
+                                int64_t in, int dtype, void* y, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* Bytes of device workspace dora_q8_linear_bwd needs. */
+DORA_API size_t dora_q8_linear_bwd_workspace_bytes(int64_t T, int64_t out, int64_t in);
+
+/*
+ * dx [T x in] = g W0 from packed rows g [T x out] and the same packed weight
+ * (its transpose is not stored: the kernel's reads transpose it).  W0 is frozen,
+ * so there is no gradient of the weight.  out == 0 gives dx = 0.
+ */
+DORA_API int dora_q8_linear_bwd(const void* gq, const void* ge, const void* wq, const void* we, int64_t T, int64_t out,
+                                int64_t in, int dtype, void* dx, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* Bytes of device workspace dora_q8_lora_compose_bwd needs (fp32 slices, column partials, padded copies). */
+DORA_API size_t dora_q8_lora_compose_bwd_workspace_bytes(int64_t T, int64_t out, int64_t r);
+
+/*
+ * dora_lora_compose_bwd with the base from packed rows [T x out] (the forward's
+ * base, kept in 8 bits until the backward): the same formulas for d_base, d_B
+ * and d_mag, base being the values the rows are held as.  d_base is written in
+ * dtype to d_base, or packed straight from fp32 to (dq, de) as dora_q8_pack
+ * would of the unrounded product, which is what dora_q8_linear_bwd takes; either
+ * or both may be NULL (dq and de together).
+ *
+ * dy [T x out], h [T x r], B, d_B [out x r], d_base: device, dtype, 16-byte
+ * aligned; any sizes (rows that are not multiples of 8 elements are copied into
+ * the workspace first).  r == 0 is lora = 0.  out == 0 is a no-op; T == 0 gives
+ * d_B = 0 and d_mag = 0 / norm.  r <= 2^20 and a token slice below 2 GiB, else
+ * DORA_UNSUPPORTED.
+ */
+DORA_API int dora_q8_lora_compose_bwd(const void* dy, const void* bq, const void* be, const void* h, const void* B,
+                                      const float* mag, const float* norm, float s, int64_t T, int64_t out, int64_t r,
+                                      int dtype, int add_base, void* d_base, void* dq, void* de, void* d_B,
+                                      float* d_mag, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* Bytes of device workspace dora_q8_grad_a needs (fp32 slices of x^T d_h, a padded copy of d_h). */
+DORA_API size_t dora_q8_grad_a_workspace_bytes(int64_t T, int64_t in, int64_t r);
+
+/*
+ * d_A [r x in] = d_h^T x, the gradient of the adapter's first projection h = x
+ * A^T, from x kept in packed rows [T x in] since the forward.  x enters the
+ * products as dora_q8_unpack gives it in dtype, d_h [T x r] (device, dtype,
+ * 16-byte aligned) as it is; fp32 sums, token slices added in a fixed order,
+ * rounded once.  in == 0 or r == 0 is a no-op; T == 0 gives d_A = 0.  r <= 2^20
+ * and a token slice below 2 GiB, else DORA_UNSUPPORTED.
+ */
+DORA_API int dora_q8_grad_a(const void* dh, const void* xq, const void* xe, int64_t T, int64_t in, int64_t r, int dtype,
+                            void* d_A, void* ws, size_t ws_bytes, hipStream_t stream);
+
 /* Message of the calling thread's last non-OK status ("" if none).  Valid until the next call. */
 DORA_API const char* dora_last_error(void);
 
