@@ -9,10 +9,11 @@ using namespace dora::abi;
 namespace {
 
 // Sizes up to here keep every product of two of them, and every byte count,
-// inside 63 bits; a packed row stays below 2^23 bytes, so that 256 rows of it
-// lie inside one buffer resource.
+// inside 63 bits; a packed row stays below 2^22 bytes, so that 256 rows of it (or
+// of 16-bit outputs) lie inside one buffer resource, and a weight's blocks are
+// numbered in 30 bits.
 constexpr int64_t kMaxRows = int64_t(1) << 31;
-constexpr int64_t kMaxCols = (int64_t(1) << 23) - 128;
+constexpr int64_t kMaxCols = (int64_t(1) << 22) - 128;
 constexpr int64_t kMaxRank = int64_t(1) << 20;
 
 int check_sizes(const char* fn, int dtype, int64_t rows, int64_t a, int64_t b) {
@@ -21,7 +22,7 @@ int check_sizes(const char* fn, int dtype, int64_t rows, int64_t a, int64_t b) {
     return fail(DORA_INVALID_ARG, "%s: negative size (%lld, %lld, %lld)", fn, (long long)rows, (long long)a,
                 (long long)b);
   if (rows >= kMaxRows || a > kMaxCols || b > kMaxCols)
-    return fail(DORA_UNSUPPORTED, "%s: sizes (%lld, %lld, %lld) beyond 2^31 rows or 2^23 columns", fn,
+    return fail(DORA_UNSUPPORTED, "%s: sizes (%lld, %lld, %lld) beyond 2^31 rows or 2^22 columns", fn,
                 (long long)rows, (long long)a, (long long)b);
   return DORA_OK;
 }
@@ -51,7 +52,7 @@ int pack_call(const char* fn, const void* x, int64_t rows, int64_t cols, int dty
               hipStream_t stream) {
   if (int st = check_sizes(fn, dtype, rows, cols, 0)) return st;
   if (tiles && rows > kMaxCols)
-    return fail(DORA_UNSUPPORTED, "%s: out=%lld beyond 2^23", fn, (long long)rows);
+    return fail(DORA_UNSUPPORTED, "%s: out=%lld beyond 2^22", fn, (long long)rows);
   if (rows == 0 || cols == 0) return ok();
   if (!x) return fail(DORA_INVALID_ARG, "%s: the input is NULL", fn);
   if (int st = packed_ptrs(fn, "the packed output", q, e)) return st;

@@ -21,17 +21,22 @@
 // the price taken for the instruction's rate, twice the 16-bit one's.
 //
 // Kernels:
-//   q8_gemm_tile    a workgroup owns a BM x BN tile of the output and a range
-//                   of the contraction's stages of 128.  Stages go global ->
-//                   LDS by DMA into a ring; fragments are read one half stage
-//                   ahead of the matrix instructions that use them, one read
-//                   between two instructions, so the matrix pipe is fed without
-//                   a pause by one wave per SIMD.  The backward's weight panel
-//                   keeps its rows (the contraction axis) and is transposed by
-//                   the reads (ds_read_b64_tr_b8);
+//   q8_gemm_tile    one workgroup a CU takes tiles of the output, or of the last
+//                   tiles ranges of the contraction's stages of 128.  Stages go
+//                   global -> LDS by DMA into a ring; fragments are read one
+//                   half stage ahead of the matrix instructions that use them,
+//                   a few reads behind each instruction, so the matrix pipe is
+//                   fed without a pause by one wave per SIMD.  The backward's
+//                   weight panel keeps its rows (the contraction axis) and is
+//                   transposed by the reads (ds_read_b64_tr_b8);
 //   q8_gemm_join    adds the fp32 tiles of a split contraction in order;
 //   q8_gemm_few     few rows: the weight is streamed once, straight from global
 //                   memory into the fragments of mfma 16x16x128.
+//
+// What bounds the tiles, at 8192^2 x 8192 with normal values: the card's power.
+// The 415 us (2650 TFLOP/s) run at 1.65 to 1.8 GHz with the matrix pipes busy 71%
+// of the cycles; the same launch on zeros takes 319 us, at 2.3 GHz.  A stage of the
+// 256 x 256 tile takes 2450 cycles, 2048 of them matrix instructions.
 #include <algorithm>
 #include <type_traits>
 
@@ -76,13 +81,16 @@ __device__ inline void unrolled(F&& f) {
 }
 
 // Tile geometry: WM x WN waves, each TMW x TNW matrix tiles of 32 x 32 with
-// their accumulators in registers; a ring of NS stages of 128 contraction
-// steps.
+// their accumulators in registers; a ring of NS slots of one stage, 128
+// contraction steps of both panels.  (Half stages in a ring of twice the slots,
+// which load further ahead, fetch half a cache line a row: 8192^2 x 8192 took
+// 2880 cycles a stage with them, bound by the L2's requests, 2450 with whole
+// lines.)
 //
-// LDS images.  X and the forward's W panel: rows of 128 bytes, logical 16-byte
-// chunk c of row p in slot c ^ ((p/2) % 8): 16 consecutive rows at one chunk
-// then fall in 16 distinct bank groups.  The backward's W panel: 128 rows of BN
-// bytes; a transposing read touches 8 consecutive rows and two chunks c, c + 1
+// LDS images of a slot.  X and the forward's W panel: rows of 128 bytes, logical
+// 16-byte chunk c of row p in place c ^ ((p/2) % 8): 16 consecutive rows at one
+// chunk then fall in 16 distinct bank groups.  The backward's W panel: 128 rows of
+// BN bytes; a transposing read touches 8 consecutive rows and two chunks c, c + 1
 // (c even), so the chunk is exchanged by the row, leaving its lowest bit alone,
 // which spreads the 16 (row, chunk) pairs over the 16 bank groups.
 template <int WM_, int WN_, int TMW_, int TNW_, int NS_, bool TRANS_>
@@ -91,18 +99,23 @@ struct Q8Tile {
   static constexpr bool TRANS = TRANS_;
   static constexpr int NW = WM * WN, NT = 64 * NW;
   static constexpr int BM = 32 * TMW * WM, BN = 32 * TNW * WN, BK = 128;
-  static constexpr int X_BYTES = BM * BK, W_BYTES = BN * BK, STAGE_BYTES = X_BYTES + W_BYTES;
+  static constexpr int X_BYTES = BM * BK, W_BYTES = BN * BK, SLOT_BYTES = X_BYTES + W_BYTES;
   static constexpr int XQ = X_BYTES / 1024 / NW, WQ = W_BYTES / 1024 / NW, L = XQ + WQ;  // DMA instructions a wave
-  static constexpr int E_BYTES = BM * 4;  // exponents of the X rows, four stages
-  static constexpr int LDS_BYTES = NS * STAGE_BYTES + 2 * E_BYTES;
+  static constexpr int E_BYTES = BM * 4, NE = 8;  // exponents of the X rows, four stages; slots of them
+  static constexpr int LDS_BYTES = NS * SLOT_BYTES + NE * E_BYTES;
   static constexpr int CPR = BN / 16;  // chunks per row of the backward's W panel
+  static constexpr int NST = 2 * TMW * TNW;  // 16-byte stores of a wave's tile
+  static constexpr int WAIT = (NS - 2) * L;  // DMA instructions younger than the slot waited for
   static_assert(X_BYTES % (1024 * NW) == 0 && W_BYTES % (1024 * NW) == 0, "whole DMA instructions per wave");
-  static_assert(NW % 2 == 0 && BM % 64 == 0, "panel swizzle and exponent DMA");
+  static_assert(NW % 2 == 0 && BM % 64 == 0 && BM / 64 <= NW, "panel swizzle and exponent DMA");
   static_assert(BN == 128 || BN == 256, "the backward's panel rows");
-  static_assert((32 * TNW) % 32 == 0 && 128 % (32 * TNW) == 0, "a wave's columns lie in one weight block");
-  static_assert(NS >= 2 && NS <= 4, "an exponent slot is not overwritten before its four stages are done");
+  static_assert(128 % (32 * TNW) == 0, "a wave's columns lie in one weight block");
+  static_assert(NS >= 2 && NS < NE, "an exponent slot outlives the stages in flight");
+  static_assert(WAIT + NST < 64, "vmcnt range");
   static_assert(LDS_BYTES <= 160 * 1024, "LDS");
 };
+
+constexpr int kCUs = 256;
 
 struct GemmArgs {
   const uint8_t *xq, *xe, *wq, *we;
@@ -110,20 +123,70 @@ struct GemmArgs {
   int64_t xp, wp;    // bytes of a row of xq and wq
   int64_t xep, wep;  // bytes of a row of exponents
   int64_t wrows;     // rows of wq (whole tiles)
-  int S;             // stages of the contraction
-  int nRB, nTiles, nSplit;
-  uint32_t group;
+  int S;             // stages (of 128) of the contraction
+  // units of work: tiles [0, whole) over the whole contraction, then tiles
+  // [whole, nRB * nTiles) in nSplit ranges of its stages each
+  int nRB, nTiles, whole, nSplit;
+  uint32_t group;  // column tiles of a group of the tile order
   void* y;
   int vec;  // 16-byte stores of y
   float* part;
 };
 
+// Tile order: groups of `group` column tiles, row blocks within a group, on
+// XCD-contiguous ranges: an XCD's concurrent tiles form a block of rows and
+// columns whose panels its L2 holds for all of them.
+__device__ inline void tile_of(uint32_t v, const GemmArgs& a, int& rb, int& nt) {
+  const uint32_t nRB = static_cast<uint32_t>(a.nRB), nTl = static_cast<uint32_t>(a.nTiles), G = a.group;
+  const uint32_t grp = v / (G * nRB);
+  const uint32_t gn = min(G, nTl - grp * G);
+  const uint32_t loc = v - grp * G * nRB;
+  rb = static_cast<int>(loc / gn);
+  nt = static_cast<int>(grp * G + loc % gn);
+}
+
+// The k-th unit of work of this workgroup (of the 8 XCDs x gridDim.x/8): false
+// past its last.  An XCD takes contiguous ranges of the whole tiles and of the
+// split ones.
+struct Unit {
+  int rb, nt, st0, st1, split, tail;  // tail: index among the split tiles, -1 for a whole tile
+};
+__device__ inline bool unit_of(int k, const GemmArgs& a, Unit& u) {
+  // (opaque, so that nothing of this moves out of the rare branches it stands in)
+  asm volatile("" : "+s"(k));
+  const int x = blockIdx.x & 7, i = blockIdx.x >> 3, per = gridDim.x >> 3;
+  const int wpx = (a.whole + 7) >> 3;  // whole tiles of an XCD
+  const int w0 = min(x * wpx, a.whole), w1 = min(w0 + wpx, a.whole);
+  const int rounds = (w1 - w0 + per - 1 - i) / per;  // whole tiles of this workgroup
+  int v;
+  if (k < rounds) {
+    v = w0 + k * per + i;
+    u.st0 = 0;
+    u.st1 = a.S;
+    u.split = 0;
+    u.tail = -1;
+  } else {
+    const int ntail = a.nRB * a.nTiles - a.whole, nun = ntail * a.nSplit, upx = (nun + 7) >> 3;
+    const int j = (k - rounds) * per + i, n = x * upx + j;
+    if (j >= upx || n >= nun) return false;
+    u.split = n / ntail;
+    u.tail = n - u.split * ntail;
+    v = a.whole + u.tail;
+    u.st0 = a.S * u.split / a.nSplit;  // S <= 2^16
+    u.st1 = a.S * (u.split + 1) / a.nSplit;
+  }
+  tile_of(static_cast<uint32_t>(v), a, u.rb, u.nt);
+  return true;
+}
+
 // Rows of y from a wave's accumulators: register q of lane l is output column
 // 8*(q/4) + 4*(l/32) + q%4 of its tile, row l%32.  Packed in pairs, two groups
 // of four columns change places between the lane halves, and each lane then
-// holds 8 consecutive columns.
+// holds 8 consecutive columns.  Stores past the matrix are dropped by the buffer
+// resource, so that a tile is always the same number of stores.
 template <int DT>
-__device__ inline void store_tile(const GemmArgs& a, int64_t t, int64_t c0, const f32x16& acc, int half) {
+__device__ inline void store_tile(__amdgpu_buffer_rsrc_t ry, int vec, uint32_t row, int64_t N, int64_t c0,
+                                  const f32x16& acc, int half) {
   using T16 = typename Dt<DT>::T;
   typedef T16 t2 __attribute__((ext_vector_type(2)));
   uint32_t p[8];
@@ -139,132 +202,147 @@ __device__ inline void store_tile(const GemmArgs& a, int64_t t, int64_t c0, cons
       p[4 * g + 2 + d] = s[1];
     }
   }
-  if (t >= a.T) return;
-  T16* y = static_cast<T16*>(a.y) + t * a.N;
 #pragma unroll
   for (int g = 0; g < 2; ++g) {
-    const int64_t c = c0 + 16 * g + 8 * half;
+    const uint32_t c = static_cast<uint32_t>(c0) + 16 * g + 8 * half, n = static_cast<uint32_t>(N);
+    const uint32_t at = (row * n + c) * 2;
     const u32x4 w = u32x4{p[4 * g], p[4 * g + 1], p[4 * g + 2], p[4 * g + 3]};
-    if (a.vec) {
-      if (c < a.N) *reinterpret_cast<u32x4*>(y + c) = w;
+    if (vec) {
+      __builtin_amdgcn_raw_buffer_store_b128(w, ry, c < n ? at : kOob, 0, 0);
     } else {
-      const auto v = __builtin_bit_cast(typename Dt<DT>::V8, w);
 #pragma unroll
       for (int i = 0; i < 8; ++i)
-        if (c + i < a.N) y[c + i] = v[i];
+        __builtin_amdgcn_raw_buffer_store_b16(static_cast<uint16_t>(w[i >> 1] >> (16 * (i & 1))), ry,
+                                              c + i < n ? at + 2 * i : kOob, 0, 0);
     }
   }
 }
 
-// Tile order: groups of `group` column tiles, row blocks within a group, on
-// XCD-contiguous ranges: an XCD's concurrent tiles form a block of rows and
-// columns whose panels its L2 holds for all of them.
-__device__ inline void tile_of(uint32_t v, const GemmArgs& a, int& rb, int& nt) {
-  const uint32_t nRB = static_cast<uint32_t>(a.nRB), nTl = static_cast<uint32_t>(a.nTiles), G = a.group;
-  const uint32_t grp = v / (G * nRB);
-  const uint32_t gn = min(G, nTl - grp * G);
-  const uint32_t loc = v - grp * G * nRB;
-  rb = static_cast<int>(loc / gn);
-  nt = static_cast<int>(grp * G + loc % gn);
+__device__ inline __amdgpu_buffer_rsrc_t buffer_of(const void* p, int64_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), static_cast<short>(0), static_cast<int>(bytes),
+                                           kBufferWord3);
+}
+// Rows [m, m + most) of y, as far as they exist.
+__device__ inline __amdgpu_buffer_rsrc_t rows_of_y(const GemmArgs& a, int64_t m, int most) {
+  const int64_t rows = min(max(a.T - m, int64_t(0)), static_cast<int64_t>(most));
+  return buffer_of(static_cast<char*>(a.y) + (rows > 0 ? m * a.N * 2 : 0), rows * a.N * 2);
 }
 
+// One workgroup a CU, each taking its units in turn.  The ring runs on from one
+// unit to the next: while a unit's last slots are worked on, the next one's
+// first ones load, and its stores are under way while the next one's products
+// run.  Splitting the tiles that do not fill a round of all CUs takes 27648 x 5120
+// with 10240 rows backward (800 tiles, 3.1 rounds) from 1340 us to 1160 us.
 template <int DT, class TL>
 __global__ __launch_bounds__(TL::NT, 1) void q8_gemm_tile(GemmArgs a) {
   __shared__ __attribute__((aligned(1024))) char smem[TL::LDS_BYTES];
-  const uint32_t v = static_cast<uint32_t>(xcd_logical_index());
-  const uint32_t tiles = static_cast<uint32_t>(a.nRB) * static_cast<uint32_t>(a.nTiles);
-  if (v >= tiles * static_cast<uint32_t>(a.nSplit)) return;
-  const int sp = static_cast<int>(v / tiles);
-  int rb, nt;
-  tile_of(v - static_cast<uint32_t>(sp) * tiles, a, rb, nt);
-  const int64_t m0 = static_cast<int64_t>(rb) * TL::BM, n0 = static_cast<int64_t>(nt) * TL::BN;
-  const int st0 = static_cast<int>(static_cast<int64_t>(a.S) * sp / a.nSplit);
-  const int st1 = static_cast<int>(static_cast<int64_t>(a.S) * (sp + 1) / a.nSplit);
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / TL::WN, wn = wave % TL::WN;
   const int frow = lane & 31, half = lane >> 5;
   const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_char_t*)smem));
 
-  // Buffer resources over the tile's rows; rows past the operand read zero.
-  auto rsrc = [](const uint8_t* p, int64_t bytes) {
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p), static_cast<short>(0), static_cast<int>(bytes),
-                                             kBufferWord3);
-  };
-  const int64_t xrows = min(a.T - m0, static_cast<int64_t>(TL::BM));
-  const __amdgpu_buffer_rsrc_t rx = rsrc(a.xq + m0 * a.xp, xrows * a.xp);
-  const __amdgpu_buffer_rsrc_t re = rsrc(a.xe + m0 * a.xep, xrows * a.xep);
-  const int64_t wr = TL::TRANS ? 0 : min(a.wrows - n0, static_cast<int64_t>(TL::BN));
-  const __amdgpu_buffer_rsrc_t rw = TL::TRANS ? rx : rsrc(a.wq + n0 * a.wp, wr * a.wp);
+  Unit cu;
+  if (!unit_of(0, a, cu)) return;
 
-  const __amdgpu_buffer_rsrc_t none = rsrc(a.xq, 0);
-
-  // Per-lane DMA offsets.  Instruction q of wave w moves 1 KiB block q*NW + w of
-  // its panel, lane l writing bytes 16l .. 16l + 15.
-  const int xr = wave * 8 + (lane >> 3);
+  // ---- the issuing side: its unit, and that unit's buffer resources (rows past
+  // the operand read zero; past the last unit everything does, so that every half
+  // stage issues the same instructions and the waits count them exactly)
+  const int xr = wave * 8 + (lane >> 3);  // X rows (and the forward's W rows) of DMA instruction 0
   const uint32_t kc = static_cast<uint32_t>(((lane & 7) ^ ((xr >> 1) & 7)) * 16);
   const uint32_t xo = static_cast<uint32_t>(xr * a.xp) + kc;
   const uint32_t xstep = static_cast<uint32_t>(TL::NW * 8 * a.xp);
-  uint32_t wo, wstep;
-  if constexpr (TL::TRANS) {
-    constexpr int RPI = 64 / TL::CPR;  // rows per instruction
-    const int r = wave * RPI + lane / TL::CPR, sl = lane % TL::CPR;
-    // (row + q*NW*RPI has the same swizzle: NW*RPI is a multiple of 8)
-    static_assert((TL::NW * RPI) % 8 == 0, "swizzle period");
-    const int c = sl ^ (TL::CPR == 16 ? 2 * (r & 7) : 2 * ((r >> 1) & 3));
-    const int64_t col = n0 + 16 * c;
-    wo = col < a.wp ? static_cast<uint32_t>(r * a.wp + col) : kOob;
-    wstep = col < a.wp ? static_cast<uint32_t>(TL::NW * RPI * a.wp) : 0u;
-  } else {
-    wo = static_cast<uint32_t>(xr * a.wp) + kc;
-    wstep = static_cast<uint32_t>(TL::NW * 8 * a.wp);
-  }
-  // one DMA instruction of a stage (k = 0 .. L - 1, compile time)
-  auto issue1 = [&](int st, int slot, auto kk) {
+  const uint32_t eo = static_cast<uint32_t>((wave * 64 + lane) * a.xep);
+  constexpr int RPI = TL::TRANS ? 64 / TL::CPR : 8;  // W rows per DMA instruction
+  static_assert((TL::NW * RPI) % 8 == 0, "swizzle period");
+  const int tr = wave * RPI + lane / TL::CPR;  // backward: W row of instruction 0, and its logical chunk
+  const int tc = (lane % TL::CPR) ^ (TL::CPR == 16 ? 2 * (tr & 7) : 2 * ((tr >> 1) & 3));
+  uint32_t wo = static_cast<uint32_t>(xr * a.wp) + kc;
+  uint32_t wstep = static_cast<uint32_t>(TL::NW * RPI * a.wp);
+
+  int ik = 0, ist = 0, iend = 0, ig = 0;
+  bool live = true;
+  __amdgpu_buffer_rsrc_t rx, re, rw;
+  const uint8_t* iw = a.wq;
+  int64_t in0 = 0;
+  // backward: the stage's 128 rows from column n0 on; the last byte that exists
+  // is the last row's last, n0 bytes before the end of 128 rows from here
+  auto issue_rows = [&]() {
+    if constexpr (TL::TRANS)
+      rw = buffer_of(iw + (live ? static_cast<int64_t>(ist) * TL::BK * a.wp : 0), live ? TL::BK * a.wp - in0 : 0);
+  };
+  auto issue_unit = [&](Unit u) {
+    ist = u.st0;
+    iend = u.st1;
+    const int64_t m0 = static_cast<int64_t>(u.rb) * TL::BM, n0 = static_cast<int64_t>(u.nt) * TL::BN;
+    const int64_t xrows = live ? min(a.T - m0, static_cast<int64_t>(TL::BM)) : 0;
+    rx = buffer_of(a.xq + m0 * a.xp, xrows * a.xp);
+    re = buffer_of(a.xe + m0 * a.xep, xrows * a.xep);
+    if constexpr (TL::TRANS) {
+      iw = a.wq + n0;
+      in0 = n0;
+      const bool ok = n0 + 16 * tc < a.wp;
+      wo = ok ? static_cast<uint32_t>(tr * a.wp + 16 * tc) : kOob;
+      wstep = ok ? static_cast<uint32_t>(TL::NW * RPI * a.wp) : 0u;
+    } else {
+      rw = buffer_of(a.wq + n0 * a.wp, live ? min(a.wrows - n0, static_cast<int64_t>(TL::BN)) * a.wp : 0);
+    }
+  };
+  // DMA instruction k of the issuing side's stage (k compile time)
+  auto issue1 = [&](int slot, auto kk) {
     constexpr int k = decltype(kk)::value;
-    char* so = smem + slot * TL::STAGE_BYTES;
-    const bool in = st < st1;
+    char* so = smem + slot * TL::SLOT_BYTES;
+    const uint32_t at = static_cast<uint32_t>(ist) * TL::BK;
     if constexpr (k < TL::XQ) {
-      dma16(in ? rx : none, so + (k * TL::NW + wave) * 1024, xo + k * xstep + static_cast<uint32_t>(st) * TL::BK);
+      dma16(rx, so + (k * TL::NW + wave) * 1024, xo + k * xstep + at);
     } else {
       constexpr int q = k - TL::XQ;
       char* d = so + TL::X_BYTES + (q * TL::NW + wave) * 1024;
-      if constexpr (TL::TRANS) {
-        const __amdgpu_buffer_rsrc_t rs =
-            rsrc(a.wq + static_cast<int64_t>(st) * TL::BK * a.wp, in ? TL::BK * a.wp : 0);
-        dma16(rs, d, wo + q * wstep);
-      } else {
-        dma16(in ? rw : none, d, wo + q * wstep + static_cast<uint32_t>(st) * TL::BK);
-      }
+      if constexpr (TL::TRANS)
+        dma16(rw, d, wo + q * wstep);
+      else
+        dma16(rw, d, wo + q * wstep + at);
     }
   };
-  // Exponents of the X rows, one dword (four stages) a row, before the first of
-  // the stages it serves; stage groups are counted from stage 0 of the operand.
-  auto issue_exp = [&](int st) {
+  // exponents of the X rows, a dword (four stages) a row, with the first stage
+  // of the unit and of every four
+  auto issue_exp = [&](bool first) {
+    if (!first && (ist & 3) != 0) return;
+    ig = (ig + 1) & (TL::NE - 1);
     if (TL::BM / 64 > wave) {
-      char* d = smem + TL::NS * TL::STAGE_BYTES + ((st >> 2) & 1) * TL::E_BYTES + wave * 256;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(st < st1 ? re : none, (lds_void_t*)d, 4,
-                                               static_cast<uint32_t>((wave * 64 + lane) * a.xep) + (st & ~3), 0, 0, 0);
+      char* d = smem + TL::NS * TL::SLOT_BYTES + ig * TL::E_BYTES + wave * 256;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(re, (lds_void_t*)d, 4, eo + (ist & ~3), 0, 0, 0);
     }
   };
-  static_assert(TL::BM / 64 <= TL::NW, "one exponent DMA instruction a wave");
-  auto issue_all = [&](int st, int slot) {
-    if (st == st0 || (st & 3) == 0) issue_exp(st);
-    unrolled<TL::L>([&](auto kk) { issue1(st, slot, kk); });
+  bool ifirst = true;
+  auto issue_next = [&]() {  // to the next stage, or the next unit's first
+    ifirst = false;
+    if (++ist == iend) {
+      Unit u;
+      live = unit_of(++ik, a, u);
+      if (!live) u = Unit{0, 0, 0, 1 << 30, 0, -1};
+      issue_unit(u);
+      ifirst = true;
+    }
+    issue_rows();
   };
+  using H0 = std::integral_constant<int, 0>;
+  using H1 = std::integral_constant<int, 1>;
 
-  // Fragment read addresses within a stage slot: half stage s, lane half h takes
+  // ---- fragment read addresses within a slot: half stage s, lane half h takes
   // contraction steps 64s + 32h .. + 31.  (The instruction's own order of the
-  // contraction steps within a lane does not matter: both operands use the same.)
+  // steps within a lane does not matter: both operands use the same.)
   const int sw = (frow >> 1) & 7;
-  uint32_t co[2][2];
+  uint32_t xa[2][2], wa[2][2];
 #pragma unroll
   for (int s = 0; s < 2; ++s)
 #pragma unroll
-    for (int c = 0; c < 2; ++c) co[s][c] = static_cast<uint32_t>(((4 * s + 2 * half + c) ^ sw) * 16);
-  const uint32_t xrow = lds0 + static_cast<uint32_t>((wm * TL::TMW * 32 + frow) * TL::BK);
-  const uint32_t wrow = lds0 + static_cast<uint32_t>(TL::X_BYTES + (wn * TL::TNW * 32 + frow) * TL::BK);
-  const uint32_t erow = lds0 + static_cast<uint32_t>(TL::NS * TL::STAGE_BYTES + (wm * TL::TMW * 32 + frow) * 4);
+    for (int c = 0; c < 2; ++c) {
+      const uint32_t co = static_cast<uint32_t>(((4 * s + 2 * half + c) ^ sw) * 16);
+      xa[s][c] = lds0 + static_cast<uint32_t>((wm * TL::TMW * 32 + frow) * TL::BK) + co;
+      wa[s][c] = lds0 + static_cast<uint32_t>(TL::X_BYTES + (wn * TL::TNW * 32 + frow) * TL::BK) + co;
+    }
+  const uint32_t erow = lds0 + static_cast<uint32_t>(TL::NS * TL::SLOT_BYTES + (wm * TL::TMW * 32 + frow) * 4);
   uint32_t wtr[TL::TNW];
   if constexpr (TL::TRANS) {
     const int L16 = lane & 15, g = lane >> 4;
@@ -278,11 +356,6 @@ __global__ __launch_bounds__(TL::NT, 1) void q8_gemm_tile(GemmArgs a) {
   }
 
   f32x16 acc[TL::TMW][TL::TNW];
-#pragma unroll
-  for (int i = 0; i < TL::TMW; ++i)
-#pragma unroll
-    for (int j = 0; j < TL::TNW; ++j) acc[i][j] = f32x16{};
-
   // A half stage's fragments: X rows as two 16-byte reads, W as two (forward)
   // or four transposing reads.
   struct Frag {
@@ -291,15 +364,14 @@ __global__ __launch_bounds__(TL::NT, 1) void q8_gemm_tile(GemmArgs a) {
     u32x2 t[TL::TRANS ? TL::TNW : 1][4];
   };
   constexpr int NR = 2 * TL::TMW + (TL::TRANS ? 4 : 2) * TL::TNW;  // reads of a half stage
-  // read n of half stage s (n, s compile time)
   auto read1 = [&](Frag& f, uint32_t so, auto ss, auto nn) {
     constexpr int s = decltype(ss)::value, n = decltype(nn)::value;
     if constexpr (n < 2 * TL::TMW) {
       constexpr int i = n / 2, c = n % 2;
-      f.x[i][c] = lds_read16_at<i * 32 * TL::BK>(xrow + co[s][c] + so);
+      f.x[i][c] = lds_read16_at<i * 32 * TL::BK>(xa[s][c] + so);
     } else if constexpr (!TL::TRANS) {
       constexpr int j = (n - 2 * TL::TMW) / 2, c = n % 2;
-      f.w[j][c] = lds_read16_at<j * 32 * TL::BK>(wrow + co[s][c] + so);
+      f.w[j][c] = lds_read16_at<j * 32 * TL::BK>(wa[s][c] + so);
     } else {
       constexpr int j = (n - 2 * TL::TMW) / 4, p = (n - 2 * TL::TMW) % 4;
       f.t[j][p] = lds_read_tr8_at<(64 * s + 8 * p) * TL::BN>(wtr[j] + so);
@@ -342,32 +414,36 @@ __global__ __launch_bounds__(TL::NT, 1) void q8_gemm_tile(GemmArgs a) {
                                                                 static_cast<int>(sx[i]));
   };
   constexpr int NM = TL::TMW * TL::TNW;  // matrix instructions of a half stage
-  // The weight block's exponent byte of a stage (a scalar load: the address is
-  // the wave's own and nothing writes there while the kernel runs).
+
+  // ---- exponents of the computing side.  The weight block's byte by a scalar
+  // load: the address is the wave's own and nothing writes there while the kernel
+  // runs.  (Columns past the weight have zero panels: any exponent.)
   typedef const uint32_t __attribute__((address_space(4))) const_u32;
-  const int64_t wblk = (n0 + wn * TL::TNW * 32) / kQ8Block;
-  const int64_t nblk = (TL::TRANS ? a.wp : a.wrows) / kQ8Block;
-  const int64_t wb = min(wblk, nblk - 1);  // columns past the weight have zero panels: any exponent
-  auto wexp_idx = [&](int st) { return TL::TRANS ? static_cast<int64_t>(st) * a.wep + wb : wb * a.wep + st; };
-  auto wexp_load = [&](int st) -> uint32_t {
-    return ((const_u32*)(reinterpret_cast<uintptr_t>(a.we)))[wexp_idx(st) >> 2];
+  const int nblk = static_cast<int>((TL::TRANS ? a.wp : a.wrows) / kQ8Block);
+  const int wep = static_cast<int>(a.wep);  // a weight has below 2^30 blocks
+  auto wexp_idx = [&](const Unit& u) -> int {
+    const int wb = min((u.nt * TL::BN + wn * TL::TNW * 32) / static_cast<int>(kQ8Block), nblk - 1);
+    return TL::TRANS ? u.st0 * wep + wb : wb * wep + u.st0;
   };
-  // The stage's exponent dwords of this lane's rows.
+  const int wexp_step = TL::TRANS ? wep : 1;
+  auto wexp_load = [&](int idx) -> uint32_t {
+    return ((const_u32*)(reinterpret_cast<uintptr_t>(a.we)))[idx >> 2];
+  };
   uint32_t ex[TL::TMW];
-  auto read_exp = [&](int st) {
-    const uint32_t ea = erow + static_cast<uint32_t>(((st >> 2) & 1) * TL::E_BYTES);
+  int cg = 0;  // exponent slot of the computing side
+  auto read_exp = [&]() {
+    const uint32_t ea = erow + static_cast<uint32_t>(cg * TL::E_BYTES);
     unrolled<TL::TMW>([&](auto ii) { ex[decltype(ii)::value] = lds_read4_at<decltype(ii)::value * 128>(ea); });
   };
-  auto take_exp = [&](int st, uint32_t w) {  // after lds_wait()
+  auto take_exp = [&](int st, uint32_t w, int idx) {  // after lds_wait()
 #pragma unroll
     for (int i = 0; i < TL::TMW; ++i) {
       asm volatile("" : "+v"(ex[i]));
       sx[i] = ex[i] >> (8 * (st & 3));
     }
     asm volatile("" : "+s"(w));  // the scalar load is waited for here, not where it is issued
-    swb = w >> (8 * static_cast<int>(wexp_idx(st) & 3));
+    swb = w >> (8 * (idx & 3));
   };
-
   // The accumulators are named here, so the products above stay above (the
   // compiler would otherwise sink them past the barrier to their next use).
   auto pin_acc = [&]() {
@@ -377,102 +453,155 @@ __global__ __launch_bounds__(TL::NT, 1) void q8_gemm_tile(GemmArgs a) {
       for (int j = 0; j < TL::TNW; ++j) asm volatile("" : "+a"(acc[i][j]));
   };
 
-  if (st1 > st0) {
-    // Every stage of the loop issues the same DMA instructions, so that the waits
-    // count them exactly; those past the range read nothing and write zeros.
+  // An accumulator is cleared by a short product of zeros, which takes its zero
+  // addend as an inline constant (a zero vector would need registers that the
+  // accumulators occupy).
+  auto clear = [&](int i, int j) {
+    uint32_t z = 0;
+    asm volatile("" : "+v"(z));
+    const bf16x8 zv = __builtin_bit_cast(bf16x8, u32x4{z, z, z, z});
+    acc[i][j] = Dt<0>::mfma32(zv, zv, f32x16{});
+    asm volatile("" : "+a"(acc[i][j]));
+  };
+
+  // ---- fill the ring
+  issue_unit(cu);
+  issue_rows();
 #pragma unroll
-    for (int u = 0; u < TL::NS; ++u) issue_all(st0 + u, u);
-    wait_vmcnt<(TL::NS - 1) * TL::L>();
-    __builtin_amdgcn_s_barrier();
-    Frag f0, f1;
-    using H0 = std::integral_constant<int, 0>;
-    using H1 = std::integral_constant<int, 1>;
-    unrolled<NR>([&](auto nn) { read1(f0, 0u, H0{}, nn); });
-    read_exp(st0);
-    const uint32_t w0 = wexp_load(st0);
+  for (int s = 0; s < TL::NS; ++s) {
+    issue_exp(ifirst);
+    unrolled<TL::L>([&](auto kk) { issue1(s, kk); });
+    issue_next();
+  }
+  wait_vmcnt<(TL::NS - 1) * TL::L>();
+  __builtin_amdgcn_s_barrier();
+  Frag f0, f1;
+  cg = 1;
+  unrolled<NR>([&](auto nn) { read1(f0, 0u, H0{}, nn); });
+  read_exp();
+  int widx = wexp_idx(cu);
+  {
+    const uint32_t w = wexp_load(widx);
     lds_wait();
     tie_all(f0);
-    take_exp(st0, w0);
-
-    int slot = 0;
-    for (int st = st0; st < st1; ++st) {
-      const uint32_t so = static_cast<uint32_t>(slot * TL::STAGE_BYTES);
-      const int nslot = slot + 1 == TL::NS ? 0 : slot + 1;
-      const uint32_t sn = static_cast<uint32_t>(nslot * TL::STAGE_BYTES);
-      const int stn = st + 1 < st1 ? st + 1 : st;
-      const uint32_t wn1 = wexp_load(stn);
-      // first half stage's products; the second half's fragments come in
-      constexpr int RA = (NR + NM - 1) / NM;  // reads after each matrix instruction
-      unrolled<NM>([&](auto mm) {
-        constexpr int m = decltype(mm)::value;
-        mfma1(f0, m / TL::TNW, m % TL::TNW);
-        unrolled<RA>([&](auto rr) {
-          constexpr int n = m * RA + decltype(rr)::value;
-          if constexpr (n < NR) read1(f1, so, H1{}, std::integral_constant<int, n>{});
-        });
-        __builtin_amdgcn_sched_barrier(0);
-      });
-      pin_acc();
-      lds_wait();
-      tie_all(f1);
-      // this wave is done with the stage's slot; when all are, and the next
-      // stage's loads have landed, the slot takes stage st + NS
-      wait_vmcnt<(TL::NS - 2) * TL::L>();
-      __builtin_amdgcn_s_barrier();
-      __builtin_amdgcn_sched_barrier(0);
-      if (((st + TL::NS) & 3) == 0) issue_exp(st + TL::NS);
-      read_exp(stn);
-      constexpr int DA = (TL::L + NM - 1) / NM;  // DMA instructions after each matrix instruction
-      unrolled<NM>([&](auto mm) {
-        constexpr int m = decltype(mm)::value;
-        mfma1(f1, m / TL::TNW, m % TL::TNW);
-        unrolled<RA>([&](auto rr) {
-          constexpr int n = m * RA + decltype(rr)::value;
-          if constexpr (n < NR) read1(f0, sn, H0{}, std::integral_constant<int, n>{});
-        });
-        unrolled<DA>([&](auto dd) {
-          constexpr int k = m * DA + decltype(dd)::value;
-          if constexpr (k < TL::L) issue1(st + TL::NS, slot, std::integral_constant<int, k>{});
-        });
-        __builtin_amdgcn_sched_barrier(0);
-      });
-      lds_wait();
-      tie_all(f0);
-      take_exp(stn, wn1);
-      slot = nslot;
-    }
-    wait_vmcnt<0>();  // the DMA past the range is done before the workgroup's LDS is given up
+    take_exp(cu.st0, w, widx);
   }
 
-  // lane coordinates taken anew, so that nothing but the accumulators and the
-  // loop's own values is live across the loop
-  int el = static_cast<int>(threadIdx.x) & 63;
-  asm volatile("" : "+v"(el));
-  const int erow32 = el & 31, ehalf = el >> 5;
-  if (a.nSplit > 1) {
-    // this split's fp32 tile, 16 bytes a lane, in the order the join reads it
-    f32x4* p = reinterpret_cast<f32x4*>(a.part) +
-               ((static_cast<int64_t>(sp) * tiles + (static_cast<int64_t>(rb) * a.nTiles + nt)) * TL::NW + wave) *
-                   (TL::TMW * TL::TNW * 256) + el;
-#pragma unroll
-    for (int i = 0; i < TL::TMW; ++i)
-#pragma unroll
-      for (int j = 0; j < TL::TNW; ++j) {
-        asm volatile("" : "+a"(acc[i][j]));  // one tile at a time leaves the accumulator registers
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          p[((i * TL::TNW + j) * 4 + q) * 64] = f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2],
-                                                      acc[i][j][4 * q + 3]};
-      }
-    return;
-  }
+  // the unit worked on, and what comes after it
+  int st = cu.st0, ck = 0, nst0 = 0;
+  int nwidx = 0;
+  bool more = false;
+  auto look_ahead = [&]() {
+    Unit n;
+    more = unit_of(ck + 1, a, n);
+    nst0 = more ? n.st0 : cu.st0;  // past the last unit: anything readable
+    nwidx = more ? wexp_idx(n) : widx;
+  };
+  look_ahead();
 #pragma unroll
   for (int i = 0; i < TL::TMW; ++i)
 #pragma unroll
-    for (int j = 0; j < TL::TNW; ++j) {
-      asm volatile("" : "+a"(acc[i][j]));
-      store_tile<DT>(a, m0 + (wm * TL::TMW + i) * 32 + erow32, n0 + (wn * TL::TNW + j) * 32, acc[i][j], ehalf);
+    for (int j = 0; j < TL::TNW; ++j) clear(i, j);
+
+  // Half a stage: the products of fragments `cur`, while fragments `nxt` come in
+  // (half s of the slot at rd).  Both reads and DMA instructions stand behind the
+  // first matrix instructions, RA and DA a piece, so that the last ones cover
+  // their latency.
+  int slot = 0;
+  int relax = 0;  // stages until the last tile's stores must be done
+  constexpr int RA = 2 * ((NR + NM - 1) / NM), DA = (TL::L + NM - 1) / NM;
+  auto half_stage = [&](auto ss, Frag& cur, Frag& nxt, uint32_t rd, int wr) {
+    unrolled<NM>([&](auto mm) {
+      constexpr int m = decltype(mm)::value;
+      mfma1(cur, m / TL::TNW, m % TL::TNW);
+      unrolled<RA>([&](auto rr) {
+        constexpr int n = m * RA + decltype(rr)::value;
+        if constexpr (n < NR) read1(nxt, rd, ss, std::integral_constant<int, n>{});
+      });
+      if constexpr (decltype(ss)::value == 0) {  // the stage's second half: its slot loads anew
+        unrolled<DA>([&](auto dd) {
+          constexpr int k = m * DA + decltype(dd)::value;
+          if constexpr (k < TL::L) issue1(wr, std::integral_constant<int, k>{});
+        });
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    });
+    pin_acc();
+  };
+
+  while (true) {
+    const int s1 = slot + 1 == TL::NS ? 0 : slot + 1;
+    const uint32_t rd0 = static_cast<uint32_t>(slot * TL::SLOT_BYTES), rd1 = static_cast<uint32_t>(s1 * TL::SLOT_BYTES);
+    // the next stage: this unit's, or the next unit's first
+    const bool last = st + 1 == cu.st1;
+    const int nst = last ? nst0 : st + 1;
+    widx = last ? nwidx : widx + wexp_step;
+    const uint32_t wn1 = wexp_load(widx);
+
+    half_stage(H1{}, f0, f1, rd0, slot);
+    lds_wait();
+    tie_all(f1);
+    // this wave has read the slot; the next slot has landed; when that holds for
+    // all waves, the slot takes the issuing side's next stage
+    if (relax > 0) {
+      --relax;
+      wait_vmcnt<TL::WAIT + TL::NST>();
+    } else {
+      wait_vmcnt<TL::WAIT>();
     }
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    issue_exp(ifirst);
+    if (last || (nst & 3) == 0) cg = (cg + 1) & (TL::NE - 1);
+    read_exp();
+    half_stage(H0{}, f1, f0, rd1, slot);
+    issue_next();
+    lds_wait();
+    tie_all(f0);
+    if (last) {
+      // lane coordinates taken anew, so that nothing but the accumulators and the
+      // loop's own values is live across the loop
+      int el = static_cast<int>(threadIdx.x) & 63;
+      asm volatile("" : "+v"(el));
+      const uint32_t er = static_cast<uint32_t>(el & 31);
+      const int eh = el >> 5;
+      const bool part = cu.tail >= 0 && a.nSplit > 1;
+      // a split's fp32 tile: 16 bytes a lane, in the order the join reads it
+      f32x4* p = reinterpret_cast<f32x4*>(a.part) +
+                 ((static_cast<int64_t>(cu.split) * (a.nRB * a.nTiles - a.whole) + cu.tail) * TL::NW + wave) *
+                     (TL::TMW * TL::TNW * 256) + el;
+      const __amdgpu_buffer_rsrc_t ry =
+          rows_of_y(a, static_cast<int64_t>(cu.rb) * TL::BM + wm * TL::TMW * 32, TL::TMW * 32);
+      const int64_t c0 = static_cast<int64_t>(cu.nt) * TL::BN + wn * TL::TNW * 32;
+#pragma unroll
+      for (int i = 0; i < TL::TMW; ++i)
+#pragma unroll
+        for (int j = 0; j < TL::TNW; ++j) {
+          asm volatile("" : "+a"(acc[i][j]));  // one tile at a time leaves the accumulator registers
+          if (part) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              p[((i * TL::TNW + j) * 4 + q) * 64] = f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1],
+                                                          acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+          } else {
+            store_tile<DT>(ry, a.vec, i * 32 + er, a.N, c0 + j * 32, acc[i][j], eh);
+          }
+          clear(i, j);
+        }
+      if (!part && a.vec)
+        relax = TL::NS - 1;
+      else
+        wait_vmcnt<0>();
+      if (!more) break;
+      ++ck;
+      unit_of(ck, a, cu);
+      look_ahead();
+    }
+    take_exp(nst, wn1, widx);
+    st = nst;
+    slot = s1;
+  }
+  wait_vmcnt<0>();  // the DMA past the last unit is done before the workgroup's LDS is given up
 }
 
 // One wave a matrix tile of the output: its splits' sums added in order.
@@ -480,142 +609,155 @@ template <int DT, class TL>
 __global__ __launch_bounds__(256) void q8_gemm_join(GemmArgs a) {
   const int lane = threadIdx.x & 63;
   constexpr int PT = TL::NW * TL::TMW * TL::TNW;  // matrix tiles of a workgroup tile
-  const int64_t tiles = static_cast<int64_t>(a.nRB) * a.nTiles;
+  const int64_t ntail = static_cast<int64_t>(a.nRB) * a.nTiles - a.whole;
   const int64_t w = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
-  if (w >= tiles * PT) return;
-  const int64_t tile = w / PT;
+  if (w >= ntail * PT) return;
+  const int64_t tail = w / PT;
   const int sub = static_cast<int>(w % PT);
   const int wave = sub / (TL::TMW * TL::TNW), ij = sub % (TL::TMW * TL::TNW);
-  const f32x4* p = reinterpret_cast<const f32x4*>(a.part) + (tile * PT + sub) * 256 + lane;
+  const f32x4* p = reinterpret_cast<const f32x4*>(a.part) + (tail * PT + sub) * 256 + lane;
   f32x4 s[4];
 #pragma unroll
   for (int q = 0; q < 4; ++q) s[q] = p[q * 64];
   for (int k = 1; k < a.nSplit; ++k) {
-    const f32x4* pk = p + static_cast<int64_t>(k) * tiles * PT * 256;
+    const f32x4* pk = p + static_cast<int64_t>(k) * ntail * PT * 256;
 #pragma unroll
     for (int q = 0; q < 4; ++q) s[q] += pk[q * 64];
   }
   f32x16 acc;
 #pragma unroll
   for (int q = 0; q < 16; ++q) acc[q] = s[q / 4][q % 4];
-  const int64_t m0 = tile / a.nTiles * TL::BM, n0 = tile % a.nTiles * TL::BN;
+  int rb, nt;
+  tile_of(static_cast<uint32_t>(a.whole + tail), a, rb, nt);
   const int i = ij / TL::TNW, j = ij % TL::TNW, wm = wave / TL::WN, wn = wave % TL::WN;
-  store_tile<DT>(a, m0 + (wm * TL::TMW + i) * 32 + (lane & 31), n0 + (wn * TL::TNW + j) * 32, acc, lane >> 5);
+  const int64_t m = static_cast<int64_t>(rb) * TL::BM + (wm * TL::TMW + i) * 32;
+  store_tile<DT>(rows_of_y(a, m, 32), a.vec, static_cast<uint32_t>(lane & 31), a.N,
+                 static_cast<int64_t>(nt) * TL::BN + (wn * TL::TNW + j) * 32, acc, lane >> 5);
 }
 
-// Few rows (T <= 16 TM).  A workgroup owns 16 NJ output columns; its eight
-// waves take the stages in turn and their sums meet in LDS.  The weight goes
-// from global memory straight into fragments, each row's 128 bytes of a stage
-// by two 16-byte loads of four lanes; x stays in the caches.  Lane group g of
-// 16 holds chunks g and g + 4 of a stage on both sides.
-constexpr int kFewWaves = 8, kFewU = 4;
+// Few rows (T <= 16).  A workgroup owns 16 output columns; its 16 waves take the
+// stages in turn and their sums meet in LDS.  The weight goes from global memory
+// straight into fragments of mfma 16x16x128, each row's 128 bytes of a stage by
+// two 16-byte loads of four lanes, four stages in flight a wave; the rows stay in
+// the caches.  Lane group g of 16 holds chunks g and g + 4 of a stage on both
+// sides.  Bound by HBM: 5.5 TB/s of weight at 27648 x 5120 with one row.  Eight
+// waves were 0 to 5% slower, 32 columns a workgroup 10 to 25% (one row).
+constexpr int kFewWaves = 16, kFewU = 4;
 
-template <int DT, int TM, int NJ>
-__global__ __launch_bounds__(64 * kFewWaves, 2) void q8_gemm_few(GemmArgs a) {
+template <int DT>
+__global__ __launch_bounds__(64 * kFewWaves) void q8_gemm_few(GemmArgs a) {
   using T16 = typename Dt<DT>::T;
-  __shared__ f32x4 red[kFewWaves][NJ * TM][64];
+  __shared__ f32x4 red[kFewWaves][64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int l16 = lane & 15, g = lane >> 4;
-  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * (16 * NJ);
-  const uint8_t* xr[TM];
-  const uint8_t* er[TM];
-#pragma unroll
-  for (int i = 0; i < TM; ++i) {  // rows past T repeat the last one; their sums are not stored
-    const int64_t t = min(static_cast<int64_t>(i * 16 + l16), a.T - 1);
-    xr[i] = a.xq + t * a.xp + g * 16;
-    er[i] = a.xe + t * a.xep;
-  }
-  const uint8_t* wr[NJ];
-#pragma unroll
-  for (int j = 0; j < NJ; ++j) wr[j] = a.wq + min(n0 + j * 16 + l16, a.wrows - 1) * a.wp + g * 16;
-  const uint8_t* we = a.we + n0 / kQ8Block * a.wep;  // 16 NJ divides 128: one block
-  f32x4 acc[NJ][TM];
-#pragma unroll
-  for (int j = 0; j < NJ; ++j)
-#pragma unroll
-    for (int i = 0; i < TM; ++i) acc[j][i] = f32x4{};
-
+  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * 16;
+  // rows past T repeat the last one; their sums are not stored
+  const int64_t t = min(static_cast<int64_t>(l16), a.T - 1);
+  const uint8_t* xr = a.xq + t * a.xp + g * 16;
+  const uint8_t* er = a.xe + t * a.xep;
+  const uint8_t* wr = a.wq + min(n0 + l16, a.wrows - 1) * a.wp + g * 16;
+  const uint8_t* we = a.we + n0 / kQ8Block * a.wep;  // 16 divides 128: one block
+  f32x4 acc = f32x4{};
   for (int s0 = wave; s0 < a.S; s0 += kFewWaves * kFewU) {
-    u32x4 w[kFewU][NJ][2], x[kFewU][TM][2];
-    uint32_t ew[kFewU], ex[kFewU][TM];
+    u32x4 w[kFewU][2], x[kFewU][2];
+    uint32_t ew[kFewU], ex[kFewU];
 #pragma unroll
     for (int u = 0; u < kFewU; ++u) {
-      const int st = min(s0 + u * kFewWaves, a.S - 1);
+      const int64_t st = min(s0 + u * kFewWaves, a.S - 1);
 #pragma unroll
-      for (int j = 0; j < NJ; ++j)
-#pragma unroll
-        for (int c = 0; c < 2; ++c)
-          w[u][j][c] = *reinterpret_cast<const u32x4*>(wr[j] + static_cast<int64_t>(st) * kQ8Block + c * 64);
-      ew[u] = we[st];
-#pragma unroll
-      for (int i = 0; i < TM; ++i) {
-#pragma unroll
-        for (int c = 0; c < 2; ++c)
-          x[u][i][c] = *reinterpret_cast<const u32x4*>(xr[i] + static_cast<int64_t>(st) * kQ8Block + c * 64);
-        ex[u][i] = er[i][st];
+      for (int c = 0; c < 2; ++c) {
+        w[u][c] = *reinterpret_cast<const u32x4*>(wr + st * kQ8Block + c * 64);
+        x[u][c] = *reinterpret_cast<const u32x4*>(xr + st * kQ8Block + c * 64);
       }
+      ew[u] = we[st];
+      ex[u] = er[st];
     }
 #pragma unroll
     for (int u = 0; u < kFewU; ++u) {
       if (s0 + u * kFewWaves >= a.S) break;
-#pragma unroll
-      for (int j = 0; j < NJ; ++j)
-#pragma unroll
-        for (int i = 0; i < TM; ++i) {
-          auto v8 = [](const u32x4 (&c)[2]) {
-            return v8i{static_cast<int>(c[0][0]), static_cast<int>(c[0][1]), static_cast<int>(c[0][2]),
-                       static_cast<int>(c[0][3]), static_cast<int>(c[1][0]), static_cast<int>(c[1][1]),
-                       static_cast<int>(c[1][2]), static_cast<int>(c[1][3])};
-          };
-          acc[j][i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-              v8(w[u][j]), v8(x[u][i]), acc[j][i], 0, 0, 0, static_cast<int>(ew[u]), 0, static_cast<int>(ex[u][i]));
-        }
+      auto v8 = [](const u32x4 (&c)[2]) {
+        return v8i{static_cast<int>(c[0][0]), static_cast<int>(c[0][1]), static_cast<int>(c[0][2]),
+                   static_cast<int>(c[0][3]), static_cast<int>(c[1][0]), static_cast<int>(c[1][1]),
+                   static_cast<int>(c[1][2]), static_cast<int>(c[1][3])};
+      };
+      acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(v8(w[u]), v8(x[u]), acc, 0, 0, 0,
+                                                             static_cast<int>(ew[u]), 0, static_cast<int>(ex[u]));
     }
   }
-#pragma unroll
-  for (int j = 0; j < NJ; ++j)
-#pragma unroll
-    for (int i = 0; i < TM; ++i) red[wave][j * TM + i][lane] = acc[j][i];
+  red[wave][lane] = acc;
   __syncthreads();
-  // matrix tile k = wave, wave + 8, ..: register q of lane l is output column
-  // 4*(l/16) + q of row l%16
-  for (int k = wave; k < NJ * TM; k += kFewWaves) {
-    f32x4 s = red[0][k][lane];
+  // register q of lane l is output column 4*(l/16) + q of row l%16
+  if (wave > 0) return;
+  f32x4 s = red[0][lane];
 #pragma unroll
-    for (int w = 1; w < kFewWaves; ++w) s += red[w][k][lane];
-    const int64_t t = (k % TM) * 16 + l16, c = n0 + (k / TM) * 16 + 4 * g;
-    if (t >= a.T) continue;
-    typedef T16 t4 __attribute__((ext_vector_type(4)));
-    const t4 o = {Dt<DT>::from_f(s[0]), Dt<DT>::from_f(s[1]), Dt<DT>::from_f(s[2]), Dt<DT>::from_f(s[3])};
-    T16* y = static_cast<T16*>(a.y) + t * a.N + c;
-    if (a.vec) {  // N % 8 == 0
-      if (c < a.N) *reinterpret_cast<t4*>(y) = o;
-    } else {
+  for (int w = 1; w < kFewWaves; ++w) s += red[w][lane];
+  const int64_t c = n0 + 4 * g;
+  if (l16 >= a.T) return;
+  typedef T16 t4 __attribute__((ext_vector_type(4)));
+  const t4 o = {Dt<DT>::from_f(s[0]), Dt<DT>::from_f(s[1]), Dt<DT>::from_f(s[2]), Dt<DT>::from_f(s[3])};
+  T16* y = static_cast<T16*>(a.y) + static_cast<int64_t>(l16) * a.N + c;
+  if (a.vec) {  // N % 8 == 0
+    if (c < a.N) *reinterpret_cast<t4*>(y) = o;
+  } else {
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        if (c + q < a.N) y[q] = o[q];
-    }
+    for (int q = 0; q < 4; ++q)
+      if (c + q < a.N) y[q] = o[q];
   }
 }
 
-#ifndef Q8_BIG_MIN
-#define Q8_BIG_MIN 192
-#endif
+// An empty contraction: zeros (the kernels above need at least one stage).
+__global__ __launch_bounds__(256) void q8_gemm_zero(uint16_t* y, int64_t n) {
+  for (int64_t e = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; e < n;
+       e += static_cast<int64_t>(gridDim.x) * 256)
+    y[e] = 0;
+}
+
 template <bool TRANS>
 using BigTile = Q8Tile<2, 2, 4, 4, 2, TRANS>;  // 256 x 256
 template <bool TRANS>
 using MidTile = Q8Tile<2, 2, 2, 2, 4, TRANS>;  // 128 x 128
+template <bool TRANS>
+using LowTile = Q8Tile<1, 4, 2, 1, 6, TRANS>;  // 64 x 128, a deep ring: the weight's stream
 
-constexpr int64_t kFewRows = 64;
+// Up to here the weight's stream decides and every wave reads the rows for
+// itself; beyond, 16 rows a wave cost as much as its 16 columns, and tiles of 64
+// rows share them.  27648 x 5120, us: 26 with 1 row; 42 with 16 rows here, 31 in
+// tiles.  8192^2: 16 with 1 row, 19 with 8, 22 with 16, 21.5 in tiles.
+constexpr int64_t kFewRows = 8;
+constexpr int64_t kLowRows = 64;
 
 struct GemmPlan {
-  enum Path { kFew, kBig, kMid } path = kBig;
+  enum Path { kFew, kBig, kMid, kLow } path = kBig;
   int64_t N = 0;
   int S = 0, nSplit = 1;
-  int64_t nRB = 0, nTiles = 0;
+  int64_t nRB = 0, nTiles = 0, whole = 0;
   int64_t grid = 0;
   size_t bytes = 0;
 };
+
+// Tiles of bm x bn: as many rounds of one whole tile a CU as there are, and the
+// rest in up to 16 ranges of stages each (at least four stages), whichever
+// number gives the shortest rounds; a split costs the tile's fp32 partials,
+// written and read, priced in stages.  Returns the cost in stages of one tile.
+double split_plan(GemmPlan& p, int64_t T, int64_t bm, int64_t bn, double cost_split) {
+  p.nRB = q8_ceil(T, bm);
+  p.nTiles = q8_ceil(p.N, bn);
+  const int64_t tiles = p.nRB * p.nTiles;
+  const int64_t rounds = tiles / kCUs, rest = tiles - rounds * kCUs;
+  p.whole = rounds * kCUs;
+  p.nSplit = 1;
+  double best = 0.0;
+  if (rest > 0) {
+    best = p.S;
+    for (int s = 2; s <= 16 && p.S / s >= 4; ++s) {
+      const double c = static_cast<double>(q8_ceil(rest * s, kCUs)) * q8_ceil(p.S, s) + cost_split * s * rest / kCUs;
+      if (c < best) best = c, p.nSplit = s;
+    }
+  }
+  p.grid = std::min<int64_t>(kCUs, q8_ceil(p.whole + rest * p.nSplit, 8) * 8);
+  p.bytes = p.nSplit > 1 ? static_cast<size_t>(rest) * p.nSplit * bm * bn * 4 : 0;
+  return static_cast<double>(rounds) * p.S + best;
+}
 
 GemmPlan gemm_plan(int64_t T, int64_t out, int64_t in, bool trans) {
   GemmPlan p;
@@ -623,31 +765,27 @@ GemmPlan gemm_plan(int64_t T, int64_t out, int64_t in, bool trans) {
   p.S = static_cast<int>(q8_ceil(trans ? out : in, kQ8Block));
   if (!trans && T <= kFewRows) {
     p.path = GemmPlan::kFew;
-    p.grid = q8_ceil(p.N, T <= 16 ? 16 : 32);
+    p.grid = q8_ceil(p.N, 16);
     return p;
   }
-  const int64_t big = q8_ceil(T, 256) * q8_ceil(p.N, 256);
-  p.path = big >= Q8_BIG_MIN ? GemmPlan::kBig : GemmPlan::kMid;
-  const int64_t b = p.path == GemmPlan::kBig ? 256 : 128;
-  p.nRB = q8_ceil(T, b);
-  p.nTiles = q8_ceil(p.N, b);
-  const int64_t tiles = p.nRB * p.nTiles;
-  if (p.path == GemmPlan::kMid) {
-    // one workgroup a CU: split the contraction while CUs are idle, at least
-    // eight stages a split
-    int64_t split = std::min<int64_t>(256 / std::max<int64_t>(tiles, 1), p.S / 8);
-    p.nSplit = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(split, 16)));
+  if (T <= kLowRows) {
+    p.path = GemmPlan::kLow;
+    split_plan(p, T, 64, 128, 4.0);
+    return p;
   }
-  p.grid = q8_ceil(tiles * p.nSplit, 8) * 8;
-  if (p.nSplit > 1) p.bytes = static_cast<size_t>(tiles) * p.nSplit * b * b * 4;
-  return p;
+  GemmPlan big = p, mid = p;
+  const double cb = split_plan(big, T, 256, 256, 20.0), cm = split_plan(mid, T, 128, 128, 16.0);
+  // a stage of the small tile costs 0.4 of the large one's
+  if (cb <= 0.4 * cm) return big;
+  mid.path = GemmPlan::kMid;
+  return mid;
 }
 
 template <int DT, class TL>
 void launch_tile(const GemmArgs& g, const GemmPlan& p, hipStream_t stream) {
   hipLaunchKernelGGL((q8_gemm_tile<DT, TL>), dim3(static_cast<unsigned>(p.grid)), dim3(TL::NT), 0, stream, g);
   if (p.nSplit > 1) {
-    const int64_t waves = p.nRB * p.nTiles * TL::NW * TL::TMW * TL::TNW;
+    const int64_t waves = (p.nRB * p.nTiles - p.whole) * TL::NW * TL::TMW * TL::TNW;
     hipLaunchKernelGGL((q8_gemm_join<DT, TL>), dim3(static_cast<unsigned>(q8_ceil(waves, 4))), dim3(256), 0, stream, g);
   }
 }
@@ -655,18 +793,15 @@ void launch_tile(const GemmArgs& g, const GemmPlan& p, hipStream_t stream) {
 template <int DT>
 void launch_few(const GemmArgs& g, const GemmPlan& p, hipStream_t stream) {
   const dim3 grid(static_cast<unsigned>(p.grid)), block(64 * kFewWaves);
-  if (g.T <= 16)
-    hipLaunchKernelGGL((q8_gemm_few<DT, 1, 1>), grid, block, 0, stream, g);
-  else if (g.T <= 32)
-    hipLaunchKernelGGL((q8_gemm_few<DT, 2, 2>), grid, block, 0, stream, g);
-  else
-    hipLaunchKernelGGL((q8_gemm_few<DT, 4, 2>), grid, block, 0, stream, g);
+  hipLaunchKernelGGL((q8_gemm_few<DT>), grid, block, 0, stream, g);
 }
 
 template <int DT>
 void launch_typed(const GemmArgs& g, const GemmPlan& p, bool trans, hipStream_t stream) {
   if (p.path == GemmPlan::kFew)
     launch_few<DT>(g, p, stream);
+  else if (p.path == GemmPlan::kLow)
+    trans ? launch_tile<DT, LowTile<true>>(g, p, stream) : launch_tile<DT, LowTile<false>>(g, p, stream);
   else if (p.path == GemmPlan::kBig)
     trans ? launch_tile<DT, BigTile<true>>(g, p, stream) : launch_tile<DT, BigTile<false>>(g, p, stream);
   else
@@ -678,11 +813,20 @@ void launch_typed(const GemmArgs& g, const GemmPlan& p, bool trans, hipStream_t 
 size_t q8_gemm_workspace_bytes(int64_t T, int64_t out, int64_t in, bool trans) {
   return gemm_plan(T, out, in, trans).bytes;
 }
-int64_t q8_gemm_max_grid(int64_t T, int64_t out, int64_t in, bool trans) { return gemm_plan(T, out, in, trans).grid; }
+int64_t q8_gemm_max_grid(int64_t T, int64_t out, int64_t in, bool trans) {
+  const GemmPlan p = gemm_plan(T, out, in, trans);
+  return std::max(p.grid, p.nRB * p.nTiles * 16);  // units of work (tiles in up to 16 ranges) are numbered in 32 bits
+}
 
 hipError_t launch_q8_gemm(const Q8GemmArgs& p) {
   const GemmPlan plan = gemm_plan(p.T, p.out, p.in, p.trans);
   const int64_t K = p.trans ? p.out : p.in;
+  if (K == 0) {
+    const int64_t n = p.T * plan.N;
+    hipLaunchKernelGGL(q8_gemm_zero, dim3(static_cast<unsigned>(std::min<int64_t>(q8_ceil(n, 256), 4096))), dim3(256),
+                       0, p.stream, static_cast<uint16_t*>(p.y), n);
+    return hipGetLastError();
+  }
   GemmArgs g{};
   g.xq = static_cast<const uint8_t*>(p.xq);
   g.xe = static_cast<const uint8_t*>(p.xe);
@@ -699,6 +843,7 @@ hipError_t launch_q8_gemm(const Q8GemmArgs& p) {
   g.nRB = static_cast<int>(plan.nRB);
   g.nTiles = static_cast<int>(plan.nTiles);
   g.nSplit = plan.nSplit;
+  g.whole = static_cast<int>(plan.whole);
   g.group = 8;
   g.y = p.y;
   g.vec = plan.N % 8 == 0 && (reinterpret_cast<uintptr_t>(p.y) & 15u) == 0;

@@ -342,7 +342,7 @@ DORA_API int dora_compose_bwd_noalloc(const void* dy, const void* base, const vo
  * of any arithmetic.  q is 16-byte aligned and e 4-byte.  Only bytes written by
  * these entry points (1 to 247) are exponents.
  *
- * Sizes: fewer than 2^31 rows and at most 2^23 - 128 columns (else
+ * Sizes: fewer than 2^31 rows and at most 2^22 - 128 columns (else
  * DORA_UNSUPPORTED).  No output may overlap an input or another output.
  */
 

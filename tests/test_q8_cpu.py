@@ -223,8 +223,8 @@ def test_pack_refusals():
         _status(fn(P, 8, 8, 0, P * 2, P * 3 + 2, None), INVALID, "alignment")
         _status(fn(P, 8, 8, 0, P, P * 3, None), INVALID, "overlaps")
         _status(fn(P, 8, 8, 0, P * 2, P * 2 + 64, None), INVALID, "overlaps")
-        _status(fn(FAR[0], 8, 1 << 24, 0, FAR[1], FAR[2], None), UNSUPPORTED, "beyond")
-        _status(fn(FAR[0], (1 << 23) - 128, (1 << 23) - 128, 0, FAR[1], FAR[2], None), UNSUPPORTED, "blocks")
+        _status(fn(FAR[0], 8, 1 << 23, 0, FAR[1], FAR[2], None), UNSUPPORTED, "beyond")
+        _status(fn(FAR[0], (1 << 22) - 128, (1 << 22) - 128, 0, FAR[1], FAR[2], None), UNSUPPORTED, "blocks")
         assert fn(None, 0, 8, 0, None, None, None) == OK and fn(None, 8, 0, 0, None, None, None) == OK
     _status(LIB.dora_q8_pack(FAR[0], 1 << 31, 8, 0, FAR[1], FAR[2], None), UNSUPPORTED, "beyond")
     u = LIB.dora_q8_unpack
@@ -247,7 +247,7 @@ def test_linear_refusals(name):
 
     _status(call(dt=2), UNSUPPORTED, "dtype")
     _status(call(T=-1), INVALID, "negative")
-    _status(call(out=1 << 23), UNSUPPORTED, "beyond")
+    _status(call(out=1 << 22), UNSUPPORTED, "beyond")
     _status(call(y=None), INVALID, "NULL")
     _status(call(y=FAR[4] + 1), INVALID, "alignment")
     _status(call(xq=None), INVALID, "packed rows")
@@ -262,7 +262,7 @@ def test_linear_refusals(name):
     _status(call(T=T, out=out, in_=in_, wsb=need - 1), INVALID, "workspace of")
     _status(call(T=T, out=out, in_=in_, ws=None), INVALID, "workspace is NULL")
     _status(call(T=T, out=out, in_=in_, ws=FAR[4]), INVALID, "overlaps")
-    _status(call(T=(1 << 31) - 1, out=(1 << 23) - 128, in_=(1 << 23) - 128, xe=1 << 60, wq=1 << 59, we=1 << 58, y=1 << 61), UNSUPPORTED, "workgroups")
+    _status(call(T=(1 << 31) - 1, out=(1 << 22) - 128, in_=(1 << 22) - 128, xe=1 << 60, wq=1 << 59, we=1 << 58, y=1 << 61), UNSUPPORTED, "workgroups")
     assert call(T=0, xq=None, y=None) == OK
     assert query(0, 8, 8) == 0 and query(-1, 8, 8) == 0 and query(8, 1 << 24, 8) == 0
 
