@@ -383,7 +383,9 @@ def dora_norm_bwd(W0, A, B, norm, d_norm, s: float, d_A=None, d_B=None, workspac
 #
 # A packed matrix is a pair (q, e): torch.float8_e4m3fn values and uint8 exponent
 # bytes in the layout of include/dora.h.  These calls run on the tensors' own
-# device, whatever the current one is.
+# device, whatever the current one is.  They are short calls of a serving loop, so
+# what they do besides the launch is kept small (the raw stream handle, no device
+# switch where the device is the current one).
 
 Q8_BLOCK = 128
 
@@ -402,8 +404,10 @@ def q8_weight_shapes(out: int, in_: int):
 
 
 def _packed(q, e, name, shapes, device):
-    _matrix(q, name, shapes[0], torch.float8_e4m3fn, device)
-    _matrix(e, name + "'s exponents", shapes[1], torch.uint8, device)
+    if (q.shape != shapes[0] or e.shape != shapes[1] or q.dtype != torch.float8_e4m3fn or e.dtype != torch.uint8
+            or q.device != device or e.device != device or not q.is_contiguous() or not e.is_contiguous()):
+        _matrix(q, name, shapes[0], torch.float8_e4m3fn, device)  # says which it is
+        _matrix(e, name + "'s exponents", shapes[1], torch.uint8, device)
     if q.data_ptr() % 16 or e.data_ptr() % 4:
         raise ValueError(f"{name} must be 16-byte aligned, its exponents 4-byte")
 
@@ -420,13 +424,34 @@ def _on_gpu(t, name):
     return t.device
 
 
+class _Stay:
+    """In place of a device switch where there is nothing to switch."""
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *exc):
+        return False
+
+
+_STAY = _Stay()
+
+
+def _on_device(device):
+    return _STAY if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+
+
+def _raw_stream(device) -> int:
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
 def _new_packed(shapes, device):
     return (torch.empty(shapes[0], dtype=torch.float8_e4m3fn, device=device),
             torch.empty(shapes[1], dtype=torch.uint8, device=device))
 
 
 def _workspace(need: int, device):
-    return torch.empty(max(need, 1), dtype=torch.uint8, device=device)
+    return torch.empty(need, dtype=torch.uint8, device=device) if need else None
 
 
 def dora_q8_pack(x):
@@ -434,9 +459,9 @@ def dora_q8_pack(x):
     code = _code(x)
     rows, cols = x.shape
     _matrix(x, "x", (rows, cols))
-    with torch.cuda.device(x.device):
+    with _on_device(x.device):
         q, e = _new_packed(q8_row_shapes(rows, cols), x.device)
-        _check(LIB.dora_q8_pack(_ptr(x), rows, cols, code, _ptr(q), _ptr(e), _stream(x.device)))
+        _check(LIB.dora_q8_pack(_ptr(x), rows, cols, code, _ptr(q), _ptr(e), _raw_stream(x.device)))
     return q, e
 
 
@@ -445,9 +470,9 @@ def dora_q8_pack_weight(W):
     code = _code(W)
     out, in_ = W.shape
     _matrix(W, "W", (out, in_))
-    with torch.cuda.device(W.device):
+    with _on_device(W.device):
         q, e = _new_packed(q8_weight_shapes(out, in_), W.device)
-        _check(LIB.dora_q8_pack_weight(_ptr(W), out, in_, code, _ptr(q), _ptr(e), _stream(W.device)))
+        _check(LIB.dora_q8_pack_weight(_ptr(W), out, in_, code, _ptr(q), _ptr(e), _raw_stream(W.device)))
     return q, e
 
 
@@ -460,9 +485,9 @@ def dora_q8_unpack(q, e, rows: int, cols: int, dtype, weight: bool = False):
         _packed(q, e, "q", q8_weight_shapes(q.shape[0], cols), dev)
     else:
         _packed(q, e, "q", q8_row_shapes(rows, cols), dev)
-    with torch.cuda.device(dev):
+    with _on_device(dev):
         x = torch.empty((rows, cols), dtype=dtype, device=dev)
-        _check(LIB.dora_q8_unpack(_ptr(q), _ptr(e), rows, cols, int(weight), code, _ptr(x), _stream(dev)))
+        _check(LIB.dora_q8_unpack(_ptr(q), _ptr(e), rows, cols, int(weight), code, _ptr(x), _raw_stream(dev)))
     return x
 
 
@@ -471,11 +496,12 @@ def dora_q8_linear_fwd(xq, xe, wq, we, out: int, in_: int, dtype):
     code, dev, T = _dtype_code(dtype), _on_gpu(xq, "xq"), xq.shape[0]
     _packed(xq, xe, "xq", q8_row_shapes(T, in_), dev)
     _packed(wq, we, "wq", q8_weight_shapes(out, in_), dev)
-    with torch.cuda.device(dev):
+    with _on_device(dev):
         y = torch.empty((T, out), dtype=dtype, device=dev)
-        ws = _workspace(int(LIB.dora_q8_linear_workspace_bytes(T, out, in_)), dev)
+        need = int(LIB.dora_q8_linear_workspace_bytes(T, out, in_))
+        ws = _workspace(need, dev)
         _check(LIB.dora_q8_linear_fwd(_ptr(xq), _ptr(xe), _ptr(wq), _ptr(we), T, out, in_, code, _ptr(y), _ptr(ws),
-                                      ws.numel(), _stream(dev)))
+                                      need, _raw_stream(dev)))
     return y
 
 
@@ -484,11 +510,12 @@ def dora_q8_linear_bwd(gq, ge, wq, we, out: int, in_: int, dtype):
     code, dev, T = _dtype_code(dtype), _on_gpu(gq, "gq"), gq.shape[0]
     _packed(gq, ge, "gq", q8_row_shapes(T, out), dev)
     _packed(wq, we, "wq", q8_weight_shapes(out, in_), dev)
-    with torch.cuda.device(dev):
+    with _on_device(dev):
         dx = torch.empty((T, in_), dtype=dtype, device=dev)
-        ws = _workspace(int(LIB.dora_q8_linear_bwd_workspace_bytes(T, out, in_)), dev)
+        need = int(LIB.dora_q8_linear_bwd_workspace_bytes(T, out, in_))
+        ws = _workspace(need, dev)
         _check(LIB.dora_q8_linear_bwd(_ptr(gq), _ptr(ge), _ptr(wq), _ptr(we), T, out, in_, code, _ptr(dx), _ptr(ws),
-                                      ws.numel(), _stream(dev)))
+                                      need, _raw_stream(dev)))
     return dx
 
 
@@ -511,7 +538,7 @@ def dora_q8_lora_compose_bwd(dy, bq, be, h, B, mag, norm, s: float, add_base: bo
     _matrix(mag, "mag", (out,), torch.float32, dev)
     _matrix(norm, "norm", (out,), torch.float32, dev)
     dy, h, B = _aligned(dy), _aligned(h), _aligned(B)
-    with torch.cuda.device(dev):
+    with _on_device(dev):
         d_base = q = e = None
         if want_d_base and packed:
             q, e = _new_packed(q8_row_shapes(T, out), dev)
@@ -519,10 +546,11 @@ def dora_q8_lora_compose_bwd(dy, bq, be, h, B, mag, norm, s: float, add_base: bo
             d_base = torch.empty((T, out), dtype=dy.dtype, device=dev)
         d_B = torch.empty((out, r), dtype=dy.dtype, device=dev)
         d_mag = torch.empty(out, dtype=torch.float32, device=dev)
-        ws = _workspace(int(LIB.dora_q8_lora_compose_bwd_workspace_bytes(T, out, r)), dev)
+        need = int(LIB.dora_q8_lora_compose_bwd_workspace_bytes(T, out, r))
+        ws = _workspace(need, dev)
         _check(LIB.dora_q8_lora_compose_bwd(_ptr(dy), _ptr(bq), _ptr(be), _ptr(h), _ptr(B), _ptr(mag), _ptr(norm),
                                             float(s), T, out, r, code, int(bool(add_base)), _ptr(d_base), _ptr(q),
-                                            _ptr(e), _ptr(d_B), _ptr(d_mag), _ptr(ws), ws.numel(), _stream(dev)))
+                                            _ptr(e), _ptr(d_B), _ptr(d_mag), _ptr(ws), need, _raw_stream(dev)))
     return (q, e) if q is not None else d_base, d_B, d_mag
 
 
@@ -534,9 +562,10 @@ def dora_q8_grad_a(dh, xq, xe, in_: int):
     _matrix(dh, "dh", (T, r))
     _packed(xq, xe, "xq", q8_row_shapes(T, in_), dev)
     dh = _aligned(dh)
-    with torch.cuda.device(dev):
+    with _on_device(dev):
         d_A = torch.empty((r, in_), dtype=dh.dtype, device=dev)
-        ws = _workspace(int(LIB.dora_q8_grad_a_workspace_bytes(T, in_, r)), dev)
-        _check(LIB.dora_q8_grad_a(_ptr(dh), _ptr(xq), _ptr(xe), T, in_, r, code, _ptr(d_A), _ptr(ws), ws.numel(),
-                                  _stream(dev)))
+        need = int(LIB.dora_q8_grad_a_workspace_bytes(T, in_, r))
+        ws = _workspace(need, dev)
+        _check(LIB.dora_q8_grad_a(_ptr(dh), _ptr(xq), _ptr(xe), T, in_, r, code, _ptr(d_A), _ptr(ws), need,
+                                  _raw_stream(dev)))
     return d_A

@@ -6,21 +6,32 @@
 //   d_mag  = (sum_t dy * base + s * sum_k B * E) / n
 //   d_A    = d_h^T x = (x^T d_h)^T                         [r x in]
 //
-// Both are row contractions of the tile kernel of bwd_tile.hpp; only how a panel
-// comes in differs.  The compose's backward is bound by HBM: dy at 2 bytes and
-// the base at 1 in, d_base at 2 or (packed) 1 out.  A workgroup's 128 columns
-// are one block of every row, so the packed d_base needs no other workgroup's
-// values, and the product that consumes it (dx = d_base W0) reads half the
-// bytes.  The gradient of A reads x at 1 byte and is bound by the matrix pipe
-// and the LDS reads that feed it.
+// Both are contractions over the tokens, E = X^T Y with X = dy or x and Y = h or
+// d_h, in 16-bit matrix instructions with fp32 sums.
 //
-// Row lengths that are not multiples of 8 (out of dy, r of h, B and d_h) are
-// copied into the workspace with rows padded by zeros first: a copy of the
-// operand costs less than any path of the kernel without 16-byte loads.
+// Kernels:
+//   q8_rows          one pass over X (and the base).  A workgroup owns 128
+//                    columns of X, one block of every row, x up to 384 columns
+//                    of Y x a slice of the tokens.  Stages of 32 tokens go
+//                    global -> LDS by DMA into a ring.  Four waves, one a SIMD,
+//                    each own 64 x 64 TNW of E: a wave reads the fragments of
+//                    the next half stage (16 tokens), transposed by the reads,
+//                    behind the matrix instructions of this one, and its other
+//                    work stands between them too: d_base, its packing and the
+//                    column sums, or the values of x from their bytes.  With
+//                    eight waves and the same work behind the products, a stage
+//                    took the sum of the two: 137 us at 8192^2, r = 384, packed,
+//                    and 73 us for the gradient of A;
+//   q8_bwd_finalize, q8_grad_a_finalize
+//                    the slices added in order, scaled or transposed, rounded;
+//   pad_rows         rows that are not multiples of 8 elements (out of dy, r of h,
+//                    B and d_h) are copied into the workspace with zeros behind
+//                    them first: a copy of the operand costs less than any path
+//                    of the kernel without 16-byte loads.
 #include <algorithm>
 #include <type_traits>
 
-#include "bwd_tile.hpp"
+#include "dma_common.hpp"
 #include "q8_common.hpp"
 
 namespace dora {
@@ -29,6 +40,521 @@ namespace {
 
 inline size_t al256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 inline int64_t up8(int64_t n) { return (n + 7) / 8 * 8; }
+
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+__device__ inline void tie2(u32x2& v) { asm volatile("" : "+v"(v)); }
+template <class F, int... I>
+__device__ inline void unrolled(F&& f, std::integer_sequence<int, I...>) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, class F>
+__device__ inline void unrolled(F&& f) {
+  unrolled(static_cast<F&&>(f), std::make_integer_sequence<int, N>{});
+}
+
+// Transposing LDS reads; in each group of 16 lanes a source lane L gives an
+// 8-byte address and result lane i receives column i.
+//   16 bits: four columns of row L/4, and result lane i the four rows of its column;
+//    8 bits: eight columns (half L%2 of 16) of row L/2, and the eight rows.
+// All LDS reads here are inline assembly (the compiler would wait for every DMA
+// in flight before each); their results are valid after lds_wait*().
+template <int OFF>
+__device__ inline u32x2 read_tr16(uint32_t addr) {
+  u32x2 v;
+  asm volatile("ds_read_b64_tr_b16 %0, %1 offset:%2" : "=v"(v) : "v"(addr), "n"(OFF) : "memory");
+  return v;
+}
+template <int OFF>
+__device__ inline u32x2 read_tr8(uint32_t addr) {
+  u32x2 v;
+  asm volatile("ds_read_b64_tr_b8 %0, %1 offset:%2" : "=v"(v) : "v"(addr), "n"(OFF) : "memory");
+  return v;
+}
+template <int OFF>
+__device__ inline u32x2 read8(uint32_t addr) {
+  u32x2 v;
+  asm volatile("ds_read_b64 %0, %1 offset:%2" : "=v"(v) : "v"(addr), "n"(OFF) : "memory");
+  return v;
+}
+template <int OFF>
+__device__ inline uint32_t read4(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ds_read_b32 %0, %1 offset:%2" : "=v"(v) : "v"(addr), "n"(OFF) : "memory");
+  return v;
+}
+
+// Tile geometry.  LDS image of a stage's 16-bit panels (X = dy, Y): rows of
+// tokens, 256-byte groups of 16 chunks, logical 16-byte chunk c of row t in place
+// c ^ (4 * (t % 4)): the transposing reads touch 4 consecutive rows and 2 chunks
+// of each, and the 8 (row, chunk) pairs then fall in 8 distinct bank groups.  An
+// 8-bit X: rows of 128 bytes, chunk c of row t in place c ^ (2 * ((t/2) % 4)), for
+// 8 rows and 2 chunks.  The 8-bit base is read along its rows and lies plain.
+template <int TNW_, bool GRAD_>
+struct RowsTile {
+  static constexpr int TNW = TNW_;
+  static constexpr bool GRAD = GRAD_;  // the gradient of A; else the compose's backward
+  static constexpr int WM = 2, WN = 2, NW = 4, NT = 256, TMW = 2;
+  static constexpr int BM = 128, BN = 32 * TNW * WN, BK = 32;
+  static constexpr int XROWB = GRAD ? BM : 2 * BM, YROWB = 2 * BN;
+  static constexpr int X_BYTES = BK * XROWB, Y_BYTES = BK * YROWB, B_BYTES = GRAD ? 0 : BK * BM;
+  static constexpr int E_BYTES = 256;  // a dword with the block's exponent per token
+  static constexpr int Y_OFF = X_BYTES, B_OFF = Y_OFF + Y_BYTES, E_OFF = B_OFF + B_BYTES;
+  static constexpr int SLOT_BYTES = (E_OFF + E_BYTES + 1023) / 1024 * 1024;
+  static constexpr int XQ = X_BYTES / 1024 / NW, YQ = Y_BYTES / 1024 / NW, BQ = B_BYTES / 1024 / NW;
+  static constexpr int L = XQ + YQ + BQ;  // DMA instructions a wave and stage (wave 0: and the exponents)
+  static constexpr int NSMAX = 160 * 1024 / SLOT_BYTES, NS = NSMAX < 6 ? NSMAX : 6;
+  static constexpr int LDS_BYTES = NS * SLOT_BYTES;
+  static constexpr int NM = TMW * TNW;  // matrix instructions of a half stage
+  static_assert(NS >= 3 && (NS - 2) * (L + 6) < 64, "ring depth and vmcnt range");
+  static_assert((16 + WN) * BM * 4 <= LDS_BYTES, "the epilogue's sums fit the ring");
+};
+
+__device__ inline int slot16(int c, int t) { return (c & ~15) | ((c ^ (4 * (t & 3))) & 15); }
+
+struct RowsArgs {
+  const void *x, *y;         // X = dy (16 bits) or null, Y [T x r] (16 bits, r % 8 == 0)
+  const uint8_t *q8, *e8;    // the base, or X: 8-bit blocks
+  int64_t T, nx, r;          // nx: columns of X
+  int64_t ldx;               // row pitch of dy in elements: nx rounded up to 8, zeros behind
+  int64_t qp, ep;            // bytes of a packed row, of its exponents
+  int nCB, nTiles, nSplit;
+  float* e_part;             // [nSplit][nx][r]
+  // the compose's backward
+  const void* B;             // [nx x r]
+  const float *mag, *norm;
+  float s;
+  int add_base;
+  void* d_base;              // 16 bits, or null
+  uint8_t *dq, *de;          // packed, or null
+  float* col_part;           // [nSplit][nTiles][nx]
+};
+
+template <int DT, class TL>
+__global__ __launch_bounds__(TL::NT, 1) void q8_rows(RowsArgs a) {
+  using V8 = typename Dt<DT>::V8;
+  using T16 = typename Dt<DT>::T;
+  __shared__ __attribute__((aligned(1024))) char smem[TL::LDS_BYTES];
+  const uint32_t v = static_cast<uint32_t>(xcd_logical_index());
+  const uint32_t nCB = static_cast<uint32_t>(a.nCB), nTl = static_cast<uint32_t>(a.nTiles);
+  if (v >= nCB * nTl * static_cast<uint32_t>(a.nSplit)) return;
+  // consecutive workgroups share a token slice (one slice of Y per XCD's L2)
+  const int nt = static_cast<int>(v % nTl), cb = static_cast<int>((v / nTl) % nCB), sp = static_cast<int>(v / (nTl * nCB));
+  const int64_t nx = a.nx, r = a.r;
+  const int64_t j0 = static_cast<int64_t>(cb) * TL::BM, k0 = static_cast<int64_t>(nt) * TL::BN;
+  const int64_t ts = a.T * sp / a.nSplit, rows = a.T * (sp + 1) / a.nSplit - ts;
+  const int S = static_cast<int>((rows + TL::BK - 1) / TL::BK);
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / TL::WN, wn = wave % TL::WN;
+  const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_char_t*)smem));
+  const bool elem = !TL::GRAD && nt == 0;  // the elementwise part is done by the first block of Y's columns
+
+  // Buffer resources over the token slice: rows past it read zero and are not written.
+  auto slice = [&](const void* p, int64_t pitch) {
+    return __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<char*>(p ? static_cast<const char*>(p) + ts * pitch : nullptr), static_cast<short>(0),
+        static_cast<int>(p ? rows * pitch : 0), kBufferWord3);
+  };
+  const __amdgpu_buffer_rsrc_t rx = TL::GRAD ? slice(a.q8, a.qp) : slice(a.x, a.ldx * 2), ry = slice(a.y, r * 2),
+                               rb = slice(elem ? a.q8 : nullptr, a.qp), re = slice(a.e8, a.ep);
+
+  // Per-lane DMA offsets (stage 0).  Instruction q of wave w moves 1 KiB block q*NW
+  // + w of its panel, lane l writing bytes 16l .. 16l + 15.
+  uint32_t xo[TL::XQ], yo[TL::YQ];
+  const int t8 = 8 * wave + (lane >> 3), c8 = lane & 7;  // an 8-bit panel's row and place
+#pragma unroll
+  for (int q = 0; q < TL::XQ; ++q) {
+    if constexpr (TL::GRAD) {
+      xo[q] = static_cast<uint32_t>(t8 * a.qp + j0 + 16 * (c8 ^ (2 * ((t8 >> 1) & 3))));
+    } else {
+      const int t = 4 * (q * TL::NW + wave) + (lane >> 4);
+      const int64_t col = j0 + 8 * slot16(lane & 15, t);
+      xo[q] = col < a.ldx ? static_cast<uint32_t>((t * a.ldx + col) * 2) : kOob;
+    }
+  }
+#pragma unroll
+  for (int q = 0; q < TL::YQ; ++q) {
+    const int lin = (q * TL::NW + wave) * 64 + lane, t = lin / (TL::BN / 8);
+    const int64_t col = k0 + 8 * slot16(lin % (TL::BN / 8), t);
+    yo[q] = col < r ? static_cast<uint32_t>((t * r + col) * 2) : kOob;
+  }
+  const uint32_t bo = static_cast<uint32_t>(t8 * a.qp + j0 + 16 * c8);
+  const uint32_t eo = lane < TL::BK ? static_cast<uint32_t>(lane * a.ep) + (static_cast<uint32_t>(cb) & ~3u) : kOob;
+  const int eshift = 8 * (cb & 3);
+  const uint32_t xstep = static_cast<uint32_t>(TL::BK * (TL::GRAD ? a.qp : a.ldx * 2));
+  const uint32_t ystep = static_cast<uint32_t>(TL::BK * r * 2), qstep = static_cast<uint32_t>(TL::BK * a.qp);
+  const uint32_t estep = static_cast<uint32_t>(TL::BK * a.ep);
+  // (an offset out of range stays there: it is not advanced)
+  auto at = [](uint32_t o, uint32_t step, uint32_t st) { return o == kOob ? kOob : o + step * st; };
+  auto issue1 = [&](uint32_t st, int slot, auto kk) {
+    constexpr int k = decltype(kk)::value;
+    char* so = smem + slot * TL::SLOT_BYTES;
+    if constexpr (k < TL::XQ)
+      dma16(rx, so + (k * TL::NW + wave) * 1024, at(xo[k], xstep, st));
+    else if constexpr (k < TL::XQ + TL::YQ)
+      dma16(ry, so + TL::Y_OFF + ((k - TL::XQ) * TL::NW + wave) * 1024, at(yo[k - TL::XQ], ystep, st));
+    else
+      dma16(rb, so + TL::B_OFF + wave * 1024, bo + qstep * st);
+  };
+  auto issue_exp = [&](uint32_t st, int slot) {
+    if (wave == 0)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(re, (lds_void_t*)(smem + slot * TL::SLOT_BYTES + TL::E_OFF), 4,
+                                               at(eo, estep, st), 0, 0, 0);
+  };
+
+  // ---- fragment read addresses within a slot.  In a 16-lane group g = l/16, a
+  // 16-bit read covers tokens R0 .. R0 + 3 with R0 = 16 step + 8 (g/2) (+ 4 for the
+  // second read).  Y (operand A): result lane i gets column 32 j + sigma(16 (g%2) +
+  // i), sigma(p) = 16 ((p/4)%2) + 4 (p/8) + p%4, so that accumulator register q of
+  // lane l holds Y column 16 (l/32) + q.  X (operand B): column 32 i + l%32.
+  const int g = lane >> 4, L16 = lane & 15, half = lane >> 5;
+  const int trow = 8 * (g >> 1) + (L16 >> 2);
+  auto addr16 = [&](int off, int rowb, int col) {
+    const int c = col >> 3;
+    return lds0 + static_cast<uint32_t>(off + trow * rowb + slot16(c, trow) * 16 + (col & 7) * 2);
+  };
+  uint32_t ya[TL::TNW], xa[TL::TMW];
+#pragma unroll
+  for (int j = 0; j < TL::TNW; ++j)
+    ya[j] = addr16(TL::Y_OFF, TL::YROWB,
+                   32 * (wn * TL::TNW + j) + 16 * ((L16 & 3) & 1) + 8 * (g & 1) + 4 * ((L16 & 3) >> 1));
+#pragma unroll
+  for (int i = 0; i < TL::TMW; ++i) {
+    if constexpr (TL::GRAD) {
+      const int row = 8 * half + (L16 >> 1), c = 2 * (wm * TL::TMW + i) + (g & 1);
+      xa[i] = lds0 + static_cast<uint32_t>(row * TL::XROWB + (c ^ (2 * ((row >> 1) & 3))) * 16 + (L16 & 1) * 8);
+    } else {
+      xa[i] = addr16(0, TL::XROWB, 32 * (wm * TL::TMW + i) + 16 * (g & 1) + 4 * (L16 & 3));
+    }
+  }
+
+  f32x16 acc[TL::TMW][TL::TNW];
+#pragma unroll
+  for (int i = 0; i < TL::TMW; ++i)
+#pragma unroll
+    for (int j = 0; j < TL::TNW; ++j) acc[i][j] = f32x16{};
+
+  // A half stage's fragments as read, and (8-bit X) its values once decoded.
+  struct Frag {
+    u32x2 y[TL::TNW][2];
+    u32x2 x[TL::TMW][2];  // 8-bit X: one read, eight tokens
+    u32x4 e[2];           // 8-bit X: the eight tokens' exponent dwords
+    V8 xv[TL::TMW];
+  };
+  constexpr int NX = TL::GRAD ? TL::TMW + 2 : 2 * TL::TMW;  // reads of X (first), then of Y
+  constexpr int NR = NX + 2 * TL::TNW;
+  auto read1 = [&](Frag& f, uint32_t so, auto ss, auto nn) {
+    constexpr int s = decltype(ss)::value, n = decltype(nn)::value;
+    if constexpr (n >= NX) {
+      constexpr int j = (n - NX) / 2, c = (n - NX) % 2;
+      f.y[j][c] = read_tr16<(16 * s + 4 * c) * TL::YROWB>(ya[j] + so);
+    } else if constexpr (!TL::GRAD) {
+      constexpr int i = n / 2, c = n % 2;
+      f.x[i][c] = read_tr16<(16 * s + 4 * c) * TL::XROWB>(xa[i] + so);
+    } else if constexpr (n < TL::TMW) {
+      f.x[n][0] = read_tr8<16 * s * TL::XROWB>(xa[n] + so);
+    } else {
+      constexpr int c = n - TL::TMW;
+      f.e[c] = lds_read16_at<TL::E_OFF + 64 * s + 16 * c>(lds0 + so + 32 * half);
+    }
+  };
+  auto tie_y = [&](Frag& f) {
+#pragma unroll
+    for (int j = 0; j < TL::TNW; ++j)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) tie2(f.y[j][c]);
+  };
+  auto tie_x = [&](Frag& f) {
+#pragma unroll
+    for (int i = 0; i < TL::TMW; ++i)
+#pragma unroll
+      for (int c = 0; c < (TL::GRAD ? 1 : 2); ++c) tie2(f.x[i][c]);
+    if constexpr (TL::GRAD) {
+      tie(f.e[0]);
+      tie(f.e[1]);
+    }
+  };
+  // x's values of fragment i: a lane holds eight tokens of one column
+  float sc[8];
+  bool top = false;  // a block of these tokens may hold values past the type's range
+  auto scales = [&](Frag& f) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const uint32_t byte = (f.e[k >> 2][k & 3] >> eshift) & 255u;
+      m = max(m, byte);
+      sc[k] = q8_scale(byte);
+    }
+    top = __any(m >= (DT == 0 ? 247u : 135u));  // 256 * 2^e past the type
+  };
+  auto decode = [&](Frag& f, int i) {
+    float x[8];
+    q8_decode8(uint2{f.x[i][0][0], f.x[i][0][1]}, 1.0f, x);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x[k] *= sc[k];
+    if (top) q8_hold<DT>(x);
+    f.xv[i] = __builtin_bit_cast(V8, f32_to_chunk<DT>(x));
+  };
+  auto mfma1 = [&](Frag& f, int i, int j) {
+    const V8 yv = __builtin_bit_cast(V8, u32x4{f.y[j][0][0], f.y[j][0][1], f.y[j][1][0], f.y[j][1][1]});
+    if constexpr (TL::GRAD)
+      acc[i][j] = Dt<DT>::mfma32(yv, f.xv[i], acc[i][j]);
+    else
+      acc[i][j] = Dt<DT>::mfma32(
+          yv, __builtin_bit_cast(V8, u32x4{f.x[i][0][0], f.x[i][0][1], f.x[i][1][0], f.x[i][1][1]}), acc[i][j]);
+  };
+  auto pin_acc = [&]() {
+#pragma unroll
+    for (int i = 0; i < TL::TMW; ++i)
+#pragma unroll
+      for (int j = 0; j < TL::TNW; ++j) asm volatile("" : "+a"(acc[i][j]));
+  };
+
+  // ---- the elementwise part of the compose's backward: this thread takes chunk
+  // ec (8 columns) of token rows et and et + 16 of every stage
+  const int et = tid >> 4, ec = tid & 15;
+  const int64_t ecol = j0 + 8 * ec;
+  float gb[8], colsum[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    colsum[e] = 0.0f;
+    gb[e] = 0.0f;
+    if (elem && ecol + e < nx) {
+      const float m = a.mag[ecol + e], n = a.norm[ecol + e];
+      gb[e] = a.add_base ? m / n : (m - n) / n;
+    }
+  }
+  const __amdgpu_buffer_rsrc_t rdb = slice(elem ? a.d_base : nullptr, nx * 2),
+                               rdq = slice(elem ? a.dq : nullptr, a.qp), rde = slice(elem ? a.de : nullptr, a.ep);
+  const bool out16 = elem && a.d_base, outq = elem && a.dq, pair = a.ldx == nx;
+  const uint32_t ea = lds0 + static_cast<uint32_t>(et * TL::XROWB + slot16(ec, et) * 16);  // (et + 16: the same place)
+  const uint32_t ba = lds0 + static_cast<uint32_t>(TL::B_OFF + et * TL::BM + ec * 8);
+  const uint32_t xa4 = lds0 + static_cast<uint32_t>(TL::E_OFF + et * 4);
+  u32x4 wd[2];
+  u32x2 wb[2];
+  uint32_t we[2];
+  auto elem_read = [&](uint32_t so) {
+    wd[0] = lds_read16_at<0>(ea + so);
+    wd[1] = lds_read16_at<16 * TL::XROWB>(ea + so);
+    wb[0] = read8<0>(ba + so);
+    wb[1] = read8<16 * TL::BM>(ba + so);
+    we[0] = read4<0>(xa4 + so);
+    we[1] = read4<64>(xa4 + so);
+  };
+  auto elem_tie = [&]() {
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      tie(wd[c]);
+      tie2(wb[c]);
+      asm volatile("" : "+v"(we[c]));
+    }
+  };
+  // one of six pieces of the work on row c, a few instructions each
+  float ed[8], eb[8];
+  uint32_t ebyte = 127;
+  auto elem_piece = [&](uint32_t st, int c, int piece) {
+    const uint32_t t = st * TL::BK + static_cast<uint32_t>(et + 16 * c);
+    if (piece == 0) {
+      q8_decode8(uint2{wb[c][0], wb[c][1]}, q8_scale((we[c] >> eshift) & 255u), eb);
+    } else if (piece == 1) {
+      chunk_to_f32<DT>(__builtin_bit_cast(Chunk, wd[c]), ed);
+    } else if (piece == 2) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) colsum[e] = __builtin_fmaf(ed[e], eb[e], colsum[e]);
+    } else if (piece == 3) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) ed[e] *= gb[e];
+    } else if (piece == 4) {
+      if (outq) ebyte = q8_exp_byte(q8_block_amax(ed));
+    } else {
+      if (out16) {
+        const uint32_t o = (t * static_cast<uint32_t>(nx) + static_cast<uint32_t>(ecol)) * 2;
+        if (pair) {
+          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, f32_to_chunk<DT>(ed)), rdb,
+                                                 ecol < nx ? o : kOob, 0, 0);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            __builtin_amdgcn_raw_buffer_store_b16(__builtin_bit_cast(uint16_t, Dt<DT>::from_f(ed[e])), rdb,
+                                                  ecol + e < nx ? o + 2 * e : kOob, 0, 0);
+        }
+      }
+      if (outq) {
+        // columns behind nx have dy = 0 and gb = 0: their packed values are zeros
+        const uint2 w = q8_encode8(ed, q8_scale(ebyte));
+        __builtin_amdgcn_raw_buffer_store_b64(u32x2{w.x, w.y}, rdq,
+                                              t * static_cast<uint32_t>(a.qp) + static_cast<uint32_t>(ecol), 0, 0);
+        // the block's byte by lane 0, the exponent row's padding by the last block's other lanes
+        const bool pad = cb == a.nCB - 1 && cb + ec < a.ep;
+        __builtin_amdgcn_raw_buffer_store_b8(
+            static_cast<uint8_t>(ec == 0 ? ebyte : 127u), rde,
+            ec == 0 || pad ? t * static_cast<uint32_t>(a.ep) + static_cast<uint32_t>(cb + ec) : kOob, 0, 0);
+      }
+    }
+  };
+  // The slot after stage st's has landed when at most what was issued after its
+  // loads is outstanding: the loads of NS - 2 stages, and the stores of as many
+  // (none is counted before there are so many; more stores than counted, as single
+  // 16-bit ones, only make the wait longer).
+  const int nstore = (out16 ? 2 : 0) + (outq ? 4 : 0);
+  auto wait_next = [&](int st) {
+    constexpr int W = (TL::NS - 2) * TL::L, M = TL::NS - 2;
+    const int n = st < M ? 0 : nstore;
+    if (n == 0)
+      wait_vmcnt<W>();
+    else if (n == 2)
+      wait_vmcnt<W + 2 * M>();
+    else if (n == 4)
+      wait_vmcnt<W + 4 * M>();
+    else
+      wait_vmcnt<W + 6 * M>();
+  };
+
+  using H0 = std::integral_constant<int, 0>;
+  using H1 = std::integral_constant<int, 1>;
+  constexpr int RA = (NR + TL::NM - 1) / TL::NM * 2, DA = (TL::L + TL::NM - 1) / TL::NM;
+  constexpr int PA = (12 + TL::NM - 1) / TL::NM;                     // elementwise pieces behind each instruction
+  constexpr int MX = (NX + RA - 1) / RA < TL::NM / 2 ? TL::NM / 2 : 0;  // 8-bit X: decoding starts behind it
+  constexpr int SENT = (MX + 1) * RA < NR ? (MX + 1) * RA : NR;      // reads sent by then
+  static_assert(!TL::GRAD || SENT - NX < 16, "lgkmcnt range");
+
+  // Half a stage: the products of `cur` while the fragments `nxt` come in (half s
+  // of the slot at rd).  In the stage's second half its slot loads anew and the
+  // elementwise part, read in the first half, is worked on.
+  auto half_stage = [&](auto ss, Frag& cur, Frag& nxt, uint32_t rd, uint32_t st, int wr) {
+    constexpr int s = decltype(ss)::value;
+    unrolled<TL::NM>([&](auto mm) {
+      constexpr int m = decltype(mm)::value;
+      mfma1(cur, m / TL::TNW, m % TL::TNW);
+      unrolled<RA>([&](auto rr) {
+        constexpr int n = m * RA + decltype(rr)::value;
+        if constexpr (n < NR) read1(nxt, rd, ss, std::integral_constant<int, n>{});
+      });
+      if constexpr (s == 0) {
+        unrolled<DA>([&](auto dd) {
+          constexpr int k = m * DA + decltype(dd)::value;
+          if constexpr (k < TL::L) issue1(st + TL::NS, wr, std::integral_constant<int, k>{});
+        });
+        if constexpr (!TL::GRAD) {
+          if (elem) {
+#pragma unroll
+            for (int p = m * PA; p < (m + 1) * PA && p < 12; ++p) elem_piece(st, p / 6, p % 6);
+          }
+        }
+      }
+      if constexpr (TL::GRAD && m == MX) {
+        lds_wait_keep<(SENT > NX ? SENT - NX : 0)>();
+        tie_x(nxt);
+        scales(nxt);
+      }
+      if constexpr (TL::GRAD && m > MX && m - MX - 1 < TL::TMW) decode(nxt, m - MX - 1);
+      __builtin_amdgcn_sched_barrier(0);
+    });
+    pin_acc();
+  };
+  auto end_half = [&](Frag& nxt) {
+    lds_wait();
+    tie_y(nxt);
+    if constexpr (!TL::GRAD) tie_x(nxt);
+    if constexpr (TL::GRAD) {
+#pragma unroll
+      for (int i = 0; i < TL::TMW; ++i)
+        if (TL::NM - 1 - MX <= i) decode(nxt, i);  // (a narrow tile has too few instructions for all)
+    }
+  };
+
+  if (S > 0) {
+#pragma unroll
+    for (int u = 0; u < TL::NS; ++u) {  // stages past the slice read zeros
+      issue_exp(u, u);
+      unrolled<TL::L>([&](auto kk) { issue1(u, u, kk); });
+    }
+    wait_vmcnt<(TL::NS - 1) * TL::L>();
+    __builtin_amdgcn_s_barrier();
+    Frag f0, f1;
+    unrolled<NR>([&](auto nn) { read1(f0, 0u, H0{}, nn); });
+    lds_wait();
+    tie_x(f0);
+    tie_y(f0);
+    if constexpr (TL::GRAD) {
+      scales(f0);
+#pragma unroll
+      for (int i = 0; i < TL::TMW; ++i) decode(f0, i);
+    }
+    int slot = 0;
+    for (int st = 0; st < S; ++st) {
+      const int s1 = slot + 1 == TL::NS ? 0 : slot + 1;
+      const uint32_t so = static_cast<uint32_t>(slot * TL::SLOT_BYTES);
+      if constexpr (!TL::GRAD) elem_read(so);
+      half_stage(H1{}, f0, f1, so, static_cast<uint32_t>(st), slot);
+      end_half(f1);
+      if constexpr (!TL::GRAD) elem_tie();
+      wait_next(st);
+      __builtin_amdgcn_s_barrier();
+      __builtin_amdgcn_sched_barrier(0);
+      issue_exp(static_cast<uint32_t>(st + TL::NS), slot);
+      half_stage(H0{}, f1, f0, static_cast<uint32_t>(s1 * TL::SLOT_BYTES), static_cast<uint32_t>(st), slot);
+      end_half(f0);
+      slot = s1;
+    }
+    wait_vmcnt<0>();
+  }
+  __syncthreads();
+
+  // ---- epilogue: E's slice, and with it s * sum_k B E and the column sums
+  float* red = reinterpret_cast<float*>(smem);  // [16][128] column sums, then [WN][128] sums of B E
+  const T16* Bp = static_cast<const T16*>(a.B);
+  const int fr = lane & 31;
+  float* ep = a.e_part + static_cast<int64_t>(sp) * nx * r;
+#pragma unroll
+  for (int i = 0; i < TL::TMW; ++i) {
+    const int jl = 32 * (wm * TL::TMW + i) + fr;
+    const int64_t j = j0 + jl;
+    float bsum = 0.0f;
+#pragma unroll
+    for (int jj = 0; jj < TL::TNW; ++jj) {
+      asm volatile("" : "+a"(acc[i][jj]));
+      const int64_t k = k0 + 32 * (wn * TL::TNW + jj) + 16 * half;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        if (j >= nx || k + 8 * c >= r) continue;  // r % 8 == 0: whole chunks
+        float* dst = ep + j * r + k + 8 * c;
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+          *reinterpret_cast<f32x4*>(dst + 4 * q) =
+              f32x4{acc[i][jj][8 * c + 4 * q], acc[i][jj][8 * c + 4 * q + 1], acc[i][jj][8 * c + 4 * q + 2],
+                    acc[i][jj][8 * c + 4 * q + 3]};
+        if constexpr (!TL::GRAD) {
+          float bf[8];
+          chunk_to_f32<DT>(*reinterpret_cast<const Chunk*>(Bp + j * r + k + 8 * c), bf);
+          float u0 = 0.0f, u1 = 0.0f;
+#pragma unroll
+          for (int q = 0; q < 8; q += 2) {
+            u0 = __builtin_fmaf(bf[q], acc[i][jj][8 * c + q], u0);
+            u1 = __builtin_fmaf(bf[q + 1], acc[i][jj][8 * c + q + 1], u1);
+          }
+          bsum += u0 + u1;
+        }
+      }
+    }
+    if constexpr (!TL::GRAD) {
+      bsum += __shfl_xor(bsum, 32, 64);
+      if (half == 0) red[16 * 128 + wn * 128 + jl] = bsum;
+    }
+  }
+  if constexpr (!TL::GRAD) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) red[et * 128 + 8 * ec + e] = colsum[e];
+    __syncthreads();
+    if (tid < TL::BM && j0 + tid < nx) {
+      float cs = 0.0f;
+      if (elem)
+        for (int t = 0; t < 16; ++t) cs += red[t * 128 + tid];
+      const float bs = red[16 * 128 + tid] + red[17 * 128 + tid];
+      a.col_part[(static_cast<int64_t>(sp) * nTl + nt) * nx + j0 + tid] = cs + a.s * bs;
+    }
+  }
+}
 
 // Rows of n 16-bit elements to rows of np >= n, zeros behind: 8 elements a thread.
 __global__ __launch_bounds__(256) void pad_rows(const uint16_t* x, int64_t rows, int64_t n, int64_t np, Chunk* y) {
@@ -123,21 +649,44 @@ __global__ __launch_bounds__(256) void q8_grad_a_finalize(const float* e_part, i
   for (int q = jy; q < 64 && j0 + q < r; q += 4) o[(j0 + q) * in] = Dt<DT>::from_f(tile[q][kx]);
 }
 
+// Y's columns a workgroup takes, in 128s (least padding, then widest), and token
+// slices: one workgroup a CU (it holds most of its LDS), at least eight stages.
+struct RowsPlan {
+  int tn = 1, nCB = 0, nTiles = 0, nSplit = 1;
+  size_t off_col = 0, bytes = 0;
+};
+RowsPlan rows_plan(int64_t T, int64_t nx, int64_t r) {
+  RowsPlan p;
+  int64_t best = -1;
+  for (int tn = 1; tn <= 3; ++tn) {
+    const int64_t pad = q8_ceil(r, 128 * tn) * 128 * tn;
+    if (best < 0 || pad <= best) best = pad, p.tn = tn;
+  }
+  p.nCB = static_cast<int>(q8_ceil(nx, 128));
+  p.nTiles = static_cast<int>(q8_ceil(r, 128 * p.tn));
+  const int64_t blocks = static_cast<int64_t>(p.nCB) * p.nTiles;
+  int64_t split = std::min<int64_t>(q8_ceil(256, blocks), std::max<int64_t>(1, T / 256));
+  p.nSplit = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(split, 64)));
+  p.off_col = al256(static_cast<size_t>(p.nSplit) * nx * r * 4);
+  p.bytes = p.off_col + static_cast<size_t>(p.nSplit) * p.nTiles * nx * 4;
+  return p;
+}
+
 struct Q8BwdPlan {
-  BwdPlan tile;
+  RowsPlan tile;
   int64_t xp = 0, rp = 0;  // padded row lengths of dy (or d_h's rank) in elements
   size_t off_dy = 0, off_h = 0, off_B = 0, bytes = 0;
   bool pad_x = false, pad_r = false;
 };
 
-// nx: columns of the X operand (out, or in); with_x: X is 16 bits (dy).
+// nx: columns of X (out, or in); compose: X is dy.
 Q8BwdPlan q8_bwd_plan(int64_t T, int64_t nx, int64_t r, bool compose) {
   Q8BwdPlan p;
   p.rp = std::max<int64_t>(8, up8(r));
   p.xp = up8(nx);
   p.pad_x = compose && p.xp != nx;
   p.pad_r = p.rp != r;
-  p.tile = bwd_plan(T, nx, p.rp, true);
+  p.tile = rows_plan(T, nx, p.rp);
   size_t at = al256(p.tile.bytes);
   p.off_dy = at;
   if (p.pad_x) at = al256(at + static_cast<size_t>(T) * p.xp * 2);
@@ -149,13 +698,26 @@ Q8BwdPlan q8_bwd_plan(int64_t T, int64_t nx, int64_t r, bool compose) {
   return p;
 }
 
-template <int DT, bool BASE, int KIND>
-void launch_kind(const BwdArgs& a, int tn, hipStream_t stream) {
-  switch (tn) {
-    case 1: launch_bwd_dma<DT, 1, BASE, false, KIND>(a, stream); break;
-    case 2: launch_bwd_dma<DT, 2, BASE, false, KIND>(a, stream); break;
-    default: launch_bwd_dma<DT, 3, BASE, false, KIND>(a, stream); break;
-  }
+template <bool GRAD>
+void launch_rows(const RowsArgs& a, int tn, int dtype, hipStream_t stream) {
+  const int64_t total = static_cast<int64_t>(a.nCB) * a.nTiles * a.nSplit;
+  const dim3 grid(static_cast<unsigned>(q8_ceil(total, 8) * 8));
+  auto go = [&](auto dt, auto t) {
+    using TL = RowsTile<2 * decltype(t)::value, GRAD>;
+    hipLaunchKernelGGL((q8_rows<decltype(dt)::value, TL>), grid, dim3(TL::NT), 0, stream, a);
+  };
+  auto by_tile = [&](auto dt) {
+    if (tn == 1)
+      go(dt, std::integral_constant<int, 1>{});
+    else if (tn == 2)
+      go(dt, std::integral_constant<int, 2>{});
+    else
+      go(dt, std::integral_constant<int, 3>{});
+  };
+  if (dtype == 0)
+    by_tile(std::integral_constant<int, 0>{});
+  else
+    by_tile(std::integral_constant<int, 1>{});
 }
 
 }  // namespace
@@ -172,18 +734,18 @@ Q8BwdSizes q8_bwd_sizes(int64_t T, int64_t nx, int64_t r, bool compose) {
 hipError_t launch_q8_compose_bwd(const Q8ComposeBwdArgs& p) {
   const Q8BwdPlan plan = q8_bwd_plan(p.T, p.out, p.r, true);
   char* ws = static_cast<char*>(p.ws);
-  BwdArgs a{};
-  a.dy = p.dy;
-  a.h = p.h;
+  RowsArgs a{};
+  a.x = p.dy;
+  a.y = p.h;
   a.B = p.B;
   if (plan.pad_x) {
     launch_pad(p.dy, p.T, p.out, plan.xp, ws + plan.off_dy, p.stream);
-    a.dy = ws + plan.off_dy;
+    a.x = ws + plan.off_dy;
   }
   if (plan.pad_r) {
     launch_pad(p.h, p.T, p.r, plan.rp, ws + plan.off_h, p.stream);
     launch_pad(p.B, p.out, p.r, plan.rp, ws + plan.off_B, p.stream);
-    a.h = ws + plan.off_h;
+    a.y = ws + plan.off_h;
     a.B = ws + plan.off_B;
   }
   a.mag = p.mag;
@@ -192,10 +754,9 @@ hipError_t launch_q8_compose_bwd(const Q8ComposeBwdArgs& p) {
   a.s = p.s;
   a.add_base = p.add_base;
   a.T = p.T;
-  a.out = p.out;
+  a.nx = p.out;
   a.r = plan.rp;
   a.ldx = plan.xp;
-  a.ldy = plan.rp;
   a.nCB = plan.tile.nCB;
   a.nTiles = plan.tile.nTiles;
   a.nSplit = plan.tile.nSplit;
@@ -205,13 +766,10 @@ hipError_t launch_q8_compose_bwd(const Q8ComposeBwdArgs& p) {
   a.e8 = static_cast<const uint8_t*>(p.be);
   a.qp = q8_row_bytes(p.out);
   a.ep = q8_exp_bytes(p.out);
-  a.dq8 = static_cast<uint8_t*>(p.dq);
-  a.de8 = static_cast<uint8_t*>(p.de);
+  a.dq = static_cast<uint8_t*>(p.dq);
+  a.de = static_cast<uint8_t*>(p.de);
   if (p.T > 0) {
-    if (p.dtype == 0)
-      launch_kind<0, true, kBwdBase8>(a, plan.tile.tn, p.stream);
-    else
-      launch_kind<1, true, kBwdBase8>(a, plan.tile.tn, p.stream);
+    launch_rows<false>(a, plan.tile.tn, p.dtype, p.stream);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -229,17 +787,16 @@ hipError_t launch_q8_compose_bwd(const Q8ComposeBwdArgs& p) {
 hipError_t launch_q8_grad_a(const Q8GradAArgs& p) {
   const Q8BwdPlan plan = q8_bwd_plan(p.T, p.in, p.r, false);
   char* ws = static_cast<char*>(p.ws);
-  BwdArgs a{};
-  a.h = p.dh;
+  RowsArgs a{};
+  a.y = p.dh;
   if (plan.pad_r) {
     launch_pad(p.dh, p.T, p.r, plan.rp, ws + plan.off_h, p.stream);
-    a.h = ws + plan.off_h;
+    a.y = ws + plan.off_h;
   }
   a.T = p.T;
-  a.out = p.in;
+  a.nx = p.in;
   a.r = plan.rp;
   a.ldx = plan.xp;
-  a.ldy = plan.rp;
   a.nCB = plan.tile.nCB;
   a.nTiles = plan.tile.nTiles;
   a.nSplit = plan.tile.nSplit;
@@ -249,10 +806,7 @@ hipError_t launch_q8_grad_a(const Q8GradAArgs& p) {
   a.qp = q8_row_bytes(p.in);
   a.ep = q8_exp_bytes(p.in);
   if (p.T > 0) {
-    if (p.dtype == 0)
-      launch_kind<0, false, kBwdX8>(a, plan.tile.tn, p.stream);
-    else
-      launch_kind<1, false, kBwdX8>(a, plan.tile.tn, p.stream);
+    launch_rows<true>(a, plan.tile.tn, p.dtype, p.stream);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }

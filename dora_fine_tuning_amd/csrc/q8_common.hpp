@@ -34,61 +34,77 @@ __device__ inline uint32_t q8_exp_byte(float amax) {
   const int e = static_cast<int>(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
   return static_cast<uint32_t>((e < -126 ? -126 : e) + 127);
 }
-// 2^e and 2^-e for a byte in [1, 247]
+// 2^e for a byte in [1, 247]
 __device__ inline float q8_scale(uint32_t byte) { return __builtin_bit_cast(float, byte << 23); }
-__device__ inline float q8_inv_scale(uint32_t byte) { return __builtin_bit_cast(float, (254u - byte) << 23); }
 
-// Eight values times 2^-e, rounded to nearest even e4m3; anything not finite is NaN.
-__device__ inline uint2 q8_encode8(const float (&v)[8], float inv) {
-  float f[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const bool fin = (__builtin_bit_cast(uint32_t, v[i]) & 0x7f800000u) != 0x7f800000u;
-    f[i] = fin ? v[i] * inv : __builtin_nanf("");
-  }
-  int lo = __builtin_amdgcn_cvt_pk_fp8_f32(f[0], f[1], 0, false);
-  lo = __builtin_amdgcn_cvt_pk_fp8_f32(f[2], f[3], lo, true);
-  int hi = __builtin_amdgcn_cvt_pk_fp8_f32(f[4], f[5], 0, false);
-  hi = __builtin_amdgcn_cvt_pk_fp8_f32(f[6], f[7], hi, true);
-  return uint2{static_cast<uint32_t>(lo), static_cast<uint32_t>(hi)};
+// Eight values times 2^-e, rounded to nearest even e4m3 (values that are not
+// finite give NaN); |v| * 2^-e is at most 448 where it is finite.  The conversion
+// divides by its scale operand, a power of two, exactly.
+__device__ inline uint2 q8_encode8(const float (&v)[8], float scale) {
+  typedef short s2 __attribute__((ext_vector_type(2)));
+  s2 lo = {0, 0}, hi = {0, 0};
+  lo = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(lo, v[0], v[1], scale, false);
+  lo = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(lo, v[2], v[3], scale, true);
+  hi = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(hi, v[4], v[5], scale, false);
+  hi = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(hi, v[6], v[7], scale, true);
+  return uint2{__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi)};
 }
 
 typedef float q8_f2 __attribute__((ext_vector_type(2)));
 // Eight e4m3 values times 2^e, in fp32.
 __device__ inline void q8_decode8(uint2 q, float scale, float (&f)[8]) {
-  const q8_f2 a = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(q.x), false);
-  const q8_f2 b = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(q.x), true);
-  const q8_f2 c = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(q.y), false);
-  const q8_f2 d = __builtin_amdgcn_cvt_pk_f32_fp8(static_cast<int>(q.y), true);
-  f[0] = a[0] * scale, f[1] = a[1] * scale, f[2] = b[0] * scale, f[3] = b[1] * scale;
-  f[4] = c[0] * scale, f[5] = c[1] * scale, f[6] = d[0] * scale, f[7] = d[1] * scale;
+  const q8_f2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(q.x, scale, false);
+  const q8_f2 b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(q.x, scale, true);
+  const q8_f2 c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(q.y, scale, false);
+  const q8_f2 d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(q.y, scale, true);
+  f[0] = a[0], f[1] = a[1], f[2] = b[0], f[3] = b[1], f[4] = c[0], f[5] = c[1], f[6] = d[0], f[7] = d[1];
 }
 
 // A value past the type's largest (a block's top rounded up) is held at it; NaN stays.
 template <int DT>
-__device__ inline void q8_hold(float (&f)[8]) {
+__device__ inline float q8_hold1(float f) {
   constexpr float big = DT == 0 ? 3.3895313892515355e38f : 65504.0f;
+  f = f > big ? big : f;
+  return f < -big ? -big : f;
+}
+template <int DT>
+__device__ inline void q8_hold(float (&f)[8]) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    f[i] = f[i] > big ? big : f[i];
-    f[i] = f[i] < -big ? -big : f[i];
-  }
+  for (int i = 0; i < 8; ++i) f[i] = q8_hold1<DT>(f[i]);
 }
 
-// Largest finite magnitude among eight fp32 values.
-__device__ inline float q8_amax8(const float (&v)[8]) {
-  float a = 0.0f;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float m = __builtin_fabsf(v[i]);
-    a = __builtin_fmaxf(a, m <= 3.4028234663852886e38f ? m : 0.0f);  // false for inf and NaN
-  }
-  return a;
+// max(m, |a|, |b|), NaN left out
+__device__ inline float q8_max3(float m, float a, float b) {
+  float r;
+  asm("v_max3_f32 %0, %1, abs(%2), abs(%3)" : "=v"(r) : "v"(m), "v"(a), "v"(b));
+  return r;
 }
-// Maximum over each group of 16 lanes.
+// Largest magnitude among eight values, NaN left out; infinite if one is.
+__device__ inline float q8_amax8(const float (&v)[8]) {
+  return q8_max3(q8_max3(q8_max3(q8_max3(0.0f, v[0], v[1]), v[2], v[3]), v[4], v[5]), v[6], v[7]);
+}
+// Maximum over each group of 16 lanes, of numbers >= 0 (whose bits order as they do).
 __device__ inline float q8_max16(float a) {
+  int x = __builtin_bit_cast(int, a);
+  x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x128, 0xf, 0xf, false));  // row_ror:8
+  x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x124, 0xf, 0xf, false));
+  x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x122, 0xf, 0xf, false));
+  x = max(x, __builtin_amdgcn_update_dpp(0, x, 0x121, 0xf, 0xf, false));
+  return __builtin_bit_cast(float, x);
+}
+// Largest finite magnitude among the eight values of each of 16 lanes.
+__device__ inline float q8_block_amax(const float (&v)[8]) {
+  const float inf = __builtin_inff();
+  float a = q8_max16(q8_amax8(v));
+  if (__any(a == inf)) {  // rare: once more without the infinite ones
+    float m = 0.0f;
 #pragma unroll
-  for (int d = 1; d < 16; d <<= 1) a = __builtin_fmaxf(a, __shfl_xor(a, d, 64));
+    for (int i = 0; i < 8; ++i) {
+      const float x = __builtin_fabsf(v[i]);
+      m = x < inf && x > m ? x : m;
+    }
+    a = q8_max16(m);
+  }
   return a;
 }
 

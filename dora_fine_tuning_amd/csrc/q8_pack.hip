@@ -51,10 +51,10 @@ __global__ __launch_bounds__(256) void q8_pack_rows(const void* x, uint32_t rows
     const uint32_t t = b / nb, k = b - t * nb;
     float v[8];
     chunk_to_f32<DT>(c[u], v);
-    const uint32_t byte = q8_exp_byte(q8_max16(q8_amax8(v)));
+    const uint32_t byte = q8_exp_byte(q8_block_amax(v));
     if (b >= total) continue;
     *reinterpret_cast<uint2*>(q + static_cast<int64_t>(t) * qp + static_cast<int64_t>(k) * kQ8Block + lane * 8) =
-        q8_encode8(v, q8_inv_scale(byte));
+        q8_encode8(v, q8_scale(byte));
     uint8_t* er = e + static_cast<int64_t>(t) * ep;
     if (lane == 0) er[k] = static_cast<uint8_t>(byte);
     if (k == nb - 1 && lane > 0 && k + lane < ep) er[k + lane] = 127;  // the exponent row's padding
@@ -81,10 +81,10 @@ __global__ __launch_bounds__(256) void q8_pack_tile(const void* W, int64_t out, 
   for (int u = 0; u < 8; ++u) {
     float v[8];
     chunk_to_f32<DT>(c[u], v);
-    a = __builtin_fmaxf(a, q8_amax8(v));
+    a = __builtin_fmaxf(a, q8_block_amax(v));
   }
 #pragma unroll
-  for (int d = 1; d < 64; d <<= 1) a = __builtin_fmaxf(a, __shfl_xor(a, d, 64));
+  for (int d = 16; d < 64; d <<= 1) a = __builtin_fmaxf(a, __shfl_xor(a, d, 64));
   if ((threadIdx.x & 63) == 0) wmax[threadIdx.x >> 6] = a;
   __syncthreads();
   a = __builtin_fmaxf(__builtin_fmaxf(wmax[0], wmax[1]), __builtin_fmaxf(wmax[2], wmax[3]));
@@ -94,7 +94,7 @@ __global__ __launch_bounds__(256) void q8_pack_tile(const void* W, int64_t out, 
     const int64_t row = static_cast<int64_t>(ob) * kQ8Block + u * 16 + r0;
     float v[8];
     chunk_to_f32<DT>(c[u], v);
-    *reinterpret_cast<uint2*>(q + row * qp + col) = q8_encode8(v, q8_inv_scale(byte));
+    *reinterpret_cast<uint2*>(q + row * qp + col) = q8_encode8(v, q8_scale(byte));
   }
   uint8_t* er = e + static_cast<int64_t>(ob) * ep;
   if (threadIdx.x == 0) er[ib] = static_cast<uint8_t>(byte);

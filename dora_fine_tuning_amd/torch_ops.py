@@ -461,7 +461,29 @@ def _eager_q8_grad_a(dh, xq, xe, in_features):
     return (dh.float().t() @ _held(_values(xq, xe, in_features), dh.dtype).float()).to(dh.dtype)
 
 
-@torch.library.custom_op("dora_amd::q8_pack", mutates_args=(), device_types="cuda")
+# These operators are registered without the wrapper of a custom operator: they
+# have no autograd formula of their own (``q8_layer`` has) and run in serving
+# loops, where its layers cost as much as a launch.
+_Q8_LIB = torch.library.Library("dora_amd", "FRAGMENT")
+
+
+def _q8_kernel(name):
+    """Register a function as the GPU kernel of the operator ``name``, the eager
+    form of the same name as its CPU kernel; the operator takes its place."""
+
+    def register(fn):
+        schema = torch.library.infer_schema(fn, mutates_args=())
+        _Q8_LIB.define(name + schema)
+        _Q8_LIB.impl(name, fn, "CUDA")
+        _Q8_LIB.impl(name, globals()["_eager_" + name], "CPU")
+        op = getattr(torch.ops.dora_amd, name).default
+        op.__doc__ = fn.__doc__
+        return op
+
+    return register
+
+
+@_q8_kernel("q8_pack")
 def q8_pack(x: Tensor) -> tuple[Tensor, Tensor]:
     """(q, e): the rows of x [T x K] in 8-bit blocks of 128 columns."""
     if not _kernels_take(x):
@@ -469,13 +491,13 @@ def q8_pack(x: Tensor) -> tuple[Tensor, Tensor]:
     return binding.dora_q8_pack(x.contiguous())
 
 
-@q8_pack.register_fake
+@torch.library.register_fake("dora_amd::q8_pack")
 def _q8_pack_fake(x):
     qs, es = binding.q8_row_shapes(x.shape[0], x.shape[1])
     return x.new_empty(qs, dtype=_F8), x.new_empty(es, dtype=torch.uint8)
 
 
-@torch.library.custom_op("dora_amd::q8_pack_weight", mutates_args=(), device_types="cuda")
+@_q8_kernel("q8_pack_weight")
 def q8_pack_weight(W: Tensor) -> tuple[Tensor, Tensor]:
     """(q, e): a weight [out x in] in 8-bit blocks of 128 x 128 (once: it is frozen)."""
     if not _kernels_take(W):
@@ -483,13 +505,13 @@ def q8_pack_weight(W: Tensor) -> tuple[Tensor, Tensor]:
     return binding.dora_q8_pack_weight(W.contiguous())
 
 
-@q8_pack_weight.register_fake
+@torch.library.register_fake("dora_amd::q8_pack_weight")
 def _q8_pack_weight_fake(W):
     qs, es = binding.q8_weight_shapes(W.shape[0], W.shape[1])
     return W.new_empty(qs, dtype=_F8), W.new_empty(es, dtype=torch.uint8)
 
 
-@torch.library.custom_op("dora_amd::q8_unpack", mutates_args=(), device_types="cuda")
+@_q8_kernel("q8_unpack")
 def q8_unpack(q: Tensor, e: Tensor, cols: int, dtype: torch.dtype) -> Tensor:
     """The values that packed rows are held as, [T x cols] in dtype."""
     if dtype not in binding.DTYPE_CODE:
@@ -497,12 +519,12 @@ def q8_unpack(q: Tensor, e: Tensor, cols: int, dtype: torch.dtype) -> Tensor:
     return binding.dora_q8_unpack(q.contiguous(), e.contiguous(), q.shape[0], cols, dtype)
 
 
-@q8_unpack.register_fake
+@torch.library.register_fake("dora_amd::q8_unpack")
 def _q8_unpack_fake(q, e, cols, dtype):
     return q.new_empty((q.shape[0], cols), dtype=dtype)
 
 
-@torch.library.custom_op("dora_amd::q8_unpack_weight", mutates_args=(), device_types="cuda")
+@_q8_kernel("q8_unpack_weight")
 def q8_unpack_weight(q: Tensor, e: Tensor, rows: int, cols: int, dtype: torch.dtype) -> Tensor:
     """The values of the first ``rows`` rows of a packed weight, [rows x cols] in dtype."""
     if dtype not in binding.DTYPE_CODE:
@@ -510,12 +532,12 @@ def q8_unpack_weight(q: Tensor, e: Tensor, rows: int, cols: int, dtype: torch.dt
     return binding.dora_q8_unpack(q.contiguous(), e.contiguous(), rows, cols, dtype, weight=True)
 
 
-@q8_unpack_weight.register_fake
+@torch.library.register_fake("dora_amd::q8_unpack_weight")
 def _q8_unpack_weight_fake(q, e, rows, cols, dtype):
     return q.new_empty((rows, cols), dtype=dtype)
 
 
-@torch.library.custom_op("dora_amd::q8_linear", mutates_args=(), device_types="cuda")
+@_q8_kernel("q8_linear")
 def q8_linear(xq: Tensor, xe: Tensor, wq: Tensor, we: Tensor, out_features: int, dtype: torch.dtype) -> Tensor:
     """y [T x out] = x W^T from packed rows and a packed weight."""
     if dtype not in binding.DTYPE_CODE:
@@ -524,12 +546,12 @@ def q8_linear(xq: Tensor, xe: Tensor, wq: Tensor, we: Tensor, out_features: int,
                                       out_features, xq.shape[1], dtype)
 
 
-@q8_linear.register_fake
+@torch.library.register_fake("dora_amd::q8_linear")
 def _q8_linear_fake(xq, xe, wq, we, out_features, dtype):
     return xq.new_empty((xq.shape[0], out_features), dtype=dtype)
 
 
-@torch.library.custom_op("dora_amd::q8_linear_backward", mutates_args=(), device_types="cuda")
+@_q8_kernel("q8_linear_backward")
 def q8_linear_backward(gq: Tensor, ge: Tensor, wq: Tensor, we: Tensor, in_features: int,
                        dtype: torch.dtype) -> Tensor:
     """dx [T x in] = g W from packed rows g [T x out] and the same packed weight."""
@@ -539,7 +561,7 @@ def q8_linear_backward(gq: Tensor, ge: Tensor, wq: Tensor, we: Tensor, in_featur
                                       gq.shape[1], in_features, dtype)
 
 
-@q8_linear_backward.register_fake
+@torch.library.register_fake("dora_amd::q8_linear_backward")
 def _q8_linear_backward_fake(gq, ge, wq, we, in_features, dtype):
     return gq.new_empty((gq.shape[0], in_features), dtype=dtype)
 
@@ -549,7 +571,7 @@ def _q8_compose_args(dy, bq, be, h, B, mag, norm, s):
             mag.contiguous().float(), norm.contiguous().float(), s)
 
 
-@torch.library.custom_op("dora_amd::q8_lora_compose_backward", mutates_args=(), device_types="cuda")
+@_q8_kernel("q8_lora_compose_backward")
 def q8_lora_compose_backward(dy: Tensor, bq: Tensor, be: Tensor, h: Tensor, B: Tensor, mag: Tensor, norm: Tensor,
                              s: float, add_base: bool, want_base: bool) -> tuple[Tensor, Tensor, Tensor]:
     """``lora_compose_backward`` with the base from packed rows."""
@@ -560,13 +582,13 @@ def q8_lora_compose_backward(dy: Tensor, bq: Tensor, be: Tensor, h: Tensor, B: T
     return dy.new_empty((0,)) if d_base is None else d_base, d_B, d_mag
 
 
-@q8_lora_compose_backward.register_fake
+@torch.library.register_fake("dora_amd::q8_lora_compose_backward")
 def _q8_lora_compose_backward_fake(dy, bq, be, h, B, mag, norm, s, add_base, want_base):
     d_base = torch.empty_like(dy) if want_base else dy.new_empty((0,))
     return d_base, torch.empty_like(B), mag.new_empty(mag.shape)
 
 
-@torch.library.custom_op("dora_amd::q8_lora_compose_backward_packed", mutates_args=(), device_types="cuda")
+@_q8_kernel("q8_lora_compose_backward_packed")
 def q8_lora_compose_backward_packed(dy: Tensor, bq: Tensor, be: Tensor, h: Tensor, B: Tensor, mag: Tensor,
                                     norm: Tensor, s: float, add_base: bool) -> tuple[Tensor, Tensor, Tensor, Tensor]:
     """The same with d_base packed straight from fp32: (q, e, d_B, d_mag)."""
@@ -577,13 +599,13 @@ def q8_lora_compose_backward_packed(dy: Tensor, bq: Tensor, be: Tensor, h: Tenso
     return q, e, d_B, d_mag
 
 
-@q8_lora_compose_backward_packed.register_fake
+@torch.library.register_fake("dora_amd::q8_lora_compose_backward_packed")
 def _q8_lora_compose_backward_packed_fake(dy, bq, be, h, B, mag, norm, s, add_base):
     q, e = _q8_pack_fake(dy)
     return q, e, torch.empty_like(B), mag.new_empty(mag.shape)
 
 
-@torch.library.custom_op("dora_amd::q8_grad_a", mutates_args=(), device_types="cuda")
+@_q8_kernel("q8_grad_a")
 def q8_grad_a(dh: Tensor, xq: Tensor, xe: Tensor, in_features: int) -> Tensor:
     """d_A [r x in] = d_h^T x from packed rows x."""
     if not _kernels_take(dh):
@@ -591,7 +613,7 @@ def q8_grad_a(dh: Tensor, xq: Tensor, xe: Tensor, in_features: int) -> Tensor:
     return binding.dora_q8_grad_a(dh.contiguous(), xq.contiguous(), xe.contiguous(), in_features)
 
 
-@q8_grad_a.register_fake
+@torch.library.register_fake("dora_amd::q8_grad_a")
 def _q8_grad_a_fake(dh, xq, xe, in_features):
     return dh.new_empty((dh.shape[1], in_features))
 
@@ -695,15 +717,6 @@ def _q8_layer_grad(ctx, dy, *_):
 q8_layer.register_autograd(_q8_layer_grad, setup_context=_q8_layer_setup)
 
 
-q8_pack.register_kernel("cpu")(_eager_q8_pack)
-q8_pack_weight.register_kernel("cpu")(_eager_q8_pack_weight)
-q8_unpack.register_kernel("cpu")(_eager_q8_unpack)
-q8_unpack_weight.register_kernel("cpu")(_eager_q8_unpack_weight)
-q8_linear.register_kernel("cpu")(_eager_q8_linear)
-q8_linear_backward.register_kernel("cpu")(_eager_q8_linear_backward)
-q8_lora_compose_backward.register_kernel("cpu")(_eager_q8_lora_compose_backward)
-q8_lora_compose_backward_packed.register_kernel("cpu")(_eager_q8_lora_compose_backward_packed)
-q8_grad_a.register_kernel("cpu")(_eager_q8_grad_a)
 
 
 # -------------------------------------------------------------------------- layer
