@@ -166,6 +166,9 @@ int dora_q8_lora_compose_bwd(const void* dy, const void* bq, const void* be, con
   if (dq)
     if (int st = packed_ptrs(fn, "the packed d_base", dq, de)) return st;
   const dora::Q8BwdSizes sz = dora::q8_bwd_sizes(T, out, r, true);
+  if (sz.grid > INT32_MAX)
+    return fail(DORA_UNSUPPORTED, "%s: T=%lld out=%lld r=%lld: more workgroups than one launch holds", fn, (long long)T,
+                (long long)out, (long long)r);
   if (ws_bytes < sz.bytes) return fail(DORA_INVALID_ARG, "%s: workspace of %zu bytes, %zu needed", fn, ws_bytes, sz.bytes);
   if (sz.bytes > 0 && (!ws || !aligned16(ws)))
     return fail(DORA_INVALID_ARG, "%s: workspace is NULL or not 16-byte aligned", fn);
@@ -175,9 +178,6 @@ int dora_q8_lora_compose_bwd(const void* dy, const void* bq, const void* be, con
   const Range outs[6] = {{d_base, mat16(T, out)}, {dq, row_q(T, out)}, {de, row_e(T, out)},
                          {d_B, mat16(out, r)},    {d_mag, vb},         {ws, sz.bytes}};
   if (outputs_overlap(outs, ins)) return fail(DORA_INVALID_ARG, "%s: an output overlaps another argument", fn);
-  if (sz.grid > INT32_MAX || sz.slice_bytes >= (int64_t(1) << 31))
-    return fail(DORA_UNSUPPORTED, "%s: T=%lld out=%lld r=%lld: a token slice spans 2 GiB or more", fn, (long long)T,
-                (long long)out, (long long)r);
   const dora::Q8ComposeBwdArgs a{dy, bq, be, h, B, mag, norm, s, T, out, r, dtype, add_base ? 1 : 0,
                                  d_base, dq, de, d_B, d_mag, ws, stream};
   return hip_status(dora::launch_q8_compose_bwd(a), fn);
@@ -200,15 +200,15 @@ int dora_q8_grad_a(const void* dh, const void* xq, const void* xe, int64_t T, in
     if (int st = packed_ptrs(fn, "the packed x", xq, xe)) return st;
   }
   const dora::Q8BwdSizes sz = dora::q8_bwd_sizes(T, in, r, false);
+  if (sz.grid > INT32_MAX)
+    return fail(DORA_UNSUPPORTED, "%s: T=%lld in=%lld r=%lld: more workgroups than one launch holds", fn, (long long)T,
+                (long long)in, (long long)r);
   if (ws_bytes < sz.bytes) return fail(DORA_INVALID_ARG, "%s: workspace of %zu bytes, %zu needed", fn, ws_bytes, sz.bytes);
   if (sz.bytes > 0 && (!ws || !aligned16(ws)))
     return fail(DORA_INVALID_ARG, "%s: workspace is NULL or not 16-byte aligned", fn);
   const Range ins[3] = {{dh, mat16(T, r)}, {xq, row_q(T, in)}, {xe, row_e(T, in)}};
   const Range outs[2] = {{d_A, mat16(r, in)}, {ws, sz.bytes}};
   if (outputs_overlap(outs, ins)) return fail(DORA_INVALID_ARG, "%s: an output overlaps another argument", fn);
-  if (sz.grid > INT32_MAX || sz.slice_bytes >= (int64_t(1) << 31) || (r + 63) / 64 > 65535)
-    return fail(DORA_UNSUPPORTED, "%s: T=%lld in=%lld r=%lld: a token slice spans 2 GiB or more", fn, (long long)T,
-                (long long)in, (long long)r);
   const dora::Q8GradAArgs a{dh, xq, xe, T, in, r, dtype, d_A, ws, stream};
   return hip_status(dora::launch_q8_grad_a(a), fn);
 }

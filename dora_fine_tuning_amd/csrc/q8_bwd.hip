@@ -13,15 +13,26 @@
 //   q8_rows          one pass over X (and the base).  A workgroup owns 128
 //                    columns of X, one block of every row, x up to 384 columns
 //                    of Y x a slice of the tokens.  Stages of 32 tokens go
-//                    global -> LDS by DMA into a ring.  Four waves, one a SIMD,
-//                    each own 64 x 64 TNW of E: a wave reads the fragments of
-//                    the next half stage (16 tokens), transposed by the reads,
-//                    behind the matrix instructions of this one, and its other
-//                    work stands between them too: d_base, its packing and the
-//                    column sums, or the values of x from their bytes.  With
-//                    eight waves and the same work behind the products, a stage
-//                    took the sum of the two: 137 us at 8192^2, r = 384, packed,
-//                    and 73 us for the gradient of A;
+//                    global -> LDS by DMA into a ring.  Eight waves each own 64
+//                    x 32 TNW of E: a wave reads the fragments of the next half
+//                    stage (16 tokens), transposed by the reads, behind the
+//                    matrix instructions of this one, and its other work stands
+//                    between them too: d_base, its packing and the column sums;
+//                    or, for 8-bit X, the conversion of the next stage's panel
+//                    to 16 bits, once a value, into LDS.
+//
+// Measured at 8192^2 (whole calls, r = 384 / 128 / 16): compose, packed d_base
+// 121 / 76 / 68 us, 16-bit 127 / 85 / 80; gradient of A 89 / 41 / 31; and at 10240
+// x 27648, r = 512: 573, 580, 389.  What bounds it: at narrow r the bytes (r = 16
+// packed: 256 MiB of dy, base and d_base, 4.2 TB/s in the kernel); at wide r the
+// panel of Y, 24 KiB of DMA a stage into each CU for 4 KiB of the 8-bit X: the
+// return path is busy 63 % of the gradient's kernel, the matrix cores 28 %.
+// Measured and not kept (packed, 16-bit, gradient at r = 384): four waves of 64 x
+// 64 TNW, each converting its own fragments of X, 129 / 125 / 87 and 645 / 584 /
+// 388 at 10240 x 27648; two workgroups of four waves a CU with half the columns
+// of Y, 135 / 144 / -; a start of every workgroup at another stage, slower by 5 %
+// and more; the loads spread over both half stages, the same.
+//
 //   q8_bwd_finalize, q8_grad_a_finalize
 //                    the slices added in order, scaled or transposed, rounded;
 //   pad_rows         rows that are not multiples of 8 elements (out of dy, r of h,
@@ -52,22 +63,15 @@ __device__ inline void unrolled(F&& f) {
   unrolled(static_cast<F&&>(f), std::make_integer_sequence<int, N>{});
 }
 
-// Transposing LDS reads; in each group of 16 lanes a source lane L gives an
-// 8-byte address and result lane i receives column i.
-//   16 bits: four columns of row L/4, and result lane i the four rows of its column;
-//    8 bits: eight columns (half L%2 of 16) of row L/2, and the eight rows.
+// Transposing LDS reads: in each group of 16 lanes a source lane L gives the
+// 8-byte address of four columns of row L/4, and result lane i receives the four
+// rows of column i.
 // All LDS reads here are inline assembly (the compiler would wait for every DMA
 // in flight before each); their results are valid after lds_wait*().
 template <int OFF>
 __device__ inline u32x2 read_tr16(uint32_t addr) {
   u32x2 v;
   asm volatile("ds_read_b64_tr_b16 %0, %1 offset:%2" : "=v"(v) : "v"(addr), "n"(OFF) : "memory");
-  return v;
-}
-template <int OFF>
-__device__ inline u32x2 read_tr8(uint32_t addr) {
-  u32x2 v;
-  asm volatile("ds_read_b64_tr_b8 %0, %1 offset:%2" : "=v"(v) : "v"(addr), "n"(OFF) : "memory");
   return v;
 }
 template <int OFF>
@@ -86,27 +90,31 @@ __device__ inline uint32_t read4(uint32_t addr) {
 // Tile geometry.  LDS image of a stage's 16-bit panels (X = dy, Y): rows of
 // tokens, 256-byte groups of 16 chunks, logical 16-byte chunk c of row t in place
 // c ^ (4 * (t % 4)): the transposing reads touch 4 consecutive rows and 2 chunks
-// of each, and the 8 (row, chunk) pairs then fall in 8 distinct bank groups.  An
-// 8-bit X: rows of 128 bytes, chunk c of row t in place c ^ (2 * ((t/2) % 4)), for
-// 8 rows and 2 chunks.  The 8-bit base is read along its rows and lies plain.
+// of each, and the 8 (row, chunk) pairs then fall in 8 distinct bank groups.  The
+// 8-bit panels (the base, or X) are read along their rows and lie plain; an 8-bit X
+// is turned into a 16-bit panel of the same image, two of them behind the ring.
 template <int TNW_, bool GRAD_>
 struct RowsTile {
   static constexpr int TNW = TNW_;
   static constexpr bool GRAD = GRAD_;  // the gradient of A; else the compose's backward
-  static constexpr int WM = 2, WN = 2, NW = 4, NT = 256, TMW = 2;
+  static constexpr int WM = 2, WN = 4, NW = 8, NT = 512, TMW = 2;
   static constexpr int BM = 128, BN = 32 * TNW * WN, BK = 32;
-  static constexpr int XROWB = GRAD ? BM : 2 * BM, YROWB = 2 * BN;
-  static constexpr int X_BYTES = BK * XROWB, Y_BYTES = BK * YROWB, B_BYTES = GRAD ? 0 : BK * BM;
+  static constexpr int XROWB = 2 * BM, YROWB = 2 * BN;
+  static constexpr int P_BYTES = BK * XROWB, X_BYTES = GRAD ? P_BYTES / 2 : P_BYTES, Y_BYTES = BK * YROWB, B_BYTES = GRAD ? 0 : BK * BM;
   static constexpr int E_BYTES = 256;  // a dword with the block's exponent per token
   static constexpr int Y_OFF = X_BYTES, B_OFF = Y_OFF + Y_BYTES, E_OFF = B_OFF + B_BYTES;
-  static constexpr int SLOT_BYTES = (E_OFF + E_BYTES + 1023) / 1024 * 1024;
-  static constexpr int XQ = X_BYTES / 1024 / NW, YQ = Y_BYTES / 1024 / NW, BQ = B_BYTES / 1024 / NW;
+  static constexpr int SLOT_BYTES = E_OFF + E_BYTES;
+  // (an 8-bit panel is four instructions: waves 4 to 7 load what 0 to 3 do, so that
+  // every wave issues the same number)
+  static constexpr int XQ = 1, YQ = Y_BYTES / 1024 / NW, BQ = GRAD ? 0 : 1;
   static constexpr int L = XQ + YQ + BQ;  // DMA instructions a wave and stage (wave 0: and the exponents)
-  static constexpr int NSMAX = 160 * 1024 / SLOT_BYTES, NS = NSMAX < 6 ? NSMAX : 6;
-  static constexpr int LDS_BYTES = NS * SLOT_BYTES;
+  // 8-bit X: two 16-bit panels behind the ring, this stage's and the next one's
+  static constexpr int NSMAX = (160 * 1024 - (GRAD ? 2 * P_BYTES : 0)) / SLOT_BYTES, NS = NSMAX < 6 ? NSMAX : 6;
+  static constexpr int P_OFF = NS * SLOT_BYTES, LDS_BYTES = P_OFF + (GRAD ? 2 * P_BYTES : 0);
+  static constexpr int AHEAD = GRAD ? 2 : 1;  // slots that have landed at a stage's middle
   static constexpr int NM = TMW * TNW;  // matrix instructions of a half stage
-  static_assert(NS >= 3 && (NS - 2) * (L + 6) < 64, "ring depth and vmcnt range");
-  static_assert((16 + WN) * BM * 4 <= LDS_BYTES, "the epilogue's sums fit the ring");
+  static_assert(Y_BYTES % (1024 * NW) == 0 && NS >= 2 + AHEAD && (NS - 2) * (L + 3) < 64, "ring depth and vmcnt range");
+  static_assert((32 + WN) * BM * 4 <= LDS_BYTES, "the epilogue's sums fit the ring");
 };
 
 __device__ inline int slot16(int c, int t) { return (c & ~15) | ((c ^ (4 * (t & 3))) & 15); }
@@ -130,7 +138,7 @@ struct RowsArgs {
 };
 
 template <int DT, class TL>
-__global__ __launch_bounds__(TL::NT, 1) void q8_rows(RowsArgs a) {
+__global__ __launch_bounds__(TL::NT, 2) void q8_rows(RowsArgs a) {
   using V8 = typename Dt<DT>::V8;
   using T16 = typename Dt<DT>::T;
   __shared__ __attribute__((aligned(1024))) char smem[TL::LDS_BYTES];
@@ -161,11 +169,11 @@ __global__ __launch_bounds__(TL::NT, 1) void q8_rows(RowsArgs a) {
   // Per-lane DMA offsets (stage 0).  Instruction q of wave w moves 1 KiB block q*NW
   // + w of its panel, lane l writing bytes 16l .. 16l + 15.
   uint32_t xo[TL::XQ], yo[TL::YQ];
-  const int t8 = 8 * wave + (lane >> 3), c8 = lane & 7;  // an 8-bit panel's row and place
+  const int t8 = 8 * (wave & 3) + (lane >> 3), c8 = lane & 7;  // an 8-bit panel's row and place
 #pragma unroll
   for (int q = 0; q < TL::XQ; ++q) {
     if constexpr (TL::GRAD) {
-      xo[q] = static_cast<uint32_t>(t8 * a.qp + j0 + 16 * (c8 ^ (2 * ((t8 >> 1) & 3))));
+      xo[q] = static_cast<uint32_t>(t8 * a.qp + j0 + 16 * c8);
     } else {
       const int t = 4 * (q * TL::NW + wave) + (lane >> 4);
       const int64_t col = j0 + 8 * slot16(lane & 15, t);
@@ -190,11 +198,11 @@ __global__ __launch_bounds__(TL::NT, 1) void q8_rows(RowsArgs a) {
     constexpr int k = decltype(kk)::value;
     char* so = smem + slot * TL::SLOT_BYTES;
     if constexpr (k < TL::XQ)
-      dma16(rx, so + (k * TL::NW + wave) * 1024, at(xo[k], xstep, st));
+      dma16(rx, so + (TL::GRAD ? wave & 3 : wave) * 1024, at(xo[k], xstep, st));
     else if constexpr (k < TL::XQ + TL::YQ)
       dma16(ry, so + TL::Y_OFF + ((k - TL::XQ) * TL::NW + wave) * 1024, at(yo[k - TL::XQ], ystep, st));
     else
-      dma16(rb, so + TL::B_OFF + wave * 1024, bo + qstep * st);
+      dma16(rb, so + TL::B_OFF + (wave & 3) * 1024, bo + qstep * st);
   };
   auto issue_exp = [&](uint32_t st, int slot) {
     if (wave == 0)
@@ -219,14 +227,8 @@ __global__ __launch_bounds__(TL::NT, 1) void q8_rows(RowsArgs a) {
     ya[j] = addr16(TL::Y_OFF, TL::YROWB,
                    32 * (wn * TL::TNW + j) + 16 * ((L16 & 3) & 1) + 8 * (g & 1) + 4 * ((L16 & 3) >> 1));
 #pragma unroll
-  for (int i = 0; i < TL::TMW; ++i) {
-    if constexpr (TL::GRAD) {
-      const int row = 8 * half + (L16 >> 1), c = 2 * (wm * TL::TMW + i) + (g & 1);
-      xa[i] = lds0 + static_cast<uint32_t>(row * TL::XROWB + (c ^ (2 * ((row >> 1) & 3))) * 16 + (L16 & 1) * 8);
-    } else {
-      xa[i] = addr16(0, TL::XROWB, 32 * (wm * TL::TMW + i) + 16 * (g & 1) + 4 * (L16 & 3));
-    }
-  }
+  for (int i = 0; i < TL::TMW; ++i)
+    xa[i] = addr16(TL::GRAD ? TL::P_OFF : 0, TL::XROWB, 32 * (wm * TL::TMW + i) + 16 * (g & 1) + 4 * (L16 & 3));
 
   f32x16 acc[TL::TMW][TL::TNW];
 #pragma unroll
@@ -234,74 +236,33 @@ __global__ __launch_bounds__(TL::NT, 1) void q8_rows(RowsArgs a) {
 #pragma unroll
     for (int j = 0; j < TL::TNW; ++j) acc[i][j] = f32x16{};
 
-  // A half stage's fragments as read, and (8-bit X) its values once decoded.
-  struct Frag {
-    u32x2 y[TL::TNW][2];
-    u32x2 x[TL::TMW][2];  // 8-bit X: one read, eight tokens
-    u32x4 e[2];           // 8-bit X: the eight tokens' exponent dwords
-    V8 xv[TL::TMW];
+  struct Frag {  // a half stage's fragments
+    u32x2 y[TL::TNW][2], x[TL::TMW][2];
   };
-  constexpr int NX = TL::GRAD ? TL::TMW + 2 : 2 * TL::TMW;  // reads of X (first), then of Y
-  constexpr int NR = NX + 2 * TL::TNW;
-  auto read1 = [&](Frag& f, uint32_t so, auto ss, auto nn) {
+  constexpr int RX = 2 * TL::TMW, NR = RX + 2 * TL::TNW;  // reads of X, then of Y
+  auto read1 = [&](Frag& f, uint32_t xs, uint32_t ys, auto ss, auto nn) {
     constexpr int s = decltype(ss)::value, n = decltype(nn)::value;
-    if constexpr (n >= NX) {
-      constexpr int j = (n - NX) / 2, c = (n - NX) % 2;
-      f.y[j][c] = read_tr16<(16 * s + 4 * c) * TL::YROWB>(ya[j] + so);
-    } else if constexpr (!TL::GRAD) {
+    if constexpr (n < RX) {
       constexpr int i = n / 2, c = n % 2;
-      f.x[i][c] = read_tr16<(16 * s + 4 * c) * TL::XROWB>(xa[i] + so);
-    } else if constexpr (n < TL::TMW) {
-      f.x[n][0] = read_tr8<16 * s * TL::XROWB>(xa[n] + so);
+      f.x[i][c] = read_tr16<(16 * s + 4 * c) * TL::XROWB>(xa[i] + xs);
     } else {
-      constexpr int c = n - TL::TMW;
-      f.e[c] = lds_read16_at<TL::E_OFF + 64 * s + 16 * c>(lds0 + so + 32 * half);
+      constexpr int j = (n - RX) / 2, c = (n - RX) % 2;
+      f.y[j][c] = read_tr16<(16 * s + 4 * c) * TL::YROWB>(ya[j] + ys);
     }
   };
-  auto tie_y = [&](Frag& f) {
+  auto tie_all = [&](Frag& f) {
 #pragma unroll
-    for (int j = 0; j < TL::TNW; ++j)
+    for (int c = 0; c < 2; ++c) {
 #pragma unroll
-      for (int c = 0; c < 2; ++c) tie2(f.y[j][c]);
-  };
-  auto tie_x = [&](Frag& f) {
+      for (int j = 0; j < TL::TNW; ++j) tie2(f.y[j][c]);
 #pragma unroll
-    for (int i = 0; i < TL::TMW; ++i)
-#pragma unroll
-      for (int c = 0; c < (TL::GRAD ? 1 : 2); ++c) tie2(f.x[i][c]);
-    if constexpr (TL::GRAD) {
-      tie(f.e[0]);
-      tie(f.e[1]);
+      for (int i = 0; i < TL::TMW; ++i) tie2(f.x[i][c]);
     }
-  };
-  // x's values of fragment i: a lane holds eight tokens of one column
-  float sc[8];
-  bool top = false;  // a block of these tokens may hold values past the type's range
-  auto scales = [&](Frag& f) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const uint32_t byte = (f.e[k >> 2][k & 3] >> eshift) & 255u;
-      m = max(m, byte);
-      sc[k] = q8_scale(byte);
-    }
-    top = __any(m >= (DT == 0 ? 247u : 135u));  // 256 * 2^e past the type
-  };
-  auto decode = [&](Frag& f, int i) {
-    float x[8];
-    q8_decode8(uint2{f.x[i][0][0], f.x[i][0][1]}, 1.0f, x);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) x[k] *= sc[k];
-    if (top) q8_hold<DT>(x);
-    f.xv[i] = __builtin_bit_cast(V8, f32_to_chunk<DT>(x));
   };
   auto mfma1 = [&](Frag& f, int i, int j) {
-    const V8 yv = __builtin_bit_cast(V8, u32x4{f.y[j][0][0], f.y[j][0][1], f.y[j][1][0], f.y[j][1][1]});
-    if constexpr (TL::GRAD)
-      acc[i][j] = Dt<DT>::mfma32(yv, f.xv[i], acc[i][j]);
-    else
-      acc[i][j] = Dt<DT>::mfma32(
-          yv, __builtin_bit_cast(V8, u32x4{f.x[i][0][0], f.x[i][0][1], f.x[i][1][0], f.x[i][1][1]}), acc[i][j]);
+    acc[i][j] = Dt<DT>::mfma32(
+        __builtin_bit_cast(V8, u32x4{f.y[j][0][0], f.y[j][0][1], f.y[j][1][0], f.y[j][1][1]}),
+        __builtin_bit_cast(V8, u32x4{f.x[i][0][0], f.x[i][0][1], f.x[i][1][0], f.x[i][1][1]}), acc[i][j]);
   };
   auto pin_acc = [&]() {
 #pragma unroll
@@ -311,7 +272,7 @@ __global__ __launch_bounds__(TL::NT, 1) void q8_rows(RowsArgs a) {
   };
 
   // ---- the elementwise part of the compose's backward: this thread takes chunk
-  // ec (8 columns) of token rows et and et + 16 of every stage
+  // ec (8 columns) of token row et of every stage
   const int et = tid >> 4, ec = tid & 15;
   const int64_t ecol = j0 + 8 * ec;
   float gb[8], colsum[8];
@@ -327,37 +288,51 @@ __global__ __launch_bounds__(TL::NT, 1) void q8_rows(RowsArgs a) {
   const __amdgpu_buffer_rsrc_t rdb = slice(elem ? a.d_base : nullptr, nx * 2),
                                rdq = slice(elem ? a.dq : nullptr, a.qp), rde = slice(elem ? a.de : nullptr, a.ep);
   const bool out16 = elem && a.d_base, outq = elem && a.dq, pair = a.ldx == nx;
-  const uint32_t ea = lds0 + static_cast<uint32_t>(et * TL::XROWB + slot16(ec, et) * 16);  // (et + 16: the same place)
+  const uint32_t ea = lds0 + static_cast<uint32_t>(et * TL::XROWB + slot16(ec, et) * 16);  // 
   const uint32_t ba = lds0 + static_cast<uint32_t>(TL::B_OFF + et * TL::BM + ec * 8);
   const uint32_t xa4 = lds0 + static_cast<uint32_t>(TL::E_OFF + et * 4);
-  u32x4 wd[2];
-  u32x2 wb[2];
-  uint32_t we[2];
+  u32x4 wd;
+  u32x2 wb;
+  uint32_t we;
   auto elem_read = [&](uint32_t so) {
-    wd[0] = lds_read16_at<0>(ea + so);
-    wd[1] = lds_read16_at<16 * TL::XROWB>(ea + so);
-    wb[0] = read8<0>(ba + so);
-    wb[1] = read8<16 * TL::BM>(ba + so);
-    we[0] = read4<0>(xa4 + so);
-    we[1] = read4<64>(xa4 + so);
+    wd = lds_read16_at<0>(ea + so);
+    wb = read8<0>(ba + so);
+    we = read4<0>(xa4 + so);
   };
   auto elem_tie = [&]() {
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      tie(wd[c]);
-      tie2(wb[c]);
-      asm volatile("" : "+v"(we[c]));
-    }
+    tie(wd);
+    tie2(wb);
+    asm volatile("" : "+v"(we));
   };
-  // one of six pieces of the work on row c, a few instructions each
+  // ---- 8-bit X: this thread turns chunk ec of token row et into 16 bits, a stage
+  // before its products: one pass a value instead of one in every wave along Y
+  const uint32_t ra = lds0 + static_cast<uint32_t>(et * TL::BM + ec * 8);
+  const uint32_t pa = lds0 + static_cast<uint32_t>(TL::P_OFF + et * TL::XROWB + slot16(ec, et) * 16);
+  auto conv_read = [&](uint32_t so) {
+    wb = read8<0>(ra + so);
+    we = read4<0>(xa4 + so);
+  };
+  auto conv_tie = [&]() {
+    tie2(wb);
+    asm volatile("" : "+v"(we));
+  };
+  auto conv = [&](uint32_t ps) {
+    const uint32_t byte = (we >> eshift) & 255u;
+    float f[8];
+    q8_decode8(uint2{wb[0], wb[1]}, q8_scale(byte), f);
+    if (__any(byte >= (DT == 0 ? 247u : 135u))) q8_hold<DT>(f);  // rare: 256 * 2^e is past the type
+    const u32x4 o = __builtin_bit_cast(u32x4, f32_to_chunk<DT>(f));
+    asm volatile("ds_write_b128 %0, %1" ::"v"(pa + ps), "v"(o) : "memory");
+  };
+  // one of its six pieces, a few instructions each
   float ed[8], eb[8];
   uint32_t ebyte = 127;
-  auto elem_piece = [&](uint32_t st, int c, int piece) {
-    const uint32_t t = st * TL::BK + static_cast<uint32_t>(et + 16 * c);
+  auto elem_piece = [&](uint32_t st, int piece) {
+    const uint32_t t = st * TL::BK + static_cast<uint32_t>(et);
     if (piece == 0) {
-      q8_decode8(uint2{wb[c][0], wb[c][1]}, q8_scale((we[c] >> eshift) & 255u), eb);
+      q8_decode8(uint2{wb[0], wb[1]}, q8_scale((we >> eshift) & 255u), eb);
     } else if (piece == 1) {
-      chunk_to_f32<DT>(__builtin_bit_cast(Chunk, wd[c]), ed);
+      chunk_to_f32<DT>(__builtin_bit_cast(Chunk, wd), ed);
     } else if (piece == 2) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) colsum[e] = __builtin_fmaf(ed[e], eb[e], colsum[e]);
@@ -396,40 +371,39 @@ __global__ __launch_bounds__(TL::NT, 1) void q8_rows(RowsArgs a) {
   // loads is outstanding: the loads of NS - 2 stages, and the stores of as many
   // (none is counted before there are so many; more stores than counted, as single
   // 16-bit ones, only make the wait longer).
-  const int nstore = (out16 ? 2 : 0) + (outq ? 4 : 0);
+  const int nstore = (out16 ? 1 : 0) + (outq ? 2 : 0);
   auto wait_next = [&](int st) {
-    constexpr int W = (TL::NS - 2) * TL::L, M = TL::NS - 2;
+    constexpr int M = TL::NS - 1 - TL::AHEAD, W = M * TL::L;
     const int n = st < M ? 0 : nstore;
     if (n == 0)
       wait_vmcnt<W>();
+    else if (n == 1)
+      wait_vmcnt<W + M>();
     else if (n == 2)
       wait_vmcnt<W + 2 * M>();
-    else if (n == 4)
-      wait_vmcnt<W + 4 * M>();
     else
-      wait_vmcnt<W + 6 * M>();
+      wait_vmcnt<W + 3 * M>();
   };
 
   using H0 = std::integral_constant<int, 0>;
   using H1 = std::integral_constant<int, 1>;
   constexpr int RA = (NR + TL::NM - 1) / TL::NM * 2, DA = (TL::L + TL::NM - 1) / TL::NM;
-  constexpr int PA = (12 + TL::NM - 1) / TL::NM;                     // elementwise pieces behind each instruction
-  constexpr int MX = (NX + RA - 1) / RA < TL::NM / 2 ? TL::NM / 2 : 0;  // 8-bit X: decoding starts behind it
-  constexpr int SENT = (MX + 1) * RA < NR ? (MX + 1) * RA : NR;      // reads sent by then
-  static_assert(!TL::GRAD || SENT - NX < 16, "lgkmcnt range");
+  constexpr int PA = (6 + TL::NM - 1) / TL::NM;  // elementwise pieces behind each instruction
 
   // Half a stage: the products of `cur` while the fragments `nxt` come in (half s
-  // of the slot at rd).  In the stage's second half its slot loads anew and the
-  // elementwise part, read in the first half, is worked on.
-  auto half_stage = [&](auto ss, Frag& cur, Frag& nxt, uint32_t rd, uint32_t st, int wr) {
+  // of X at rdx and of Y at rdy).  In the stage's second half its slot loads anew
+  // and the elementwise part, read in the first half, is worked on; the first half
+  // holds the conversion of the next stage's X, read in the second half before.
+  auto half_stage = [&](auto ss, Frag& cur, Frag& nxt, uint32_t rdx, uint32_t rdy, uint32_t st, int wr) {
     constexpr int s = decltype(ss)::value;
     unrolled<TL::NM>([&](auto mm) {
       constexpr int m = decltype(mm)::value;
       mfma1(cur, m / TL::TNW, m % TL::TNW);
       unrolled<RA>([&](auto rr) {
         constexpr int n = m * RA + decltype(rr)::value;
-        if constexpr (n < NR) read1(nxt, rd, ss, std::integral_constant<int, n>{});
+        if constexpr (n < NR) read1(nxt, rdx, rdy, ss, std::integral_constant<int, n>{});
       });
+      if constexpr (s == 1 && TL::GRAD && m == 0) conv(((st + 1) & 1) * TL::P_BYTES);
       if constexpr (s == 0) {
         unrolled<DA>([&](auto dd) {
           constexpr int k = m * DA + decltype(dd)::value;
@@ -438,30 +412,15 @@ __global__ __launch_bounds__(TL::NT, 1) void q8_rows(RowsArgs a) {
         if constexpr (!TL::GRAD) {
           if (elem) {
 #pragma unroll
-            for (int p = m * PA; p < (m + 1) * PA && p < 12; ++p) elem_piece(st, p / 6, p % 6);
+            for (int p = m * PA; p < (m + 1) * PA && p < 6; ++p) elem_piece(st, p);
           }
         }
       }
-      if constexpr (TL::GRAD && m == MX) {
-        lds_wait_keep<(SENT > NX ? SENT - NX : 0)>();
-        tie_x(nxt);
-        scales(nxt);
-      }
-      if constexpr (TL::GRAD && m > MX && m - MX - 1 < TL::TMW) decode(nxt, m - MX - 1);
       __builtin_amdgcn_sched_barrier(0);
     });
     pin_acc();
   };
-  auto end_half = [&](Frag& nxt) {
-    lds_wait();
-    tie_y(nxt);
-    if constexpr (!TL::GRAD) tie_x(nxt);
-    if constexpr (TL::GRAD) {
-#pragma unroll
-      for (int i = 0; i < TL::TMW; ++i)
-        if (TL::NM - 1 - MX <= i) decode(nxt, i);  // (a narrow tile has too few instructions for all)
-    }
-  };
+  auto next = [](int slot) { return slot + 1 == TL::NS ? 0 : slot + 1; };
 
   if (S > 0) {
 #pragma unroll
@@ -469,32 +428,40 @@ __global__ __launch_bounds__(TL::NT, 1) void q8_rows(RowsArgs a) {
       issue_exp(u, u);
       unrolled<TL::L>([&](auto kk) { issue1(u, u, kk); });
     }
-    wait_vmcnt<(TL::NS - 1) * TL::L>();
+    wait_vmcnt<(TL::NS - TL::AHEAD) * TL::L>();
     __builtin_amdgcn_s_barrier();
-    Frag f0, f1;
-    unrolled<NR>([&](auto nn) { read1(f0, 0u, H0{}, nn); });
-    lds_wait();
-    tie_x(f0);
-    tie_y(f0);
     if constexpr (TL::GRAD) {
-      scales(f0);
-#pragma unroll
-      for (int i = 0; i < TL::TMW; ++i) decode(f0, i);
+      conv_read(0u);
+      lds_wait();
+      conv_tie();
+      conv(0u);
+      conv_read(static_cast<uint32_t>(TL::SLOT_BYTES));
+      lds_wait();
+      conv_tie();
+      __builtin_amdgcn_s_barrier();
     }
+    Frag f0, f1;
+    unrolled<NR>([&](auto nn) { read1(f0, 0u, 0u, H0{}, nn); });
+    lds_wait();
+    tie_all(f0);
     int slot = 0;
     for (int st = 0; st < S; ++st) {
-      const int s1 = slot + 1 == TL::NS ? 0 : slot + 1;
-      const uint32_t so = static_cast<uint32_t>(slot * TL::SLOT_BYTES);
+      const int s1 = next(slot);
+      const uint32_t so = static_cast<uint32_t>(slot * TL::SLOT_BYTES), so1 = static_cast<uint32_t>(s1 * TL::SLOT_BYTES);
       if constexpr (!TL::GRAD) elem_read(so);
-      half_stage(H1{}, f0, f1, so, static_cast<uint32_t>(st), slot);
-      end_half(f1);
+      half_stage(H1{}, f0, f1, TL::GRAD ? (st & 1) * TL::P_BYTES : so, so, static_cast<uint32_t>(st), slot);
+      lds_wait();
+      tie_all(f1);
       if constexpr (!TL::GRAD) elem_tie();
       wait_next(st);
       __builtin_amdgcn_s_barrier();
       __builtin_amdgcn_sched_barrier(0);
       issue_exp(static_cast<uint32_t>(st + TL::NS), slot);
-      half_stage(H0{}, f1, f0, static_cast<uint32_t>(s1 * TL::SLOT_BYTES), static_cast<uint32_t>(st), slot);
-      end_half(f0);
+      if constexpr (TL::GRAD) conv_read(static_cast<uint32_t>(next(s1) * TL::SLOT_BYTES));
+      half_stage(H0{}, f1, f0, TL::GRAD ? ((st + 1) & 1) * TL::P_BYTES : so1, so1, static_cast<uint32_t>(st), slot);
+      lds_wait();
+      tie_all(f0);
+      if constexpr (TL::GRAD) conv_tie();
       slot = s1;
     }
     wait_vmcnt<0>();
@@ -502,7 +469,7 @@ __global__ __launch_bounds__(TL::NT, 1) void q8_rows(RowsArgs a) {
   __syncthreads();
 
   // ---- epilogue: E's slice, and with it s * sum_k B E and the column sums
-  float* red = reinterpret_cast<float*>(smem);  // [16][128] column sums, then [WN][128] sums of B E
+  float* red = reinterpret_cast<float*>(smem);  // [32][128] column sums, then [WN][128] sums of B E
   const T16* Bp = static_cast<const T16*>(a.B);
   const int fr = lane & 31;
   float* ep = a.e_part + static_cast<int64_t>(sp) * nx * r;
@@ -539,7 +506,7 @@ __global__ __launch_bounds__(TL::NT, 1) void q8_rows(RowsArgs a) {
     }
     if constexpr (!TL::GRAD) {
       bsum += __shfl_xor(bsum, 32, 64);
-      if (half == 0) red[16 * 128 + wn * 128 + jl] = bsum;
+      if (half == 0) red[32 * 128 + wn * 128 + jl] = bsum;
     }
   }
   if constexpr (!TL::GRAD) {
@@ -549,8 +516,8 @@ __global__ __launch_bounds__(TL::NT, 1) void q8_rows(RowsArgs a) {
     if (tid < TL::BM && j0 + tid < nx) {
       float cs = 0.0f;
       if (elem)
-        for (int t = 0; t < 16; ++t) cs += red[t * 128 + tid];
-      const float bs = red[16 * 128 + tid] + red[17 * 128 + tid];
+        for (int t = 0; t < 32; ++t) cs += red[t * 128 + tid];
+      const float bs = (red[32 * 128 + tid] + red[33 * 128 + tid]) + (red[34 * 128 + tid] + red[35 * 128 + tid]);
       a.col_part[(static_cast<int64_t>(sp) * nTl + nt) * nx + j0 + tid] = cs + a.s * bs;
     }
   }
@@ -655,7 +622,7 @@ struct RowsPlan {
   int tn = 1, nCB = 0, nTiles = 0, nSplit = 1;
   size_t off_col = 0, bytes = 0;
 };
-RowsPlan rows_plan(int64_t T, int64_t nx, int64_t r) {
+RowsPlan rows_plan(int64_t T, int64_t nx, int64_t r, int64_t row_bytes) {
   RowsPlan p;
   int64_t best = -1;
   for (int tn = 1; tn <= 3; ++tn) {
@@ -666,7 +633,8 @@ RowsPlan rows_plan(int64_t T, int64_t nx, int64_t r) {
   p.nTiles = static_cast<int>(q8_ceil(r, 128 * p.tn));
   const int64_t blocks = static_cast<int64_t>(p.nCB) * p.nTiles;
   int64_t split = std::min<int64_t>(q8_ceil(256, blocks), std::max<int64_t>(1, T / 256));
-  p.nSplit = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(split, 64)));
+  split = std::max<int64_t>(1, std::min<int64_t>(split, 64));
+  p.nSplit = static_cast<int>(std::max(split, q8_ceil(T, INT32_MAX / row_bytes)));
   p.off_col = al256(static_cast<size_t>(p.nSplit) * nx * r * 4);
   p.bytes = p.off_col + static_cast<size_t>(p.nSplit) * p.nTiles * nx * 4;
   return p;
@@ -686,7 +654,7 @@ Q8BwdPlan q8_bwd_plan(int64_t T, int64_t nx, int64_t r, bool compose) {
   p.xp = up8(nx);
   p.pad_x = compose && p.xp != nx;
   p.pad_r = p.rp != r;
-  p.tile = rows_plan(T, nx, p.rp);
+  p.tile = rows_plan(T, nx, p.rp, std::max(p.xp, p.rp) * 2);
   size_t at = al256(p.tile.bytes);
   p.off_dy = at;
   if (p.pad_x) at = al256(at + static_cast<size_t>(T) * p.xp * 2);
@@ -703,7 +671,7 @@ void launch_rows(const RowsArgs& a, int tn, int dtype, hipStream_t stream) {
   const int64_t total = static_cast<int64_t>(a.nCB) * a.nTiles * a.nSplit;
   const dim3 grid(static_cast<unsigned>(q8_ceil(total, 8) * 8));
   auto go = [&](auto dt, auto t) {
-    using TL = RowsTile<2 * decltype(t)::value, GRAD>;
+    using TL = RowsTile<decltype(t)::value, GRAD>;
     hipLaunchKernelGGL((q8_rows<decltype(dt)::value, TL>), grid, dim3(TL::NT), 0, stream, a);
   };
   auto by_tile = [&](auto dt) {
@@ -727,7 +695,6 @@ Q8BwdSizes q8_bwd_sizes(int64_t T, int64_t nx, int64_t r, bool compose) {
   Q8BwdSizes s;
   s.bytes = p.bytes;
   s.grid = std::max<int64_t>(static_cast<int64_t>(p.tile.nCB) * p.tile.nTiles * p.tile.nSplit + 8, q8_ceil(p.rp, 64));
-  s.slice_bytes = q8_ceil(T, p.tile.nSplit) * std::max(p.xp, p.rp) * 2;
   return s;
 }
 

@@ -154,9 +154,8 @@ struct Q8GradAArgs {
   hipStream_t stream;
 };
 struct Q8BwdSizes {
-  size_t bytes = 0;         // of the workspace
-  int64_t grid = 0;         // largest grid dimension, or a bound of it
-  int64_t slice_bytes = 0;  // largest byte range of a token slice
+  size_t bytes = 0;  // of the workspace
+  int64_t grid = 0;  // largest grid dimension, or a bound of it
 };
 // nx: columns contracted against (out of the compose's backward, in of A's).
 Q8BwdSizes q8_bwd_sizes(int64_t T, int64_t nx, int64_t r, bool compose);

@@ -87,7 +87,9 @@ extern "C" {
  *  - dora_lora_compose_bwd with a shape or pointers its fast path cannot take
  *    and T * r above 2^20 (its slow path runs T * r products in order in one
  *    thread per output column);
- *  - dora_compose_bwd_noalloc with sizes whose partials exceed its scratch.
+ *  - dora_compose_bwd_noalloc with sizes whose partials exceed its scratch;
+ *  - in the 8-bit operators (dora_q8_*), 2^31 rows or more, more than 2^22 - 128
+ *    columns, or a rank above 2^20.
  */
 enum dora_status {
   DORA_OK = 0,
@@ -405,8 +407,7 @@ DORA_API size_t dora_q8_lora_compose_bwd_workspace_bytes(int64_t T, int64_t out,
  * dy [T x out], h [T x r], B, d_B [out x r], d_base: device, dtype, 16-byte
  * aligned; any sizes (rows that are not multiples of 8 elements are copied into
  * the workspace first).  r == 0 is lora = 0.  out == 0 is a no-op; T == 0 gives
- * d_B = 0 and d_mag = 0 / norm.  r <= 2^20 and a token slice below 2 GiB, else
- * DORA_UNSUPPORTED.
+ * d_B = 0 and d_mag = 0 / norm.  r <= 2^20, else DORA_UNSUPPORTED.
  */
 DORA_API int dora_q8_lora_compose_bwd(const void* dy, const void* bq, const void* be, const void* h, const void* B,
                                       const float* mag, const float* norm, float s, int64_t T, int64_t out, int64_t r,
@@ -421,8 +422,8 @@ DORA_API size_t dora_q8_grad_a_workspace_bytes(int64_t T, int64_t in, int64_t r)
  * A^T, from x kept in packed rows [T x in] since the forward.  x enters the
  * products as dora_q8_unpack gives it in dtype, d_h [T x r] (device, dtype,
  * 16-byte aligned) as it is; fp32 sums, token slices added in a fixed order,
- * rounded once.  in == 0 or r == 0 is a no-op; T == 0 gives d_A = 0.  r <= 2^20
- * and a token slice below 2 GiB, else DORA_UNSUPPORTED.
+ * rounded once.  in == 0 or r == 0 is a no-op; T == 0 gives d_A = 0.  r <= 2^20,
+ * else DORA_UNSUPPORTED.
  */
 DORA_API int dora_q8_grad_a(const void* dh, const void* xq, const void* xe, int64_t T, int64_t in, int64_t r, int dtype,
                             void* d_A, void* ws, size_t ws_bytes, hipStream_t stream);

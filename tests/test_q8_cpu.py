@@ -294,7 +294,7 @@ def test_compose_bwd_refusals():
     _status(call(dq=FAR[1]), INVALID, "overlaps")
     _status(call(d_base=FAR[0]), INVALID, "overlaps")
     _status(call(d_mag=FAR[5]), INVALID, "overlaps")
-    _status(call(T=(1 << 31) - 1, out=4096, wsb=1 << 62), UNSUPPORTED, "token slice")
+    _status(call(T=(1 << 31) - 1, out=(1 << 22) - 128, wsb=1 << 62), UNSUPPORTED, "workgroups")
     assert LIB.dora_q8_lora_compose_bwd(*[None] * 7, 1.0, 8, 0, 8, 0, 0, *[None] * 6, 0, None) == OK
     assert LIB.dora_q8_lora_compose_bwd_workspace_bytes(8, 0, 8) == 0
 
@@ -314,7 +314,7 @@ def test_grad_a_refusals():
     _status(call(wsb=need - 1), INVALID, "workspace of")
     _status(call(ws=FAR[4] + 4), INVALID, "aligned")
     _status(call(dA=FAR[0] + 2), INVALID, "overlaps")
-    _status(call(T=(1 << 31) - 1, in_=8192, wsb=1 << 62), UNSUPPORTED, "token slice")
+    _status(call(T=(1 << 31) - 1, in_=(1 << 22) - 128, wsb=1 << 62), UNSUPPORTED, "workgroups")
     assert call(r=0, dh=None, dA=None) == OK and call(in_=0, xq=None) == OK
 
 

@@ -329,6 +329,32 @@ def test_grad_a_edges(b):
     assert list(torch.isnan(d_A).any(0).nonzero().flatten().cpu().numpy()) == [200]
 
 
+def test_compose_bwd_and_grad_a_past_32_bits(b):
+    """dy past 2^31 bytes: the token slices are cut so that each stays below.  Small
+    integers, so every sum is exact in any order."""
+    T, out, r = 33025, 32768, 8
+    gen = torch.Generator(device=DEV).manual_seed(3)
+    part = lambda n, w: torch.randint(-2, 3, (n, w), generator=gen, device=DEV).bfloat16()
+    dy, base, h, B = part(1000, out).repeat(34, 1)[:T].contiguous(), part(T, out), part(T, r), part(out, r)
+    n = torch.full((out,), 2.0, device=DEV)
+    bq, be = b.dora_q8_pack(base)
+    (q, e), d_B, d_mag = b.dora_q8_lora_compose_bwd(dy, bq, be, h, B, 2 * n, n, 0.5, True, packed=True)
+    E = torch.zeros(out, r, dtype=torch.float64, device=DEV)
+    P = torch.zeros(out, r, dtype=torch.float64, device=DEV)
+    cs = torch.zeros(out, dtype=torch.float64, device=DEV)
+    for t in range(0, T, 4096):
+        d, c, k = dy[t:t + 4096].float(), base[t:t + 4096].float(), h[t:t + 4096].float()
+        E += (d.t() @ k).double()
+        P += (c.t() @ k).double()
+        cs += (d * c).sum(0).double()
+    assert torch.equal(d_B, E.bfloat16())
+    assert torch.equal(d_mag, ((cs + 0.5 * (B.double() * E).sum(1)) / 2).float())
+    q1, e1 = b.dora_q8_pack((2 * dy[-100:].float()).bfloat16())
+    assert torch.equal(q[-100:].view(torch.uint8), q1.view(torch.uint8)) and torch.equal(e[-100:], e1)
+    del dy, base, q, e
+    assert torch.equal(b.dora_q8_grad_a(h, bq, be, out), P.t().bfloat16())
+
+
 # ------------------------------------------------------------------ calls as programs make them
 
 
