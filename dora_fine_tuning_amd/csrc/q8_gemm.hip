@@ -579,10 +579,11 @@ __global__ __launch_bounds__(TL::NT, 1) void q8_gemm_tile(GemmArgs a) {
         for (int j = 0; j < TL::TNW; ++j) {
           asm volatile("" : "+a"(acc[i][j]));  // one tile at a time leaves the accumulator registers
           if (part) {
+            if (static_cast<int64_t>(cu.rb) * TL::BM + (wm * TL::TMW + i) * 32 < a.T)
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-              p[((i * TL::TNW + j) * 4 + q) * 64] = f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1],
-                                                          acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+              for (int q = 0; q < 4; ++q)
+                p[((i * TL::TNW + j) * 4 + q) * 64] = f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1],
+                                                            acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
           } else {
             store_tile<DT>(ry, a.vec, i * 32 + er, a.N, c0 + j * 32, acc[i][j], eh);
           }
@@ -615,6 +616,11 @@ __global__ __launch_bounds__(256) void q8_gemm_join(GemmArgs a) {
   const int64_t tail = w / PT;
   const int sub = static_cast<int>(w % PT);
   const int wave = sub / (TL::TMW * TL::TNW), ij = sub % (TL::TMW * TL::TNW);
+  int rb, nt;
+  tile_of(static_cast<uint32_t>(a.whole + tail), a, rb, nt);
+  const int i = ij / TL::TNW, j = ij % TL::TNW, wm = wave / TL::WN, wn = wave % TL::WN;
+  const int64_t m = static_cast<int64_t>(rb) * TL::BM + (wm * TL::TMW + i) * 32;
+  if (m >= a.T) return;  // rows past the last: not written either
   const f32x4* p = reinterpret_cast<const f32x4*>(a.part) + (tail * PT + sub) * 256 + lane;
   f32x4 s[4];
 #pragma unroll
@@ -627,10 +633,6 @@ __global__ __launch_bounds__(256) void q8_gemm_join(GemmArgs a) {
   f32x16 acc;
 #pragma unroll
   for (int q = 0; q < 16; ++q) acc[q] = s[q / 4][q % 4];
-  int rb, nt;
-  tile_of(static_cast<uint32_t>(a.whole + tail), a, rb, nt);
-  const int i = ij / TL::TNW, j = ij % TL::TNW, wm = wave / TL::WN, wn = wave % TL::WN;
-  const int64_t m = static_cast<int64_t>(rb) * TL::BM + (wm * TL::TMW + i) * 32;
   store_tile<DT>(rows_of_y(a, m, 32), a.vec, static_cast<uint32_t>(lane & 31), a.N,
                  static_cast<int64_t>(nt) * TL::BN + (wn * TL::TNW + j) * 32, acc, lane >> 5);
 }
@@ -715,6 +717,10 @@ __global__ __launch_bounds__(256) void q8_gemm_zero(uint16_t* y, int64_t n) {
 template <bool TRANS>
 using BigTile = Q8Tile<2, 2, 4, 4, 2, TRANS>;  // 256 x 256
 template <bool TRANS>
+using TallTile = Q8Tile<2, 2, 4, 2, 3, TRANS>;  // 256 x 128
+template <bool TRANS>
+using HighTile = Q8Tile<2, 2, 3, 2, 3, TRANS>;  // 192 x 128
+template <bool TRANS>
 using MidTile = Q8Tile<2, 2, 2, 2, 4, TRANS>;  // 128 x 128
 template <bool TRANS>
 using LowTile = Q8Tile<1, 4, 2, 1, 6, TRANS>;  // 64 x 128, a deep ring: the weight's stream
@@ -727,7 +733,7 @@ constexpr int64_t kFewRows = 8;
 constexpr int64_t kLowRows = 64;
 
 struct GemmPlan {
-  enum Path { kFew, kBig, kMid, kLow } path = kBig;
+  enum Path { kLow, kMid, kHigh, kTall, kBig, kFew } path = kBig;
   int64_t N = 0;
   int S = 0, nSplit = 1;
   int64_t nRB = 0, nTiles = 0, whole = 0;
@@ -736,29 +742,41 @@ struct GemmPlan {
 };
 
 // Tiles of bm x bn: as many rounds of one whole tile a CU as there are, and the
-// rest in up to 16 ranges of stages each (at least four stages), whichever
-// number gives the shortest rounds; a split costs the tile's fp32 partials,
-// written and read, priced in stages.  Returns the cost in stages of one tile.
-double split_plan(GemmPlan& p, int64_t T, int64_t bm, int64_t bn, double cost_split) {
+// rest in up to 16 ranges of stages each (at least four stages), whichever number
+// is expected to be fastest.  Returns the expected microseconds: a stage of the
+// tile (14 % more where the reads transpose), 1.5 for the start and end of a
+// unit, and for a split 1.9 + 0.41 a range for the join's launch and sums and
+// 0.26 a MB of fp32 partials, written and read.
+double split_plan(GemmPlan& p, int64_t T, int64_t bm, int64_t bn, double stage_us) {
   p.nRB = q8_ceil(T, bm);
   p.nTiles = q8_ceil(p.N, bn);
   const int64_t tiles = p.nRB * p.nTiles;
   const int64_t rounds = tiles / kCUs, rest = tiles - rounds * kCUs;
   p.whole = rounds * kCUs;
   p.nSplit = 1;
+  const double unit_us = 1.5;
   double best = 0.0;
   if (rest > 0) {
-    best = p.S;
+    best = p.S * stage_us + unit_us;
+    // a tile's rows that exist are written, on the mean of the tiles
+    const double mb = static_cast<double>(rest) * bn * 4e-6 * static_cast<double>(T) / static_cast<double>(p.nRB);
     for (int s = 2; s <= 16 && p.S / s >= 4; ++s) {
-      const double c = static_cast<double>(q8_ceil(rest * s, kCUs)) * q8_ceil(p.S, s) + cost_split * s * rest / kCUs;
+      const double c =
+          static_cast<double>(q8_ceil(rest * s, kCUs)) * (static_cast<double>(q8_ceil(p.S, s)) * stage_us + unit_us) +
+          1.9 + 0.41 * s + 0.26 * mb * s;
       if (c < best) best = c, p.nSplit = s;
     }
   }
   p.grid = std::min<int64_t>(kCUs, q8_ceil(p.whole + rest * p.nSplit, 8) * 8);
   p.bytes = p.nSplit > 1 ? static_cast<size_t>(rest) * p.nSplit * bm * bn * 4 : 0;
-  return static_cast<double>(rounds) * p.S + best;
+  return static_cast<double>(rounds) * (p.S * stage_us + unit_us) + best;
 }
 
+// The tile is the one expected to be fastest.  The times of a stage are fitted to
+// 375 calls (five weights from 1024 x 8192 to 27648 x 5120, both directions, 16 to
+// 8192 rows, 1 to 16 ranges); over them the plan's call takes 0.9 % more than the
+// fastest measured one on the mean, 11 % at most; tiles of 128 and 256 rows alone
+// took 4.8 %, 37 % at most (27648 x 5120, 256 rows: 64 us, 48 with 256 x 128).
 GemmPlan gemm_plan(int64_t T, int64_t out, int64_t in, bool trans) {
   GemmPlan p;
   p.N = trans ? in : out;
@@ -768,17 +786,25 @@ GemmPlan gemm_plan(int64_t T, int64_t out, int64_t in, bool trans) {
     p.grid = q8_ceil(p.N, 16);
     return p;
   }
-  if (T <= kLowRows) {
-    p.path = GemmPlan::kLow;
-    split_plan(p, T, 64, 128, 4.0);
-    return p;
+  static constexpr struct {
+    GemmPlan::Path path;
+    int64_t bm, bn;
+    double us;
+  } tiles[] = {{GemmPlan::kLow, 64, 128, 0.50},
+               {GemmPlan::kMid, 128, 128, 0.55},
+               {GemmPlan::kHigh, 192, 128, 0.70},
+               {GemmPlan::kTall, 256, 128, 0.87},
+               {GemmPlan::kBig, 256, 256, 1.45}};
+  GemmPlan best;
+  double least = 0.0;
+  for (const auto& t : tiles) {
+    if ((t.path == GemmPlan::kLow) != (T <= kLowRows)) continue;
+    GemmPlan q = p;
+    q.path = t.path;
+    const double us = split_plan(q, T, t.bm, t.bn, trans ? 1.14 * t.us : t.us);
+    if (least == 0.0 || us < least) least = us, best = q;
   }
-  GemmPlan big = p, mid = p;
-  const double cb = split_plan(big, T, 256, 256, 20.0), cm = split_plan(mid, T, 128, 128, 16.0);
-  // a stage of the small tile costs 0.4 of the large one's
-  if (cb <= 0.4 * cm) return big;
-  mid.path = GemmPlan::kMid;
-  return mid;
+  return best;
 }
 
 template <int DT, class TL>
@@ -798,14 +824,20 @@ void launch_few(const GemmArgs& g, const GemmPlan& p, hipStream_t stream) {
 
 template <int DT>
 void launch_typed(const GemmArgs& g, const GemmPlan& p, bool trans, hipStream_t stream) {
-  if (p.path == GemmPlan::kFew)
-    launch_few<DT>(g, p, stream);
-  else if (p.path == GemmPlan::kLow)
-    trans ? launch_tile<DT, LowTile<true>>(g, p, stream) : launch_tile<DT, LowTile<false>>(g, p, stream);
-  else if (p.path == GemmPlan::kBig)
-    trans ? launch_tile<DT, BigTile<true>>(g, p, stream) : launch_tile<DT, BigTile<false>>(g, p, stream);
-  else
-    trans ? launch_tile<DT, MidTile<true>>(g, p, stream) : launch_tile<DT, MidTile<false>>(g, p, stream);
+  switch (p.path) {
+    case GemmPlan::kFew:
+      return launch_few<DT>(g, p, stream);
+    case GemmPlan::kLow:
+      return trans ? launch_tile<DT, LowTile<true>>(g, p, stream) : launch_tile<DT, LowTile<false>>(g, p, stream);
+    case GemmPlan::kMid:
+      return trans ? launch_tile<DT, MidTile<true>>(g, p, stream) : launch_tile<DT, MidTile<false>>(g, p, stream);
+    case GemmPlan::kHigh:
+      return trans ? launch_tile<DT, HighTile<true>>(g, p, stream) : launch_tile<DT, HighTile<false>>(g, p, stream);
+    case GemmPlan::kTall:
+      return trans ? launch_tile<DT, TallTile<true>>(g, p, stream) : launch_tile<DT, TallTile<false>>(g, p, stream);
+    case GemmPlan::kBig:
+      return trans ? launch_tile<DT, BigTile<true>>(g, p, stream) : launch_tile<DT, BigTile<false>>(g, p, stream);
+  }
 }
 
 }  // namespace

@@ -175,6 +175,15 @@ def test_linear_large_tiles(b, shape, trans):
 
 
 @pytest.mark.parametrize("trans", [False, True])
+@pytest.mark.parametrize("shape", [(377, 16000, 520), (497, 16005, 520), (187, 5000, 8200), (203, 5500, 8200)])
+def test_linear_middling_rows(b, shape, trans):
+    """Tiles of 192 and of 256 rows by 128 columns, whole and split, in both directions."""
+    T, N, K = shape
+    f, args, ref, mass, K = product_case(b, *((T, K, N) if trans else shape), "bf16", trans, seed=5)
+    assert_product(f(*args), ref, mass, K, "bf16", (shape, trans))
+
+
+@pytest.mark.parametrize("trans", [False, True])
 def test_linear_extremes(b, trans):
     """Blocks of very different scales, zeros, and rows with NaN: a row's NaN stays in it."""
     T, out, in_ = 70, 384, 512
