@@ -106,9 +106,14 @@ struct Q8Tile {
   static constexpr int CPR = BN / 16;  // chunks per row of the backward's W panel
   static constexpr int NST = 2 * TMW * TNW;  // 16-byte stores of a wave's tile
   static constexpr int WAIT = (NS - 2) * L;  // DMA instructions younger than the slot waited for
+  // a slot's loads stand in the half stage after it is free, or (deeper rings) in
+  // that and the next one (8192^2 backward, 65 to 512 rows: 4 to 10 % less; forward
+  // 0 to 2 %)
+  static constexpr int LA = NS > 2 ? (L + 1) / 2 : L;
+  static constexpr int RELAX = NS > 2 ? NS - 2 : NS - 1;  // stages whose slot was loaded before a tile's stores
   static_assert(X_BYTES % (1024 * NW) == 0 && W_BYTES % (1024 * NW) == 0, "whole DMA instructions per wave");
   static_assert(NW % 2 == 0 && BM % 64 == 0 && BM / 64 <= NW, "panel swizzle and exponent DMA");
-  static_assert(BN == 128 || BN == 256, "the backward's panel rows");
+  static_assert(!TRANS || BN == 128 || BN == 256, "the backward's panel rows");
   static_assert(128 % (32 * TNW) == 0, "a wave's columns lie in one weight block");
   static_assert(NS >= 2 && NS < NE, "an exponent slot outlives the stages in flight");
   static_assert(WAIT + NST < 64, "vmcnt range");
@@ -470,10 +475,15 @@ __global__ __launch_bounds__(TL::NT, 1) void q8_gemm_tile(GemmArgs a) {
 #pragma unroll
   for (int s = 0; s < TL::NS; ++s) {
     issue_exp(ifirst);
-    unrolled<TL::L>([&](auto kk) { issue1(s, kk); });
-    issue_next();
+    constexpr int all = TL::L, part = TL::LA;
+    if (s + 1 < TL::NS || part == all) {
+      unrolled<all>([&](auto kk) { issue1(s, kk); });
+      issue_next();
+    } else {
+      unrolled<part>([&](auto kk) { issue1(s, kk); });
+    }
   }
-  wait_vmcnt<(TL::NS - 1) * TL::L>();
+  wait_vmcnt<(TL::NS - 2) * TL::L + TL::LA>();
   __builtin_amdgcn_s_barrier();
   Frag f0, f1;
   cg = 1;
@@ -509,7 +519,7 @@ __global__ __launch_bounds__(TL::NT, 1) void q8_gemm_tile(GemmArgs a) {
   // their latency.
   int slot = 0;
   int relax = 0;  // stages until the last tile's stores must be done
-  constexpr int RA = 2 * ((NR + NM - 1) / NM), DA = (TL::L + NM - 1) / NM;
+  constexpr int RA = 2 * ((NR + NM - 1) / NM);
   auto half_stage = [&](auto ss, Frag& cur, Frag& nxt, uint32_t rd, int wr) {
     unrolled<NM>([&](auto mm) {
       constexpr int m = decltype(mm)::value;
@@ -518,12 +528,13 @@ __global__ __launch_bounds__(TL::NT, 1) void q8_gemm_tile(GemmArgs a) {
         constexpr int n = m * RA + decltype(rr)::value;
         if constexpr (n < NR) read1(nxt, rd, ss, std::integral_constant<int, n>{});
       });
-      if constexpr (decltype(ss)::value == 0) {  // the stage's second half: its slot loads anew
-        unrolled<DA>([&](auto dd) {
-          constexpr int k = m * DA + decltype(dd)::value;
-          if constexpr (k < TL::L) issue1(wr, std::integral_constant<int, k>{});
-        });
-      }
+      // the stage's second half: its slot begins to load anew; first half: the rest
+      constexpr int k0 = decltype(ss)::value == 0 ? 0 : TL::LA, k1 = decltype(ss)::value == 0 ? TL::LA : TL::L;
+      constexpr int DA = (k1 - k0 + NM - 1) / NM;
+      unrolled<DA>([&](auto dd) {
+        constexpr int k = k0 + m * DA + decltype(dd)::value;
+        if constexpr (k < k1) issue1(wr, std::integral_constant<int, k>{});
+      });
       __builtin_amdgcn_sched_barrier(0);
     });
     pin_acc();
@@ -538,7 +549,8 @@ __global__ __launch_bounds__(TL::NT, 1) void q8_gemm_tile(GemmArgs a) {
     widx = last ? nwidx : widx + wexp_step;
     const uint32_t wn1 = wexp_load(widx);
 
-    half_stage(H1{}, f0, f1, rd0, slot);
+    half_stage(H1{}, f0, f1, rd0, slot == 0 ? TL::NS - 1 : slot - 1);
+    if constexpr (TL::LA < TL::L) issue_next();
     lds_wait();
     tie_all(f1);
     // this wave has read the slot; the next slot has landed; when that holds for
@@ -555,7 +567,7 @@ __global__ __launch_bounds__(TL::NT, 1) void q8_gemm_tile(GemmArgs a) {
     if (last || (nst & 3) == 0) cg = (cg + 1) & (TL::NE - 1);
     read_exp();
     half_stage(H0{}, f1, f0, rd1, slot);
-    issue_next();
+    if constexpr (TL::LA == TL::L) issue_next();
     lds_wait();
     tie_all(f0);
     if (last) {
@@ -590,7 +602,7 @@ __global__ __launch_bounds__(TL::NT, 1) void q8_gemm_tile(GemmArgs a) {
           clear(i, j);
         }
       if (!part && a.vec)
-        relax = TL::NS - 1;
+        relax = TL::RELAX;
       else
         wait_vmcnt<0>();
       if (!more) break;
@@ -724,16 +736,18 @@ template <bool TRANS>
 using MidTile = Q8Tile<2, 2, 2, 2, 4, TRANS>;  // 128 x 128
 template <bool TRANS>
 using LowTile = Q8Tile<1, 4, 2, 1, 6, TRANS>;  // 64 x 128, a deep ring: the weight's stream
+// forward alone (64 columns of the backward's weight rows are half cache lines)
+using SlimTile = Q8Tile<2, 2, 3, 1, 4, false>;   // 192 x 64
+using SmallTile = Q8Tile<2, 2, 1, 1, 7, false>;  // 64 x 64
 
 // Up to here the weight's stream decides and every wave reads the rows for
 // itself; beyond, 16 rows a wave cost as much as its 16 columns, and tiles of 64
 // rows share them.  27648 x 5120, us: 26 with 1 row; 42 with 16 rows here, 31 in
 // tiles.  8192^2: 16 with 1 row, 19 with 8, 22 with 16, 21.5 in tiles.
 constexpr int64_t kFewRows = 8;
-constexpr int64_t kLowRows = 64;
 
 struct GemmPlan {
-  enum Path { kLow, kMid, kHigh, kTall, kBig, kFew } path = kBig;
+  enum Path { kSmall, kSlim, kLow, kMid, kHigh, kTall, kBig, kFew } path = kBig;
   int64_t N = 0;
   int S = 0, nSplit = 1;
   int64_t nRB = 0, nTiles = 0, whole = 0;
@@ -744,9 +758,9 @@ struct GemmPlan {
 // Tiles of bm x bn: as many rounds of one whole tile a CU as there are, and the
 // rest in up to 16 ranges of stages each (at least four stages), whichever number
 // is expected to be fastest.  Returns the expected microseconds: a stage of the
-// tile (14 % more where the reads transpose), 1.5 for the start and end of a
-// unit, and for a split 1.9 + 0.41 a range for the join's launch and sums and
-// 0.26 a MB of fp32 partials, written and read.
+// tile (13 % more where the reads transpose), 1.4 for the start and end of a
+// unit, and for a split 3.0 + 0.43 a range for the join's launch and sums and
+// 0.25 a MB of fp32 partials, written and read.
 double split_plan(GemmPlan& p, int64_t T, int64_t bm, int64_t bn, double stage_us) {
   p.nRB = q8_ceil(T, bm);
   p.nTiles = q8_ceil(p.N, bn);
@@ -754,7 +768,7 @@ double split_plan(GemmPlan& p, int64_t T, int64_t bm, int64_t bn, double stage_u
   const int64_t rounds = tiles / kCUs, rest = tiles - rounds * kCUs;
   p.whole = rounds * kCUs;
   p.nSplit = 1;
-  const double unit_us = 1.5;
+  const double unit_us = 1.4;
   double best = 0.0;
   if (rest > 0) {
     best = p.S * stage_us + unit_us;
@@ -763,7 +777,7 @@ double split_plan(GemmPlan& p, int64_t T, int64_t bm, int64_t bn, double stage_u
     for (int s = 2; s <= 16 && p.S / s >= 4; ++s) {
       const double c =
           static_cast<double>(q8_ceil(rest * s, kCUs)) * (static_cast<double>(q8_ceil(p.S, s)) * stage_us + unit_us) +
-          1.9 + 0.41 * s + 0.26 * mb * s;
+          3.0 + 0.43 * s + 0.25 * mb * s;
       if (c < best) best = c, p.nSplit = s;
     }
   }
@@ -772,11 +786,13 @@ double split_plan(GemmPlan& p, int64_t T, int64_t bm, int64_t bn, double stage_u
   return static_cast<double>(rounds) * (p.S * stage_us + unit_us) + best;
 }
 
-// The tile is the one expected to be fastest.  The times of a stage are fitted to
-// 375 calls (five weights from 1024 x 8192 to 27648 x 5120, both directions, 16 to
-// 8192 rows, 1 to 16 ranges); over them the plan's call takes 0.9 % more than the
-// fastest measured one on the mean, 11 % at most; tiles of 128 and 256 rows alone
-// took 4.8 %, 37 % at most (27648 x 5120, 256 rows: 64 us, 48 with 256 x 128).
+// The tile is the one expected to be fastest.  The times are fitted to 5257 calls
+// (six weights from 1024 x 8192 to 27648 x 5120, both directions, 9 to 8192 rows,
+// every tile, 1 to 16 ranges); over them the plan's call takes 0.8 % more than the
+// fastest measured one on the mean, 12 % at most.  Tiles of 64 rows for up to 64
+// rows and of 128 and 256 beyond took 4.8 %, 37 % at most.  us, the chosen tile and
+// those: 27648 x 5120 with 256 rows 48 / 64, 8192^2 with 300 rows 32 / 37, 4096^2
+// with 256 rows 15 / 19.
 GemmPlan gemm_plan(int64_t T, int64_t out, int64_t in, bool trans) {
   GemmPlan p;
   p.N = trans ? in : out;
@@ -790,18 +806,20 @@ GemmPlan gemm_plan(int64_t T, int64_t out, int64_t in, bool trans) {
     GemmPlan::Path path;
     int64_t bm, bn;
     double us;
-  } tiles[] = {{GemmPlan::kLow, 64, 128, 0.50},
+  } tiles[] = {{GemmPlan::kSmall, 64, 64, 0.31},
+               {GemmPlan::kSlim, 192, 64, 0.46},
+               {GemmPlan::kLow, 64, 128, 0.41},
                {GemmPlan::kMid, 128, 128, 0.55},
-               {GemmPlan::kHigh, 192, 128, 0.70},
-               {GemmPlan::kTall, 256, 128, 0.87},
-               {GemmPlan::kBig, 256, 256, 1.45}};
+               {GemmPlan::kHigh, 192, 128, 0.69},
+               {GemmPlan::kTall, 256, 128, 0.85},
+               {GemmPlan::kBig, 256, 256, 1.40}};
   GemmPlan best;
   double least = 0.0;
   for (const auto& t : tiles) {
-    if ((t.path == GemmPlan::kLow) != (T <= kLowRows)) continue;
+    if (trans && t.bn < 128) continue;
     GemmPlan q = p;
     q.path = t.path;
-    const double us = split_plan(q, T, t.bm, t.bn, trans ? 1.14 * t.us : t.us);
+    const double us = split_plan(q, T, t.bm, t.bn, trans ? 1.13 * t.us : t.us);
     if (least == 0.0 || us < least) least = us, best = q;
   }
   return best;
@@ -827,6 +845,10 @@ void launch_typed(const GemmArgs& g, const GemmPlan& p, bool trans, hipStream_t 
   switch (p.path) {
     case GemmPlan::kFew:
       return launch_few<DT>(g, p, stream);
+    case GemmPlan::kSmall:
+      return launch_tile<DT, SmallTile>(g, p, stream);
+    case GemmPlan::kSlim:
+      return launch_tile<DT, SlimTile>(g, p, stream);
     case GemmPlan::kLow:
       return trans ? launch_tile<DT, LowTile<true>>(g, p, stream) : launch_tile<DT, LowTile<false>>(g, p, stream);
     case GemmPlan::kMid:

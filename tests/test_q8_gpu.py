@@ -175,12 +175,36 @@ def test_linear_large_tiles(b, shape, trans):
 
 
 @pytest.mark.parametrize("trans", [False, True])
-@pytest.mark.parametrize("shape", [(377, 16000, 520), (497, 16005, 520), (187, 5000, 8200), (203, 5500, 8200)])
+@pytest.mark.parametrize("shape", [(377, 16000, 520), (497, 16005, 520), (187, 5000, 8200), (203, 5500, 8200),
+                                   (777, 3333, 520), (65, 5000, 8200), (65, 3333, 4104), (777, 2500, 520),
+                                   (390, 2500, 520), (1000, 1000, 520), (2050, 8000, 520)])
 def test_linear_middling_rows(b, shape, trans):
-    """Tiles of 192 and of 256 rows by 128 columns, whole and split, in both directions."""
+    """Every height and width of tile, whole, split, and more tiles than CUs, in both directions."""
     T, N, K = shape
     f, args, ref, mass, K = product_case(b, *((T, K, N) if trans else shape), "bf16", trans, seed=5)
     assert_product(f(*args), ref, mass, K, "bf16", (shape, trans))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("trans", [False, True])
+@pytest.mark.parametrize("shape", [(512, 5120, 27648), (2100, 5120, 5120), (1500, 8192, 8192), (300, 8192, 8192)])
+def test_linear_sizes_of_models(b, shape, trans, dtype):
+    """Whole layers, against 64-bit products on the card of the values the packed operands hold."""
+    T, N, K = shape
+    out, in_ = (K, N) if trans else (N, K)
+    gen = torch.Generator(device=DEV).manual_seed(11)
+    W = torch.randn(out, in_, generator=gen, device=DEV) * 0.02
+    x = torch.randn(T, K, generator=gen, device=DEV) * torch.exp2(torch.randn(T, 1, generator=gen, device=DEV))
+    Wp, xp = b.dora_q8_pack_weight(W.to(DT[dtype])), b.dora_q8_pack(x.to(DT[dtype]))
+    y = (b.dora_q8_linear_bwd if trans else b.dora_q8_linear_fwd)(*xp, *Wp, out, in_, DT[dtype]).double()
+    # bf16 holds every unpacked value exactly
+    M = b.dora_q8_unpack(*Wp, out, in_, torch.bfloat16, weight=True).double()
+    M = M if trans else M.t().contiguous()
+    X = b.dora_q8_unpack(*xp, T, K, torch.bfloat16).double()
+    ref = X @ M
+    tol = HALF[dtype] * (1 + 2.0**-10) * ref.abs() + SUB[dtype] + K * 2.0**-23 * (X.abs() @ M.abs())
+    tol += 7 * 2.0**-13 * (X.abs().view(T, K // 8, 8).amax(2) @ M.abs().view(K // 8, 8, N).amax(1))
+    assert torch.all((y - ref).abs() <= tol)
 
 
 @pytest.mark.parametrize("trans", [False, True])
