@@ -396,10 +396,10 @@ def _padded_exponents(e: Tensor) -> Tensor:
 
 def _eager_q8_pack(x):
     T, K = x.shape
-    v = F.pad(x.float(), (0, _round_up(K, 128) - K)).reshape(T, -1, 128)
-    if v.numel() == 0:
+    if x.numel() == 0:
         (qs, es) = binding.q8_row_shapes(T, K)
         return x.new_empty(qs, dtype=_F8), x.new_empty(es, dtype=torch.uint8)
+    v = F.pad(x.float(), (0, _round_up(K, 128) - K)).reshape(T, -1, 128)
     q, e = _eager_blocks(v, (2,))
     return q.reshape(T, -1), _padded_exponents(e[:, :, 0])
 
@@ -463,19 +463,43 @@ def _eager_q8_grad_a(dh, xq, xe, in_features):
 
 # These operators are registered without the wrapper of a custom operator: they
 # have no autograd formula of their own (``q8_layer`` has) and run in serving
-# loops, where its layers cost as much as a launch.
+# loops, where its layers cost as much as a launch.  Arguments that require a
+# gradient are refused: none would come back through them.
 _Q8_LIB = torch.library.Library("dora_amd", "FRAGMENT")
 
 
 def _q8_kernel(name):
     """Register a function as the GPU kernel of the operator ``name``, the eager
-    form of the same name as its CPU kernel; the operator takes its place."""
+    form of the same name as its CPU kernel (and for a call the library refuses
+    with DORA_UNSUPPORTED); the operator takes its place."""
 
     def register(fn):
+        eager = globals()["_eager_" + name]
+
+        def no_grad(args):
+            if any(isinstance(a, Tensor) and a.requires_grad for a in args):
+                raise RuntimeError(f"{name} has no gradient of its own: pass detached tensors, or use q8_layer")
+
+        def on_gpu(*args):
+            if torch.is_grad_enabled():
+                no_grad(args)
+            try:
+                return fn(*args)
+            except binding.DoraError as e:
+                if not _unsupported(e):
+                    raise
+                return eager(*args)
+
+        def on_cpu(*args):
+            if torch.is_grad_enabled():
+                no_grad(args)
+            return eager(*args)
+
         schema = torch.library.infer_schema(fn, mutates_args=())
         _Q8_LIB.define(name + schema)
-        _Q8_LIB.impl(name, fn, "CUDA")
-        _Q8_LIB.impl(name, globals()["_eager_" + name], "CPU")
+        _Q8_LIB.impl(name, on_gpu, "CUDA")
+        _Q8_LIB.impl(name, on_cpu, "CPU")
+        _Q8_LIB.impl(name, torch.library.fallthrough_kernel, "Autograd")
         op = getattr(torch.ops.dora_amd, name).default
         op.__doc__ = fn.__doc__
         return op
@@ -668,7 +692,7 @@ q8_weight_norm.register_autograd(_q8_norm_grad, setup_context=_q8_norm_setup)
 def q8_layer(x: Tensor, A: Tensor, B: Tensor, mag: Tensor, norm: Tensor, weight: Tensor, we: Optional[Tensor],
              s: float) -> tuple[Tensor, Tensor, Tensor, Tensor, Tensor, Tensor]:
     """The layer on x [T x in] with 8-bit checkpoints: (y, then what the backward
-    reads: x and base packed, and h).  ``weight`` is W0 [out x in] in 16 bits, or,
+    reads, itself without a gradient: x and base packed, and h).  ``weight`` is W0 [out x in] in 16 bits, or,
     with its exponents ``we``, packed: then both products with W0 run on packed
     operands, x's being the checkpoint itself."""
     xq, xe = q8_pack(x)
@@ -687,6 +711,8 @@ def _q8_layer_fake(x, A, B, mag, norm, weight, we, s):
 
 def _q8_layer_setup(ctx, inputs, output):
     x, A, B, mag, norm, weight, we, s = inputs
+    ctx.mark_non_differentiable(*output[1:])
+    ctx.set_materialize_grads(False)  # no zeros for the checkpoints
     ctx.save_for_backward(A, B, mag, norm, weight, we, *output[1:])
     ctx.s = s
 
@@ -715,8 +741,6 @@ def _q8_layer_grad(ctx, dy, *_):
 
 
 q8_layer.register_autograd(_q8_layer_grad, setup_context=_q8_layer_setup)
-
-
 
 
 # -------------------------------------------------------------------------- layer
@@ -764,6 +788,7 @@ class DoRALinear(torch.nn.Module):
         weight = weight.to(device=device, dtype=dtype).contiguous()
         if q8_weight:
             # bytes, so that a change of the module's dtype leaves them alone
+            weight = weight.detach()  # it may be another layer's parameter
             q, e = q8_pack_weight(weight)
             self.register_buffer("weight", None)
             self.register_buffer("weight_q", q.view(torch.uint8))

@@ -182,6 +182,59 @@ def test_eager_layer_gradients(kw):
     assert torch.equal(y0, layer(x).detach())
 
 
+def packed_operator_calls(device, dtype):
+    """Every 8-bit operator with the positions of its arguments that a gradient could reach."""
+    x, W = torch.randn(5, 200, device=device).to(dtype), torch.randn(140, 200, device=device).to(dtype)
+    dy, h, B = (torch.randn(*s, device=device).to(dtype) for s in ((5, 140), (5, 8), (140, 8)))
+    m, n = torch.rand(140, device=device) + 1, torch.rand(140, device=device) + 1
+    (xq, xe), (wq, we), (bq, be) = F.q8_pack(x), F.q8_pack_weight(W), F.q8_pack(dy)
+    return [(F.q8_pack, (x,), (0,)), (F.q8_pack_weight, (W,), (0,)), (F.q8_unpack, (xq, xe, 200, dtype), (0,)),
+            (F.q8_unpack_weight, (wq, we, 140, 200, dtype), (0,)),
+            (F.q8_linear, (xq, xe, wq, we, 140, dtype), (0, 2)),
+            (F.q8_linear_backward, (bq, be, wq, we, 200, dtype), (0, 2)),
+            (F.q8_lora_compose_backward, (dy, bq, be, h, B, m, n, 1.0, True, True), (0, 1, 3, 4, 5, 6)),
+            (F.q8_lora_compose_backward_packed, (dy, bq, be, h, B, m, n, 1.0, True), (0, 1, 3, 4, 5, 6)),
+            (F.q8_grad_a, (h, xq, xe, 200), (0, 1))]
+
+
+def check_gradients_are_refused(device, dtype):
+    for op, args, where in packed_operator_calls(device, dtype):
+        op(*args)
+        for i in where:
+            with_grad = [a.detach().requires_grad_() if j == i else a for j, a in enumerate(args)]
+            with pytest.raises(RuntimeError, match="no gradient of its own"):
+                op(*with_grad)
+            with torch.no_grad():
+                out = op(*with_grad)
+            assert not any(t.requires_grad for t in (out if isinstance(out, tuple) else (out,)))
+
+
+def test_packed_operators_refuse_gradients():
+    check_gradients_are_refused("cpu", torch.float32)
+
+
+def check_layer_outputs(device, dtype):
+    """Of q8_layer's outputs y alone has a gradient, and a second backward is refused."""
+    layer, x, dy = layer_case(dtype, device, 6, 200, 150, 8, q8_weight=True)
+    x.requires_grad_()
+    wq, we = layer._packed_weight()
+    y, *kept = F.q8_layer(x, layer.lora_A, layer.lora_B, layer.magnitude, layer.weight_norm(), wq, we, layer.s)
+    assert y.requires_grad and not any(t.requires_grad for t in kept)
+    with pytest.raises(RuntimeError, match="no gradient of its own"):
+        torch.autograd.grad(y, x, dy.requires_grad_(), create_graph=True)
+
+
+def test_layer_outputs():
+    check_layer_outputs(None, torch.float32)
+
+
+def test_layer_takes_another_layers_parameter():
+    lin = torch.nn.Linear(200, 150, bias=False)
+    layer = F.DoRALinear(200, 150, 8, dtype=torch.float32, weight=lin.weight, q8_weight=True)
+    assert not layer.weight_q.requires_grad and not layer.magnitude.grad_fn
+    assert F.DoRALinear(200, 150, 8, q8_weight=True)(torch.randn(0, 200).bfloat16()).shape == (0, 150)
+
+
 def test_layer_holds_the_weight_in_bytes():
     layer = F.DoRALinear(200, 150, 8, dtype=torch.bfloat16, q8_weight=True)
     assert layer.weight is None and layer.weight_q.dtype == torch.uint8 and layer.weight_q.shape == (256, 256)

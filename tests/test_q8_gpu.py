@@ -25,7 +25,7 @@ import torch
 from oracle import dora_oracle as O
 from oracle import q8_oracle as Q
 from parity_util import assert_compose, assert_dmag
-from test_q8_cpu import check_layer, layer_case, special_rows
+from test_q8_cpu import check_gradients_are_refused, check_layer, check_layer_outputs, layer_case, special_rows
 
 pytestmark = pytest.mark.gpu
 DEV = torch.device("cuda:0")
@@ -542,6 +542,54 @@ def test_strides_and_offsets(F):
     odd_dy = torch.empty(70 * 640 + 1, dtype=torch.bfloat16, device=DEV)[1:].view(70, 640)
     odd_dy.copy_(dy)
     assert same(step(F, x, odd_dy, W, odd, B, m, n), step(F, x, dy, W, h, B, m, n))
+
+
+def test_gradients_are_refused():
+    check_gradients_are_refused(DEV, torch.bfloat16)
+    check_layer_outputs(DEV, torch.bfloat16)
+
+
+def test_sizes_the_library_refuses_run_eager(F, b):
+    """Rows past 2^22 columns: the library's refusal goes to the eager form."""
+    K = (1 << 22) + 100
+    x = torch.randn(2, K, device=DEV).bfloat16()
+    with pytest.raises(b.DoraError):
+        b.dora_q8_pack(x)
+    q, e = F.q8_pack(x)
+    rq, re_ = b.dora_q8_pack(x[:, -1124:].contiguous())  # 1124 = 8 blocks and the tail of 100
+    assert torch.equal(q[:, -1152:].view(torch.uint8), rq.view(torch.uint8))
+    assert torch.equal(e[:, K // 128 - 8:K // 128 + 1], re_[:, :9])
+    y = F.q8_unpack(q, e, K, torch.bfloat16)
+    assert y.shape == x.shape and torch.all((y - x).abs() <= 2.0**-4 * x.abs() + 2.0**-9)
+
+
+@pytest.mark.parametrize("T,o,i,r", [(0, 4, 5, 2), (3, 0, 5, 2), (3, 4, 0, 2), (3, 4, 5, 0), (1, 1, 1, 1)])
+def test_empty_and_single_sizes_through_the_operators(F, T, o, i, r):
+    torch.manual_seed(T + o)
+    dt, s = torch.bfloat16, 1.5
+    x, W, dy, h, B = (torch.randn(*n).to(dt) for n in ((T, i), (o, i), (T, o), (T, r), (o, r)))
+    m = torch.rand(o) + 1
+
+    def run(dev):
+        a = [t.to(dev) for t in (x, W, dy, h, B, m, m + 0.5)]
+        (xq, xe), (wq, we), (bq, be) = F.q8_pack(a[0]), F.q8_pack_weight(a[1]), F.q8_pack(a[2])
+        return [F.q8_unpack(xq, xe, i, dt), F.q8_unpack_weight(wq, we, o, i, dt), F.q8_linear(xq, xe, wq, we, o, dt),
+                F.q8_linear_backward(bq, be, wq, we, i, dt),
+                *F.q8_lora_compose_backward(a[2], bq, be, *a[3:], s, True, True),
+                *[t.view(torch.uint8) for t in F.q8_lora_compose_backward_packed(a[2], bq, be, *a[3:], s, False)[:2]],
+                F.q8_grad_a(a[3], xq, xe, i)]
+
+    for g, c in zip(run(DEV), run("cpu")):
+        assert g.shape == c.shape and g.dtype == c.dtype
+        torch.testing.assert_close(g.cpu().float(), c.float(), rtol=2.0**-7, atol=2.0**-10)
+
+
+def test_layer_without_tokens(F):
+    for kw in (dict(q8_weight=True), dict(q8_checkpoint=True)):
+        layer = F.DoRALinear(200, 136, 8, device=DEV, **kw)
+        y = layer(torch.zeros(0, 200, dtype=torch.bfloat16, device=DEV, requires_grad=True))
+        y.sum().backward()
+        assert y.shape == (0, 136) and torch.all(layer.lora_A.grad == 0) and torch.all(layer.magnitude.grad == 0)
 
 
 def test_opcheck(F):
