@@ -35,7 +35,17 @@
  * and, for the cached base norm the page lists as future work (W0 is frozen):
  *
  *   dora_row_sqnorm            ||W0_i||^2 per row, computed once;
- *   dora_norm_factored_cached  the weight norm with that cache as its base term.
+ *   dora_norm_factored_cached  the weight norm with that cache as its base term;
+ *
+ * and, for the layer's frozen side in 8 bits (W0, and what the backward needs of
+ * the activations):
+ *
+ *   dora_q8_pack, dora_q8_pack_weight, dora_q8_unpack
+ *                              blocks of 128 of e4m3 with a power-of-two scale;
+ *   dora_q8_linear_fwd, dora_q8_linear_bwd
+ *                              x W0^T and g W0 on packed operands;
+ *   dora_q8_lora_compose_bwd   dora_lora_compose_bwd from a packed base;
+ *   dora_q8_grad_a             d_A from packed x.
  *
  * Conventions shared by every entry point
  *  - Matrices are row-major and contiguous.  W0 is [out x in], A is [r x in],
