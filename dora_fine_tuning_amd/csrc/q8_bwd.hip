@@ -29,9 +29,9 @@
 // return path is busy 63 % of the gradient's kernel, the matrix cores 28 %.
 // Measured and not kept (packed, 16-bit, gradient at r = 384): four waves of 64 x
 // 64 TNW, each converting its own fragments of X, 129 / 125 / 87 and 645 / 584 /
-// 388 at 10240 x 27648; two workgroups of four waves a CU with half the columns
-// of Y, 135 / 144 / -; a start of every workgroup at another stage, slower by 5 %
-// and more; the loads spread over both half stages, the same.
+// 388 at 10240 x 27648; at r = 128 two workgroups a CU, with twice the token
+// slices, 92 / 105 / 45 against 75 / 85 / 40; a start of every workgroup at another
+// stage, slower by 5 % and more; the loads spread over both half stages, the same.
 //
 //   q8_bwd_finalize, q8_grad_a_finalize
 //                    the slices added in order, scaled or transposed, rounded;

@@ -477,8 +477,9 @@ def _q8_kernel(name):
         eager = globals()["_eager_" + name]
 
         def no_grad(args):
-            if any(isinstance(a, Tensor) and a.requires_grad for a in args):
-                raise RuntimeError(f"{name} has no gradient of its own: pass detached tensors, or use q8_layer")
+            for a in args:
+                if isinstance(a, Tensor) and a.requires_grad:
+                    raise RuntimeError(f"{name} has no gradient of its own: pass detached tensors, or use q8_layer")
 
         def on_gpu(*args):
             if torch.is_grad_enabled():
