@@ -73,13 +73,25 @@ __device__ inline void q8_hold(float (&f)[8]) {
   for (int i = 0; i < 8; ++i) f[i] = q8_hold1<DT>(f[i]);
 }
 
-// max(m, |a|, |b|), NaN left out
+// A maximum leaves out a quiet NaN, but gives a signaling one, quieted, in place
+// of the other operands, and the next maximum then drops it with all that was
+// gathered before.  Arithmetic results and values converted from fp16 are quiet;
+// bf16 reaches fp32 by a shift, with the bits that memory holds.  (Packing 10240 x
+// 27648 takes 149 us with and without; 8192^2 out of the caches 31.5 and 30.8.)
+template <int DT>
+__device__ inline void q8_quiet(float (&v)[8]) {
+  if constexpr (DT == 0) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __builtin_canonicalizef(v[i]);
+  }
+}
+// max(m, |a|, |b|), quiet NaN left out
 __device__ inline float q8_max3(float m, float a, float b) {
   float r;
   asm("v_max3_f32 %0, %1, abs(%2), abs(%3)" : "=v"(r) : "v"(m), "v"(a), "v"(b));
   return r;
 }
-// Largest magnitude among eight values, NaN left out; infinite if one is.
+// Largest magnitude among eight values (no signaling NaN), NaN left out; infinite if one is.
 __device__ inline float q8_amax8(const float (&v)[8]) {
   return q8_max3(q8_max3(q8_max3(q8_max3(0.0f, v[0], v[1]), v[2], v[3]), v[4], v[5]), v[6], v[7]);
 }

@@ -51,6 +51,7 @@ __global__ __launch_bounds__(256) void q8_pack_rows(const void* x, uint32_t rows
     const uint32_t t = b / nb, k = b - t * nb;
     float v[8];
     chunk_to_f32<DT>(c[u], v);
+    q8_quiet<DT>(v);
     const uint32_t byte = q8_exp_byte(q8_block_amax(v));
     if (b >= total) continue;
     *reinterpret_cast<uint2*>(q + static_cast<int64_t>(t) * qp + static_cast<int64_t>(k) * kQ8Block + lane * 8) =
@@ -81,6 +82,7 @@ __global__ __launch_bounds__(256) void q8_pack_tile(const void* W, int64_t out, 
   for (int u = 0; u < 8; ++u) {
     float v[8];
     chunk_to_f32<DT>(c[u], v);
+    q8_quiet<DT>(v);
     a = __builtin_fmaxf(a, q8_block_amax(v));
   }
 #pragma unroll
@@ -94,6 +96,7 @@ __global__ __launch_bounds__(256) void q8_pack_tile(const void* W, int64_t out, 
     const int64_t row = static_cast<int64_t>(ob) * kQ8Block + u * 16 + r0;
     float v[8];
     chunk_to_f32<DT>(c[u], v);
+    q8_quiet<DT>(v);
     *reinterpret_cast<uint2*>(q + row * qp + col) = q8_encode8(v, q8_scale(byte));
   }
   uint8_t* er = e + static_cast<int64_t>(ob) * ep;
