@@ -62,6 +62,7 @@ from typing import Optional
 
 import numpy as np
 import torch
+import torch.autograd.forward_ad as fwad
 import torch.nn.functional as F
 
 from . import binding
@@ -464,8 +465,20 @@ def _eager_q8_grad_a(dh, xq, xe, in_features):
 # These operators are registered without the wrapper of a custom operator: they
 # have no autograd formula of their own (``q8_layer`` has) and run in serving
 # loops, where its layers cost as much as a launch.  Arguments that require a
-# gradient are refused: none would come back through them.
+# gradient, or carry a tangent, are refused: none would come back through them.
+# The refusal is the operators' Autograd kernel, which tracing and functorch run
+# as well as an eager call.
 _Q8_LIB = torch.library.Library("dora_amd", "FRAGMENT")
+_BELOW_AUTOGRAD = torch._C._after_autograd_keyset
+
+
+def _refuse_gradients(name, args):
+    grad, duals = torch.is_grad_enabled(), fwad._current_level >= 0
+    if grad or duals:
+        for a in args:
+            if isinstance(a, Tensor) and (grad and a.requires_grad
+                                          or duals and fwad.unpack_dual(a).tangent is not None):
+                raise RuntimeError(f"{name} has no gradient of its own: pass detached tensors, or use q8_layer")
 
 
 def _q8_kernel(name):
@@ -476,14 +489,7 @@ def _q8_kernel(name):
     def register(fn):
         eager = globals()["_eager_" + name]
 
-        def no_grad(args):
-            for a in args:
-                if isinstance(a, Tensor) and a.requires_grad:
-                    raise RuntimeError(f"{name} has no gradient of its own: pass detached tensors, or use q8_layer")
-
         def on_gpu(*args):
-            if torch.is_grad_enabled():
-                no_grad(args)
             try:
                 return fn(*args)
             except binding.DoraError as e:
@@ -491,16 +497,25 @@ def _q8_kernel(name):
                     raise
                 return eager(*args)
 
-        def on_cpu(*args):
-            if torch.is_grad_enabled():
-                no_grad(args)
-            return eager(*args)
+        kernels = {torch._C.DispatchKey.CUDA: on_gpu, torch._C.DispatchKey.CPU: eager}
+        direct = {}  # by a key set's bits: the device's kernel where nothing else is left of it, else None
+
+        def autograd(keyset, *args):
+            _refuse_gradients(name, args)
+            bits = keyset.raw_repr()
+            if bits not in direct:
+                direct[bits] = kernels.get((keyset & _BELOW_AUTOGRAD).highestPriorityTypeId())
+            kernel = direct[bits]
+            if kernel is not None:  # a second way through the dispatcher would cost 3 us
+                return kernel(*args)
+            with torch._C._AutoDispatchBelowAutograd():
+                return op.redispatch(keyset & _BELOW_AUTOGRAD, *args)
 
         schema = torch.library.infer_schema(fn, mutates_args=())
         _Q8_LIB.define(name + schema)
         _Q8_LIB.impl(name, on_gpu, "CUDA")
-        _Q8_LIB.impl(name, on_cpu, "CPU")
-        _Q8_LIB.impl(name, torch.library.fallthrough_kernel, "Autograd")
+        _Q8_LIB.impl(name, eager, "CPU")
+        _Q8_LIB.impl(name, autograd, "Autograd", with_keyset=True)
         op = getattr(torch.ops.dora_amd, name).default
         op.__doc__ = fn.__doc__
         return op
