@@ -57,6 +57,7 @@ On that path every operator is argument marshalling around the C ABI
 """
 from __future__ import annotations
 
+import functools
 import math
 from typing import Optional
 
@@ -373,6 +374,31 @@ lora_compose_backward.register_kernel("cpu")(_eager_lora_compose_backward)
 _F8 = torch.float8_e4m3fn
 
 
+_AUTOCAST_KEYS = torch._C.DispatchKeySet(torch._C.DispatchKey.AutocastCUDA) | torch._C.DispatchKeySet(
+    torch._C.DispatchKey.AutocastCPU)
+
+
+def _without_autocast(fn):
+    """fn with autocast off inside: its products keep the types they are given."""
+
+    @functools.wraps(fn)
+    def inner(*args):
+        with torch._C._ExcludeDispatchKeyGuard(_AUTOCAST_KEYS):
+            return fn(*args)
+
+    return inner
+
+
+def _autocast(*mats):
+    """The matrices in autocast's type where it is on for their device, as linear
+    takes them (64-bit and packed ones stay as they are)."""
+    kind = mats[0].device.type
+    if kind not in ("cuda", "cpu") or not torch.is_autocast_enabled(kind):
+        return mats
+    to, cast = torch.get_autocast_dtype(kind), (torch.float32, torch.float16, torch.bfloat16)
+    return tuple(t.to(to) if t.dtype in cast else t for t in mats)
+
+
 def _round_up(n: int, k: int) -> int:
     return -(-n // k) * k
 
@@ -438,19 +464,23 @@ def _eager_q8_unpack_weight(q, e, rows, cols, dtype):
     return _held(_values(q, e, cols, True)[:rows], dtype)
 
 
+@_without_autocast
 def _eager_q8_linear(xq, xe, wq, we, out_features, dtype):
     return (_values(xq, xe, xq.shape[1]) @ _values(wq, we, wq.shape[1], True)[:out_features].t()).to(dtype)
 
 
+@_without_autocast
 def _eager_q8_linear_backward(gq, ge, wq, we, in_features, dtype):
     return (_values(gq, ge, gq.shape[1]) @ _values(wq, we, in_features, True)).to(dtype)
 
 
+@_without_autocast
 def _eager_q8_lora_compose_backward(dy, bq, be, h, B, mag, norm, s, add_base, want_base):
     base = _values(bq, be, dy.shape[1])
     return _eager_lora_compose_backward(dy, base, h, B, mag, norm, s, add_base, want_base)
 
 
+@_without_autocast
 def _eager_q8_lora_compose_backward_packed(dy, bq, be, h, B, mag, norm, s, add_base):
     _, d_B, d_mag = _eager_q8_lora_compose_backward(dy, bq, be, h, B, mag, norm, s, add_base, False)
     g, gm1 = _scales(mag, norm)
@@ -458,6 +488,7 @@ def _eager_q8_lora_compose_backward_packed(dy, bq, be, h, B, mag, norm, s, add_b
     return q, e, d_B, d_mag
 
 
+@_without_autocast
 def _eager_q8_grad_a(dh, xq, xe, in_features):
     return (dh.float().t() @ _held(_values(xq, xe, in_features), dh.dtype).float()).to(dh.dtype)
 
@@ -672,6 +703,7 @@ def _slabs(wq, we, out, in_, dtype):
 
 
 @torch.library.custom_op("dora_amd::q8_weight_norm", mutates_args=())
+@_without_autocast
 def q8_weight_norm(wq: Tensor, we: Tensor, A: Tensor, B: Tensor, base_sq: Tensor, s: float) -> Tensor:
     """``weight_norm_cached`` of a packed weight."""
     n = torch.empty(B.shape[0], dtype=torch.float32, device=B.device)
@@ -759,6 +791,15 @@ def _q8_layer_grad(ctx, dy, *_):
 q8_layer.register_autograd(_q8_layer_grad, setup_context=_q8_layer_setup)
 
 
+def _q8_layer_autocast(x, A, B, mag, norm, weight, we, s):
+    x, A, B, weight = _autocast(x, A, B, weight)
+    return _without_autocast(q8_layer)(x, A, B, mag, norm, weight, we, s)
+
+
+for _key in ("AutocastCUDA", "AutocastCPU"):
+    _Q8_LIB.impl("q8_layer", _q8_layer_autocast, _key)
+
+
 # -------------------------------------------------------------------------- layer
 
 
@@ -786,7 +827,7 @@ class DoRALinear(torch.nn.Module):
     ``q8_weight`` (which implies it) also holds W0 itself in 8-bit blocks (the
     buffers ``weight_q``, ``weight_e``; ``weight`` is None) and runs both products
     with W0 on packed operands.  n is the norm of the values W0 is held as, so the
-    layer still starts out with g = 1.
+    layer still starts out with g = 1.  Under autocast both compute in its type.
     """
 
     def __init__(self, in_features: int, out_features: int, r: int, alpha: float = 32.0,
@@ -857,7 +898,10 @@ class DoRALinear(torch.nn.Module):
         if self.q8_checkpoint and torch.is_grad_enabled() and any(t.requires_grad for t in trained):
             y = q8_layer(x2, self.lora_A, self.lora_B, self.magnitude, n, weight, we, self.s)[0]
             return y.reshape(*lead, self.out_features)
-        if self.q8_weight:  # inference: x is packed for the product alone
+        B = self.lora_B
+        if self.q8_checkpoint:  # inference: the types of the training tier
+            x2, B = _autocast(x2, B)
+        if self.q8_weight:  # x is packed for the product alone
             base = q8_linear(*q8_pack(x2), weight, we, self.out_features, x2.dtype)
         else:
             base = F.linear(x2, weight)
@@ -865,5 +909,5 @@ class DoRALinear(torch.nn.Module):
         # lora = h B^T is formed inside the compose kernel on both tiers; on the
         # training tier autograd records it and its backward (lora_compose_backward)
         # never forms lora or d_lora either, so nothing T x out is saved for lora
-        y = lora_compose(base, h, self.lora_B, self.magnitude, n, self.s, True)
+        y = lora_compose(base, h, B, self.magnitude, n, self.s, True)
         return y.reshape(*lead, self.out_features)
