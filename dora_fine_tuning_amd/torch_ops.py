@@ -768,6 +768,8 @@ def _q8_layer_setup(ctx, inputs, output):
 def _q8_layer_grad(ctx, dy, *_):
     A, B, mag, norm, weight, we, xq, xe, bq, be, h = ctx.saved_tensors
     need, s, in_ = ctx.needs_input_grad, ctx.s, A.shape[1]
+    if dy is None:  # a later function gave no gradient: zeros, as autograd hands them to the 16-bit layer
+        dy = h.new_zeros((h.shape[0], B.shape[0]))
     dx = None
     if need[0] and we is not None:
         dq, de, d_B, d_mag = q8_lora_compose_backward_packed(dy, bq, be, h, B, mag, norm, s, True)
