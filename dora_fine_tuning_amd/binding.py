@@ -36,6 +36,7 @@ EXPORTS = (
     "dora_compose_bwd_noalloc",
     "dora_norm_bwd_workspace_bytes",
     "dora_norm_bwd",
+    "dora_norm_bwd_slab",
     "dora_q8_pack",
     "dora_q8_pack_weight",
     "dora_q8_unpack",
@@ -89,6 +90,8 @@ def _load() -> ctypes.CDLL:
     lib.dora_norm_bwd_workspace_bytes.restype = sz
     lib.dora_norm_bwd.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, f32, i32, vp, vp, vp, sz, vp]
     lib.dora_norm_bwd.restype = i32
+    lib.dora_norm_bwd_slab.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, f32, i32, i32, vp, vp, vp, sz, vp]
+    lib.dora_norm_bwd_slab.restype = i32
     lib.dora_q8_pack.argtypes = lib.dora_q8_pack_weight.argtypes = [vp, i64, i64, i32, vp, vp, vp]
     lib.dora_q8_pack.restype = lib.dora_q8_pack_weight.restype = i32
     lib.dora_q8_unpack.argtypes = [vp, vp, i64, i64, i32, i32, vp, vp]
@@ -377,6 +380,28 @@ def dora_norm_bwd(W0, A, B, norm, d_norm, s: float, d_A=None, d_B=None, workspac
                              _ptr(d_A), _ptr(d_B), _ptr(workspace), workspace.numel() * workspace.element_size(),
                              _stream(dev)))
     return d_A, d_B
+
+
+def dora_norm_bwd_slab(W0, A, B, norm, d_norm, s: float, d_A, add: bool):
+    """d_B of a slab of rows; its part of d_A [r x in] goes to the fp32 ``d_A``,
+    added to what that holds with ``add``."""
+    code = _code(W0)
+    out, in_ = W0.shape
+    r = A.shape[0]
+    dev = W0.device
+    _matrix(W0, "W0", (out, in_), W0.dtype, dev)
+    _matrix(A, "A", (r, in_), W0.dtype, dev)
+    _matrix(B, "B", (out, r), W0.dtype, dev)
+    _matrix(norm, "norm", (out,), torch.float32, dev)
+    _matrix(d_norm, "d_norm", (out,), torch.float32, dev)
+    _matrix(d_A, "d_A", (r, in_), torch.float32, dev)
+    d_B = torch.empty_like(B)
+    need = dora_norm_bwd_workspace_bytes(out, in_, r, W0.dtype)
+    workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+    _check(LIB.dora_norm_bwd_slab(_ptr(W0), _ptr(A), _ptr(B), _ptr(norm), _ptr(d_norm), out, in_, r, float(s), code,
+                                  int(bool(add)), _ptr(d_A), _ptr(d_B), _ptr(workspace), workspace.numel(),
+                                  _stream(dev)))
+    return d_B
 
 
 # ------------------------------------------------------------ the frozen side in 8 bits

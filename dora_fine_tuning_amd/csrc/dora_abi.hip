@@ -114,6 +114,47 @@ int compose_bwd_call(const char* fn, const void* dy, const void* base, const voi
   return hip_status(dora::launch_compose_bwd(a, vec), fn);
 }
 
+int norm_bwd_call(const char* fn, const void* W0, const void* A, const void* B, const float* norm, const float* d_norm,
+                  int64_t out, int64_t in, int64_t r, float s, int dtype, bool f32_A, bool add_A, void* d_A, void* d_B,
+                  void* ws, size_t ws_bytes, hipStream_t stream) {
+  if (!valid_dtype(dtype)) return fail(DORA_UNSUPPORTED, "%s: unknown dtype %d", fn, dtype);
+  if (out < 0 || in < 0 || r < 0)
+    return fail(DORA_INVALID_ARG, "%s: negative size (out=%lld in=%lld r=%lld)", fn, (long long)out, (long long)in,
+                (long long)r);
+  if (r == 0) return ok();
+  if (in > 0 && (!A || !d_A)) return fail(DORA_INVALID_ARG, "%s: A or d_A is NULL", fn);
+  if (out > 0 && (!B || !d_B || !norm || !d_norm)) return fail(DORA_INVALID_ARG, "%s: B, d_B, norm or d_norm is NULL", fn);
+  if (out > 0 && in > 0 && !W0) return fail(DORA_INVALID_ARG, "%s: W0 is NULL", fn);
+  const bool vec = in % 8 == 0 && r % 8 == 0 && in < (int64_t(1) << 21) && r <= (int64_t(1) << 20) &&
+                   aligned16(W0) && aligned16(A) && aligned16(B) && aligned16(d_A) && aligned16(d_B) &&
+                   aligned16(ws);
+  const dora::NormBwdPlan plan = dora::make_norm_bwd_plan(out, in, r, dtype, vec);
+  const size_t need = plan.bytes;
+  if (ws_bytes < need) return fail(DORA_INVALID_ARG, "%s: workspace of %zu bytes, %zu needed", fn, ws_bytes, need);
+  if (need > 0 && !ws) return fail(DORA_INVALID_ARG, "%s: workspace is NULL", fn);
+  const size_t e = 2, vb = static_cast<size_t>(out) * 4;
+  const void* ins[5] = {W0, A, B, norm, d_norm};
+  const size_t insz[5] = {out * in * e, r * in * e, out * r * e, vb, vb};
+  const void* outs[3] = {d_A, d_B, ws};
+  const size_t outsz[3] = {r * in * (f32_A ? 4 : e), out * r * e, need};
+  for (int o = 0; o < 3; ++o) {
+    for (int i = 0; i < 5; ++i)
+      if (any_overlap(outs[o], outsz[o], ins[i], insz[i]))
+        return fail(DORA_INVALID_ARG, "%s: an output or the workspace overlaps an input", fn);
+    for (int q = o + 1; q < 3; ++q)
+      if (any_overlap(outs[o], outsz[o], outs[q], outsz[q]))
+        return fail(DORA_INVALID_ARG, "%s: outputs or the workspace overlap", fn);
+  }
+  if (plan.max_grid > INT32_MAX)
+    return fail(DORA_UNSUPPORTED, "%s: out=%lld in=%lld r=%lld needs more workgroups than one launch holds", fn,
+                (long long)out, (long long)in, (long long)r);
+  if (plan.max_slice_bytes >= (int64_t(1) << 31))
+    return fail(DORA_UNSUPPORTED, "%s: out=%lld in=%lld r=%lld: a row slice spans 2 GiB or more", fn, (long long)out,
+                (long long)in, (long long)r);
+  dora::NormBwdArgs a{dtype, W0, A, B, norm, d_norm, s, d_A, d_B, ws, stream, f32_A, add_A};
+  return hip_status(dora::launch_norm_bwd(plan, a), fn);
+}
+
 }  // namespace
 
 extern "C" {
@@ -284,43 +325,15 @@ size_t dora_norm_bwd_workspace_bytes(int64_t out, int64_t in, int64_t r, int dty
 int dora_norm_bwd(const void* W0, const void* A, const void* B, const float* norm, const float* d_norm, int64_t out,
                   int64_t in, int64_t r, float s, int dtype, void* d_A, void* d_B, void* ws, size_t ws_bytes,
                   hipStream_t stream) {
-  const char* fn = "dora_norm_bwd";
-  if (!valid_dtype(dtype)) return fail(DORA_UNSUPPORTED, "%s: unknown dtype %d", fn, dtype);
-  if (out < 0 || in < 0 || r < 0)
-    return fail(DORA_INVALID_ARG, "%s: negative size (out=%lld in=%lld r=%lld)", fn, (long long)out, (long long)in,
-                (long long)r);
-  if (r == 0) return ok();
-  if (in > 0 && (!A || !d_A)) return fail(DORA_INVALID_ARG, "%s: A or d_A is NULL", fn);
-  if (out > 0 && (!B || !d_B || !norm || !d_norm)) return fail(DORA_INVALID_ARG, "%s: B, d_B, norm or d_norm is NULL", fn);
-  if (out > 0 && in > 0 && !W0) return fail(DORA_INVALID_ARG, "%s: W0 is NULL", fn);
-  const bool vec = in % 8 == 0 && r % 8 == 0 && in < (int64_t(1) << 21) && r <= (int64_t(1) << 20) &&
-                   aligned16(W0) && aligned16(A) && aligned16(B) && aligned16(d_A) && aligned16(d_B) &&
-                   aligned16(ws);
-  const dora::NormBwdPlan plan = dora::make_norm_bwd_plan(out, in, r, dtype, vec);
-  const size_t need = plan.bytes;
-  if (ws_bytes < need) return fail(DORA_INVALID_ARG, "%s: workspace of %zu bytes, %zu needed", fn, ws_bytes, need);
-  if (need > 0 && !ws) return fail(DORA_INVALID_ARG, "%s: workspace is NULL", fn);
-  const size_t e = 2, vb = static_cast<size_t>(out) * 4;
-  const void* ins[5] = {W0, A, B, norm, d_norm};
-  const size_t insz[5] = {out * in * e, r * in * e, out * r * e, vb, vb};
-  const void* outs[3] = {d_A, d_B, ws};
-  const size_t outsz[3] = {r * in * e, out * r * e, need};
-  for (int o = 0; o < 3; ++o) {
-    for (int i = 0; i < 5; ++i)
-      if (any_overlap(outs[o], outsz[o], ins[i], insz[i]))
-        return fail(DORA_INVALID_ARG, "%s: an output or the workspace overlaps an input", fn);
-    for (int q = o + 1; q < 3; ++q)
-      if (any_overlap(outs[o], outsz[o], outs[q], outsz[q]))
-        return fail(DORA_INVALID_ARG, "%s: outputs or the workspace overlap", fn);
-  }
-  if (plan.max_grid > INT32_MAX)
-    return fail(DORA_UNSUPPORTED, "%s: out=%lld in=%lld r=%lld needs more workgroups than one launch holds", fn,
-                (long long)out, (long long)in, (long long)r);
-  if (plan.max_slice_bytes >= (int64_t(1) << 31))
-    return fail(DORA_UNSUPPORTED, "%s: out=%lld in=%lld r=%lld: a row slice spans 2 GiB or more", fn, (long long)out,
-                (long long)in, (long long)r);
-  dora::NormBwdArgs a{dtype, W0, A, B, norm, d_norm, s, d_A, d_B, ws, stream};
-  return hip_status(dora::launch_norm_bwd(plan, a), fn);
+  return norm_bwd_call("dora_norm_bwd", W0, A, B, norm, d_norm, out, in, r, s, dtype, false, false, d_A, d_B, ws,
+                       ws_bytes, stream);
+}
+
+int dora_norm_bwd_slab(const void* W0, const void* A, const void* B, const float* norm, const float* d_norm,
+                       int64_t out, int64_t in, int64_t r, float s, int dtype, int add_A, float* d_A, void* d_B,
+                       void* ws, size_t ws_bytes, hipStream_t stream) {
+  return norm_bwd_call("dora_norm_bwd_slab", W0, A, B, norm, d_norm, out, in, r, s, dtype, true, add_A != 0, d_A, d_B,
+                       ws, ws_bytes, stream);
 }
 
 size_t dora_compose_bwd_workspace_bytes(int64_t T, int64_t out) {

@@ -27,7 +27,8 @@
 //                      once): the contraction axis [out rows of W0 ; r rows of
 //                      A] gives d_A^T in row slices;
 //   nbwd_finalize_a    sum of the slices, row j over sigma_j, transposed
-//                      through LDS into d_A [r x in].
+//                      through LDS into d_A [r x in], in the storage dtype or,
+//                      for a W0 in slabs of rows, added up in fp32.
 // The hi/lo pairs carry about 16 (bf16) or 22 (fp16) significant bits of the
 // computed operands Y and Z into the bf16/fp16 MFMAs; W0, A and B enter exactly.
 // Sizes or pointers the 16-byte path cannot take go to a general path of plain
@@ -204,15 +205,27 @@ __global__ __launch_bounds__(256) void nbwd_finalize_m(const float* E, int nSpli
   }
 }
 
+// One element of d_A: rounded to the storage dtype, or (F32, for a W0 that comes
+// in slabs of rows) kept in fp32 and added to the slabs before, so that the sum
+// over all rows is rounded once, by the caller.
+template <int DT, bool F32>
+__device__ inline void put_a(void* dA, int64_t at, float v, bool add) {
+  if constexpr (F32) {
+    float* p = static_cast<float*>(dA) + at;
+    *p = add ? *p + v : v;
+  } else {
+    static_cast<typename Dt<DT>::T*>(dA)[at] = Dt<DT>::from_f(v);
+  }
+}
+
 // d_A[j][k] = (sum over the slices of E[k][j]) / sigma_j (E [nParts][in][r],
 // the slices added in order; sigma_j a power of two), rounded once.
 // A 32 x 32 tile of (k, j) per workgroup: coalesced reads along j, a transpose
 // through LDS, coalesced writes along k.
-template <int DT>
+template <int DT, bool F32>
 __global__ __launch_bounds__(256) void nbwd_finalize_a(const float* E, int nParts, int64_t in, int64_t r,
-                                                       const float* sigma, void* dAv) {
+                                                       const float* sigma, void* dAv, bool add) {
   // sigma == nullptr: sigma_j = 1
-  using T = typename Dt<DT>::T;
   __shared__ float tile[32][33];
   const int64_t k0 = static_cast<int64_t>(blockIdx.x) * 32, j0 = static_cast<int64_t>(blockIdx.y) * 32;
   const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
@@ -254,29 +267,27 @@ __global__ __launch_bounds__(256) void nbwd_finalize_a(const float* E, int nPart
     }
   }
   __syncthreads();
-  T* dA = static_cast<T*>(dAv);
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     const int jj = ty + 8 * q;
     const int64_t j = j0 + jj, k = k0 + tx;
-    if (j < r && k < in) dA[j * in + k] = Dt<DT>::from_f(tile[tx][jj]);
+    if (j < r && k < in) put_a<DT, F32>(dAv, j * in + k, tile[tx][jj], add);
   }
 }
 
-template <int DT>
-__global__ __launch_bounds__(256) void nbwd_zero(void* pv, int64_t n) {
-  using T = typename Dt<DT>::T;
+template <class T>
+__global__ __launch_bounds__(256) void nbwd_zero(T* p, int64_t n) {
   for (int64_t e = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; e < n;
        e += static_cast<int64_t>(gridDim.x) * 256)
-    static_cast<T*>(pv)[e] = Dt<DT>::from_f(0.0f);
+    p[e] = static_cast<T>(0.0f);
 }
 
 inline dim3 stride_grid(int64_t n) { return dim3(static_cast<unsigned>(std::max<int64_t>(1, std::min<int64_t>(ndiv(n, 256), 4096)))); }
 
-template <int DT>
+template <class T>
 hipError_t zero_t(void* p, int64_t n, hipStream_t stream) {
   if (n <= 0) return hipSuccess;
-  hipLaunchKernelGGL((nbwd_zero<DT>), stride_grid(n), dim3(256), 0, stream, p, n);
+  hipLaunchKernelGGL((nbwd_zero<T>), stride_grid(n), dim3(256), 0, stream, static_cast<T*>(p), n);
   return hipGetLastError();
 }
 
@@ -327,10 +338,10 @@ __global__ __launch_bounds__(256) void nbwd_gen_db(const void* Wv, const void* A
 }
 
 // d_A[j][k] = s (sum_i c_i B_ij W0_ik + s sum_l M_jl A_lk)
-template <int DT>
+template <int DT, bool F32>
 __global__ __launch_bounds__(256) void nbwd_gen_da(const void* Wv, const void* Av, const void* Bv, const float* c,
                                                    const float* M, int64_t out, int64_t in, int64_t r, float s,
-                                                   void* dAv) {
+                                                   void* dAv, bool add) {
   using T = typename Dt<DT>::T;
   const T *W = static_cast<const T*>(Wv), *A = static_cast<const T*>(Av), *B = static_cast<const T*>(Bv);
   const int64_t e = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
@@ -340,10 +351,10 @@ __global__ __launch_bounds__(256) void nbwd_gen_da(const void* Wv, const void* A
   for (int64_t i = 0; i < out; ++i)
     a1 = __builtin_fmaf(c[i] * Dt<DT>::to_f(B[i * r + j]), Dt<DT>::to_f(W[i * in + k]), a1);
   for (int64_t l = 0; l < r; ++l) a2 = __builtin_fmaf(M[j * r + l], Dt<DT>::to_f(A[l * in + k]), a2);
-  static_cast<T*>(dAv)[e] = Dt<DT>::from_f(s * __builtin_fmaf(s, a2, a1));
+  put_a<DT, F32>(dAv, e, s * __builtin_fmaf(s, a2, a1), add);
 }
 
-template <int DT>
+template <int DT, bool F32>
 hipError_t launch_norm_bwd_gen_t(const NormBwdPlan& p, const NormBwdArgs& a) {
   const int64_t out = p.out, in = p.in, r = p.r;
   char* ws = static_cast<char*>(a.ws);
@@ -356,18 +367,22 @@ hipError_t launch_norm_bwd_gen_t(const NormBwdPlan& p, const NormBwdArgs& a) {
                      a.B, c, out, in, r, G, M);
   hipLaunchKernelGGL((nbwd_gen_db<DT>), dim3(static_cast<unsigned>(ndiv(out * r, 256))), dim3(256), 0, a.stream,
                      a.W0, a.A, a.B, c, G, out, in, r, a.s, a.d_B);
-  hipLaunchKernelGGL((nbwd_gen_da<DT>), dim3(static_cast<unsigned>(ndiv(r * in, 256))), dim3(256), 0, a.stream,
-                     a.W0, a.A, a.B, c, M, out, in, r, a.s, a.d_A);
+  hipLaunchKernelGGL((nbwd_gen_da<DT, F32>), dim3(static_cast<unsigned>(ndiv(r * in, 256))), dim3(256), 0, a.stream,
+                     a.W0, a.A, a.B, c, M, out, in, r, a.s, a.d_A, a.add_A);
   return hipGetLastError();
 }
 
-template <int DT>
+template <int DT, bool F32>
 hipError_t launch_norm_bwd_t(const NormBwdPlan& p, const NormBwdArgs& a) {
+  using T = typename Dt<DT>::T;
   const int64_t out = p.out, in = p.in, r = p.r;
   if (r == 0) return hipSuccess;
-  if (out == 0) return zero_t<DT>(a.d_A, r * in, a.stream);
-  if (in == 0) return zero_t<DT>(a.d_B, out * r, a.stream);
-  if (!p.vec) return launch_norm_bwd_gen_t<DT>(p, a);
+  if (out == 0) {
+    if constexpr (F32) return a.add_A ? hipSuccess : zero_t<float>(a.d_A, r * in, a.stream);
+    return zero_t<T>(a.d_A, r * in, a.stream);
+  }
+  if (in == 0) return zero_t<T>(a.d_B, out * r, a.stream);
+  if (!p.vec) return launch_norm_bwd_gen_t<DT, F32>(p, a);
   char* ws = static_cast<char*>(a.ws);
   float* c = reinterpret_cast<float*>(ws + p.off_c);
   void* Y = ws + p.off_y;
@@ -406,7 +421,8 @@ hipError_t launch_norm_bwd_t(const NormBwdPlan& p, const NormBwdArgs& a) {
   e = launch_row_contract(a.W0, Y, out, in, r, 2 * r, true, p.np.dtype, big, a.stream, a.A, Z, r);
   if (e != hipSuccess) return e;
   const dim3 fgrid(static_cast<unsigned>(ndiv(in, 32)), static_cast<unsigned>(ndiv(r, 32)));
-  hipLaunchKernelGGL((nbwd_finalize_a<DT>), fgrid, dim3(256), 0, a.stream, big, p.rW.nSplit, in, r, sigma, a.d_A);
+  hipLaunchKernelGGL((nbwd_finalize_a<DT, F32>), fgrid, dim3(256), 0, a.stream, big, p.rW.nSplit, in, r, sigma, a.d_A,
+                     a.add_A);
   return hipGetLastError();
 }
 
@@ -458,7 +474,8 @@ size_t norm_bwd_workspace_bytes(int64_t out, int64_t in, int64_t r, int dtype) {
 }
 
 hipError_t launch_norm_bwd(const NormBwdPlan& p, const NormBwdArgs& a) {
-  return a.dtype == 0 ? launch_norm_bwd_t<0>(p, a) : launch_norm_bwd_t<1>(p, a);
+  if (a.f32_A) return a.dtype == 0 ? launch_norm_bwd_t<0, true>(p, a) : launch_norm_bwd_t<1, true>(p, a);
+  return a.dtype == 0 ? launch_norm_bwd_t<0, false>(p, a) : launch_norm_bwd_t<1, false>(p, a);
 }
 
 }  // namespace dora

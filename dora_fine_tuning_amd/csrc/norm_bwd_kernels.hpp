@@ -37,6 +37,7 @@ struct NormBwdArgs {
   void *d_A, *d_B;
   void* ws;
   hipStream_t stream;
+  bool f32_A = false, add_A = false;  // d_A in fp32, added to what it holds
 };
 
 // The 16-byte path (p.vec) needs in % 8 == 0, r % 8 == 0, in < 2^21, r <= 2^20

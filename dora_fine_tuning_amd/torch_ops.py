@@ -717,6 +717,29 @@ def _q8_weight_norm_fake(wq, we, A, B, base_sq, s):
     return B.new_empty((B.shape[0],), dtype=torch.float32)
 
 
+@torch.library.custom_op("dora_amd::q8_weight_norm_backward", mutates_args=())
+@_without_autocast
+def q8_weight_norm_backward(wq: Tensor, we: Tensor, A: Tensor, B: Tensor, norm: Tensor, d_norm: Tensor,
+                            s: float) -> tuple[Tensor, Tensor]:
+    """``weight_norm_backward`` of a packed weight: (d_A, d_B), the slabs' parts
+    of d_A added in fp32 and rounded once."""
+    A, B, norm, d_norm = A.contiguous(), B.contiguous(), norm.contiguous().float(), d_norm.contiguous().float()
+    d_A, d_B = torch.zeros(A.shape, dtype=torch.float32, device=A.device), torch.empty_like(B)
+    for rows, W in _slabs(wq, we, B.shape[0], A.shape[1], A.dtype):
+        if _kernels_take(W, A, B):
+            d_B[rows] = binding.dora_norm_bwd_slab(W, A, B[rows], norm[rows], d_norm[rows], s, d_A, rows.start > 0)
+        else:
+            a, b = _eager_weight_norm_backward(W, A.float(), B[rows].float(), norm[rows], d_norm[rows], s)
+            d_A += a
+            d_B[rows] = b.to(B.dtype)
+    return d_A.to(A.dtype), d_B
+
+
+@q8_weight_norm_backward.register_fake
+def _q8_weight_norm_backward_fake(wq, we, A, B, norm, d_norm, s):
+    return A.new_empty(A.shape), B.new_empty(B.shape)
+
+
 def _q8_norm_setup(ctx, inputs, output):
     wq, we, A, B, _, s = inputs
     ctx.save_for_backward(wq, we, A, B, output)
@@ -725,12 +748,9 @@ def _q8_norm_setup(ctx, inputs, output):
 
 def _q8_norm_grad(ctx, d_norm):
     wq, we, A, B, n = ctx.saved_tensors
-    d_A, d_B = torch.zeros(A.shape, dtype=torch.float32, device=A.device), torch.empty_like(B)
-    for rows, W in _slabs(wq, we, B.shape[0], A.shape[1], A.dtype):
-        a, d_B[rows] = weight_norm_backward(W, A, B[rows], n[rows], d_norm[rows], ctx.s)
-        d_A += a
+    d_A, d_B = q8_weight_norm_backward(wq, we, A, B, n, d_norm, ctx.s)
     need = ctx.needs_input_grad
-    return None, None, d_A.to(A.dtype) if need[2] else None, d_B if need[3] else None, None, None
+    return None, None, d_A if need[2] else None, d_B if need[3] else None, None, None
 
 
 q8_weight_norm.register_autograd(_q8_norm_grad, setup_context=_q8_norm_setup)

@@ -31,6 +31,7 @@
  *
  *   dora_norm_bwd              d_A and d_B of the weight norm, from dL/dn,
  *                              without forming B*A;
+ *   dora_norm_bwd_slab         the same from a W0 in slabs of rows;
  *
  * and, for the cached base norm the page lists as future work (W0 is frozen):
  *
@@ -256,6 +257,17 @@ DORA_API size_t dora_norm_bwd_workspace_bytes(int64_t out, int64_t in, int64_t r
 DORA_API int dora_norm_bwd(const void* W0, const void* A, const void* B, const float* norm, const float* d_norm,
                            int64_t out, int64_t in, int64_t r, float s, int dtype, void* d_A, void* d_B, void* ws,
                            size_t ws_bytes, hipStream_t stream);
+
+/*
+ * dora_norm_bwd of `out` rows of a W0 that comes in slabs of rows (as an 8-bit
+ * one does, unpacked a slab at a time).  d_B holds these rows' gradient; d_A is
+ * fp32 [r x in] and, with add_A != 0, is added to (in the order of the calls), so
+ * that the sum over all slabs can be rounded once.  The same workspace, sizes and
+ * refusals; out == 0 gives d_A = 0 where add_A == 0, else nothing.
+ */
+DORA_API int dora_norm_bwd_slab(const void* W0, const void* A, const void* B, const float* norm, const float* d_norm,
+                                int64_t out, int64_t in, int64_t r, float s, int dtype, int add_A, float* d_A,
+                                void* d_B, void* ws, size_t ws_bytes, hipStream_t stream);
 
 /* Bytes of device workspace dora_lora_compose_bwd needs (fp32 slices of dy^T h and column partials). */
 DORA_API size_t dora_lora_compose_bwd_workspace_bytes(int64_t T, int64_t out, int64_t r);
