@@ -617,7 +617,8 @@ __global__ __launch_bounds__(256) void q8_grad_a_finalize(const float* e_part, i
 }
 
 // Y's columns a workgroup takes, in 128s (least padding, then widest), and token
-// slices: one workgroup a CU (it holds most of its LDS), at least eight stages.
+// slices: one workgroup a CU (it holds most of its LDS), at least eight stages,
+// and no slice of any operand (row_bytes: the longest row) of 2 GiB or more.
 struct RowsPlan {
   int tn = 1, nCB = 0, nTiles = 0, nSplit = 1;
   size_t off_col = 0, bytes = 0;
@@ -654,7 +655,8 @@ Q8BwdPlan q8_bwd_plan(int64_t T, int64_t nx, int64_t r, bool compose) {
   p.xp = up8(nx);
   p.pad_x = compose && p.xp != nx;
   p.pad_r = p.rp != r;
-  p.tile = rows_plan(T, nx, p.rp, std::max(p.xp, p.rp) * 2);
+  // (a packed row is longer than a 16-bit one below 64 columns)
+  p.tile = rows_plan(T, nx, p.rp, std::max({p.xp * 2, p.rp * 2, q8_row_bytes(nx)}));
   size_t at = al256(p.tile.bytes);
   p.off_dy = at;
   if (p.pad_x) at = al256(at + static_cast<size_t>(T) * p.xp * 2);
