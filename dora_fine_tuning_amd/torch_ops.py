@@ -441,8 +441,12 @@ def _eager_q8_pack_weight(W):
     return q.reshape(v.shape), _padded_exponents(e[:, 0, :, 0])
 
 
-def _values(q, e, cols, weight=False):
-    """The fp32 values of packed rows (or of a packed weight)."""
+def _values(q, e, cols, name, shapes, weight=False):
+    """The fp32 values of packed rows (or of a packed weight), which have to be
+    laid out as the kernels ask for."""
+    for t, what, shape, dtype in ((q, name, shapes[0], _F8), (e, name + "'s exponents", shapes[1], torch.uint8)):
+        if tuple(t.shape) != shape or t.dtype != dtype:
+            raise ValueError(f"{what} is {tuple(t.shape)} in {t.dtype}, expected {shape} in {dtype}")
     nb = q.shape[1] // 128
     s = _exp2i(e[:, :nb].to(torch.int32) - 127)
     s = s.repeat_interleave(128, dim=1)
@@ -457,26 +461,33 @@ def _held(v, dtype):
 
 
 def _eager_q8_unpack(q, e, cols, dtype):
-    return _held(_values(q, e, cols), dtype)
+    return _held(_values(q, e, cols, "q", binding.q8_row_shapes(q.shape[0], cols)), dtype)
 
 
 def _eager_q8_unpack_weight(q, e, rows, cols, dtype):
-    return _held(_values(q, e, cols, True)[:rows], dtype)
+    if not 0 <= rows <= q.shape[0]:
+        raise ValueError(f"rows {rows} out of range of a packed weight of {q.shape[0]}")
+    return _held(_values(q, e, cols, "q", binding.q8_weight_shapes(q.shape[0], cols), True)[:rows], dtype)
 
 
 @_without_autocast
 def _eager_q8_linear(xq, xe, wq, we, out_features, dtype):
-    return (_values(xq, xe, xq.shape[1]) @ _values(wq, we, wq.shape[1], True)[:out_features].t()).to(dtype)
+    T, n = xq.shape
+    x = _values(xq, xe, n, "xq", binding.q8_row_shapes(T, n))
+    W = _values(wq, we, n, "wq", binding.q8_weight_shapes(out_features, n), True)
+    return (x @ W[:out_features].t()).to(dtype)
 
 
 @_without_autocast
 def _eager_q8_linear_backward(gq, ge, wq, we, in_features, dtype):
-    return (_values(gq, ge, gq.shape[1]) @ _values(wq, we, in_features, True)).to(dtype)
+    T, n = gq.shape
+    g = _values(gq, ge, n, "gq", binding.q8_row_shapes(T, n))
+    return (g @ _values(wq, we, in_features, "wq", binding.q8_weight_shapes(n, in_features), True)).to(dtype)
 
 
 @_without_autocast
 def _eager_q8_lora_compose_backward(dy, bq, be, h, B, mag, norm, s, add_base, want_base):
-    base = _values(bq, be, dy.shape[1])
+    base = _values(bq, be, dy.shape[1], "bq", binding.q8_row_shapes(*dy.shape))
     return _eager_lora_compose_backward(dy, base, h, B, mag, norm, s, add_base, want_base)
 
 
@@ -490,7 +501,8 @@ def _eager_q8_lora_compose_backward_packed(dy, bq, be, h, B, mag, norm, s, add_b
 
 @_without_autocast
 def _eager_q8_grad_a(dh, xq, xe, in_features):
-    return (dh.float().t() @ _held(_values(xq, xe, in_features), dh.dtype).float()).to(dh.dtype)
+    x = _values(xq, xe, in_features, "xq", binding.q8_row_shapes(dh.shape[0], in_features))
+    return (dh.float().t() @ _held(x, dh.dtype).float()).to(dh.dtype)
 
 
 # These operators are registered without the wrapper of a custom operator: they
