@@ -903,8 +903,10 @@ class DoRALinear(torch.nn.Module):
         """Recompute ||W0_i||^2 (after ``weight`` changed)."""
         if self.q8_weight:
             wq, we = self._packed_weight()
-            slabs = _slabs(wq, we, self.out_features, self.in_features, self.lora_A.dtype)
-            self.weight_sqnorm = torch.cat([row_sqnorm(W) for _, W in slabs])
+            n = torch.empty(self.out_features, dtype=torch.float32, device=wq.device)
+            for rows, W in _slabs(wq, we, self.out_features, self.in_features, self.lora_A.dtype):
+                n[rows] = row_sqnorm(W)
+            self.weight_sqnorm = n
         else:
             self.weight_sqnorm = row_sqnorm(self.weight)
 
