@@ -389,6 +389,19 @@ def _without_autocast(fn):
     return inner
 
 
+def _q8_eager(fn):
+    """The eager form of an operator: without autocast, and with outputs in the
+    kernels' order of memory whatever its arguments' strides."""
+
+    @functools.wraps(fn)
+    def inner(*args):
+        with torch._C._ExcludeDispatchKeyGuard(_AUTOCAST_KEYS):
+            out = fn(*args)
+        return tuple(t.contiguous() for t in out) if isinstance(out, tuple) else out.contiguous()
+
+    return inner
+
+
 def _autocast(*mats):
     """The matrices in autocast's type where it is on for their device, as linear
     takes them (64-bit and packed ones stay as they are)."""
@@ -421,6 +434,7 @@ def _padded_exponents(e: Tensor) -> Tensor:
     return F.pad(e, (0, _round_up(e.shape[1], 4) - e.shape[1]), value=127)
 
 
+@_q8_eager
 def _eager_q8_pack(x):
     T, K = x.shape
     if x.numel() == 0:
@@ -431,6 +445,7 @@ def _eager_q8_pack(x):
     return q.reshape(T, -1), _padded_exponents(e[:, :, 0])
 
 
+@_q8_eager
 def _eager_q8_pack_weight(W):
     o, i = W.shape
     if W.numel() == 0:
@@ -460,17 +475,19 @@ def _held(v, dtype):
     return v.clamp(-big, big).to(dtype)
 
 
+@_q8_eager
 def _eager_q8_unpack(q, e, cols, dtype):
     return _held(_values(q, e, cols, "q", binding.q8_row_shapes(q.shape[0], cols)), dtype)
 
 
+@_q8_eager
 def _eager_q8_unpack_weight(q, e, rows, cols, dtype):
     if not 0 <= rows <= q.shape[0]:
         raise ValueError(f"rows {rows} out of range of a packed weight of {q.shape[0]}")
     return _held(_values(q, e, cols, "q", binding.q8_weight_shapes(q.shape[0], cols), True)[:rows], dtype)
 
 
-@_without_autocast
+@_q8_eager
 def _eager_q8_linear(xq, xe, wq, we, out_features, dtype):
     T, n = xq.shape
     x = _values(xq, xe, n, "xq", binding.q8_row_shapes(T, n))
@@ -478,20 +495,20 @@ def _eager_q8_linear(xq, xe, wq, we, out_features, dtype):
     return (x @ W[:out_features].t()).to(dtype)
 
 
-@_without_autocast
+@_q8_eager
 def _eager_q8_linear_backward(gq, ge, wq, we, in_features, dtype):
     T, n = gq.shape
     g = _values(gq, ge, n, "gq", binding.q8_row_shapes(T, n))
     return (g @ _values(wq, we, in_features, "wq", binding.q8_weight_shapes(n, in_features), True)).to(dtype)
 
 
-@_without_autocast
+@_q8_eager
 def _eager_q8_lora_compose_backward(dy, bq, be, h, B, mag, norm, s, add_base, want_base):
     base = _values(bq, be, dy.shape[1], "bq", binding.q8_row_shapes(*dy.shape))
     return _eager_lora_compose_backward(dy, base, h, B, mag, norm, s, add_base, want_base)
 
 
-@_without_autocast
+@_q8_eager
 def _eager_q8_lora_compose_backward_packed(dy, bq, be, h, B, mag, norm, s, add_base):
     _, d_B, d_mag = _eager_q8_lora_compose_backward(dy, bq, be, h, B, mag, norm, s, add_base, False)
     g, gm1 = _scales(mag, norm)
@@ -499,7 +516,7 @@ def _eager_q8_lora_compose_backward_packed(dy, bq, be, h, B, mag, norm, s, add_b
     return q, e, d_B, d_mag
 
 
-@_without_autocast
+@_q8_eager
 def _eager_q8_grad_a(dh, xq, xe, in_features):
     x = _values(xq, xe, in_features, "xq", binding.q8_row_shapes(dh.shape[0], in_features))
     return (dh.float().t() @ _held(x, dh.dtype).float()).to(dh.dtype)
@@ -667,8 +684,8 @@ def q8_lora_compose_backward(dy: Tensor, bq: Tensor, be: Tensor, h: Tensor, B: T
 
 @torch.library.register_fake("dora_amd::q8_lora_compose_backward")
 def _q8_lora_compose_backward_fake(dy, bq, be, h, B, mag, norm, s, add_base, want_base):
-    d_base = torch.empty_like(dy) if want_base else dy.new_empty((0,))
-    return d_base, torch.empty_like(B), mag.new_empty(mag.shape)
+    d_base = dy.new_empty(dy.shape if want_base else (0,))
+    return d_base, B.new_empty(B.shape), mag.new_empty(mag.shape, dtype=torch.float32)
 
 
 @_q8_kernel("q8_lora_compose_backward_packed")
@@ -685,7 +702,7 @@ def q8_lora_compose_backward_packed(dy: Tensor, bq: Tensor, be: Tensor, h: Tenso
 @torch.library.register_fake("dora_amd::q8_lora_compose_backward_packed")
 def _q8_lora_compose_backward_packed_fake(dy, bq, be, h, B, mag, norm, s, add_base):
     q, e = _q8_pack_fake(dy)
-    return q, e, torch.empty_like(B), mag.new_empty(mag.shape)
+    return q, e, B.new_empty(B.shape), mag.new_empty(mag.shape, dtype=torch.float32)
 
 
 @_q8_kernel("q8_grad_a")
