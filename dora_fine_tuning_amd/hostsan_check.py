@@ -2,8 +2,8 @@
 UndefinedBehaviorSanitizer.
 
 Builds libdora_hip_hostsan.so (host code instrumented, device code as in the
-product) and runs the ABI tests of tests/test_abi_cpu.py and tests/test_q8_cpu.py
-against it in a child process with the ASan runtime preloaded (ahead of anything
+product) and runs the ABI tests of tests/test_abi_cpu.py, tests/test_q8_cpu.py
+and tests/test_q8_norm_slabs.py against it in a child process with the ASan runtime preloaded (ahead of anything
 already in LD_PRELOAD).  Leak detection is off: the Python interpreter itself
 holds memory until exit.  Any sanitizer report aborts the child, so a clean run
 is exit status 0.
@@ -39,8 +39,8 @@ def main() -> int:
     env["UBSAN_OPTIONS"] = "halt_on_error=1:print_stacktrace=1"
     env["DORA_HIP_LIB"] = lib
     cmd = [sys.executable, "-m", "pytest", "-x", "-q", "-p", "no:cacheprovider",
-           os.path.join(ROOT, "tests", "test_abi_cpu.py"), os.path.join(ROOT, "tests", "test_q8_cpu.py"),
-           "-k", "abi or refus or workspace or valid or bind"]
+           *(os.path.join(ROOT, "tests", f) for f in ("test_abi_cpu.py", "test_q8_cpu.py", "test_q8_norm_slabs.py")),
+           "-m", "not gpu", "-k", "abi or refus or workspace or valid or bind"]
     print("running:", " ".join(cmd), f"(DORA_HIP_LIB={lib})", flush=True)
     return subprocess.call(cmd, cwd=ROOT, env=env)
 
