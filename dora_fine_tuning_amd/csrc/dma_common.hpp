@@ -1,11 +1,14 @@
 // Device helpers of the direct global -> LDS (DMA) kernels on gfx950: buffer
 // resources and 16-byte-per-lane loads into LDS, waits on the vector-memory
 // counter, LDS fragment reads issued as inline assembly, the XCD-aware
-// workgroup numbering, and packed squares for the base term.
+// workgroup numbering, unrolling by compile-time indices, and packed squares for
+// the base term.
 #pragma once
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+
+#include <utility>
 
 #include "dora_common.hpp"
 
@@ -21,6 +24,7 @@ __device__ inline int64_t xcd_logical_index() {
 
 typedef __attribute__((address_space(3))) void lds_void_t;
 typedef __attribute__((address_space(3))) char lds_char_t;
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr uint32_t kOob = 0xFFFFFF00u;   // buffer offset past any range: loads read zero
@@ -51,6 +55,7 @@ __device__ inline void lds_wait_keep() {
   asm volatile("s_waitcnt lgkmcnt(%0)" ::"n"(N) : "memory");
 }
 __device__ inline void tie(u32x4& v) { asm volatile("" : "+v"(v)); }
+__device__ inline void tie2(u32x2& v) { asm volatile("" : "+v"(v)); }
 // One 16-byte-per-lane buffer load straight into LDS: lane l writes bytes
 // [16l, 16l + 16) of the 1 KiB block at lds (wave-uniform); offsets at or past
 // the resource's num_records read zero.
@@ -64,6 +69,16 @@ __device__ inline u32x4 lds_read16_at(uint32_t base) {
   u32x4 v;
   asm volatile("ds_read_b128 %0, %1 offset:%2" : "=v"(v) : "v"(base), "n"(OFF) : "memory");
   return v;
+}
+
+// f(0), f(1), .. f(N - 1) with compile-time arguments.
+template <class F, int... I>
+__device__ inline void unrolled(F&& f, std::integer_sequence<int, I...>) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, class F>
+__device__ inline void unrolled(F&& f) {
+  unrolled(static_cast<F&&>(f), std::make_integer_sequence<int, N>{});
 }
 
 // acc + x0^2 + x1^2 for the two storage-dtype values packed in w (one dot2 instruction)

@@ -44,7 +44,6 @@ namespace {
 __host__ __device__ inline int64_t bcdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 typedef short v4i16 __attribute__((ext_vector_type(4)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 // Transposing LDS read: in each group of 16 lanes, source lane L gives an
 // 8-byte address (4 consecutive 16-bit elements of one row); result lane i
@@ -60,7 +59,6 @@ __device__ inline u32x2 lds_read_tr(uint32_t addr) {
   asm volatile("ds_read_b64_tr_b16 %0, %1" : "=v"(v) : "v"(addr) : "memory");
   return v;
 }
-__device__ inline void tie2(u32x2& v) { asm volatile("" : "+v"(v)); }
 
 // Tile: 128 output columns (X, 32*TM with TM = 4, WM = 2 waves along them) x
 // 128*TN rank columns (Y, WN = 4 waves along them); a wave owns TMW = 2 x TN

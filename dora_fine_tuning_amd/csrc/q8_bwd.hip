@@ -52,17 +52,6 @@ namespace {
 inline size_t al256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 inline int64_t up8(int64_t n) { return (n + 7) / 8 * 8; }
 
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-__device__ inline void tie2(u32x2& v) { asm volatile("" : "+v"(v)); }
-template <class F, int... I>
-__device__ inline void unrolled(F&& f, std::integer_sequence<int, I...>) {
-  (f(std::integral_constant<int, I>{}), ...);
-}
-template <int N, class F>
-__device__ inline void unrolled(F&& f) {
-  unrolled(static_cast<F&&>(f), std::make_integer_sequence<int, N>{});
-}
-
 // Transposing LDS reads: in each group of 16 lanes a source lane L gives the
 // 8-byte address of four columns of row L/4, and result lane i receives the four
 // rows of column i.

@@ -48,7 +48,6 @@ namespace dora {
 namespace {
 
 typedef int v8i __attribute__((ext_vector_type(8)));
-typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
 // ds_read_b64_tr_b8: in each group of 16 lanes, source lane L gives the address
 // of 8 consecutive bytes of row L/2 (half L%2 of 16 columns); result lane i
@@ -67,17 +66,6 @@ __device__ inline uint32_t lds_read4_at(uint32_t base) {
   uint32_t v;
   asm volatile("ds_read_b32 %0, %1 offset:%2" : "=v"(v) : "v"(base), "n"(OFF) : "memory");
   return v;
-}
-__device__ inline void tie2(u32x2& v) { asm volatile("" : "+v"(v)); }
-
-// f(0), f(1), .. f(N - 1) with compile-time arguments.
-template <class F, int... I>
-__device__ inline void unrolled(F&& f, std::integer_sequence<int, I...>) {
-  (f(std::integral_constant<int, I>{}), ...);
-}
-template <int N, class F>
-__device__ inline void unrolled(F&& f) {
-  unrolled(static_cast<F&&>(f), std::make_integer_sequence<int, N>{});
 }
 
 // Tile geometry: WM x WN waves, each TMW x TNW matrix tiles of 32 x 32 with
@@ -649,7 +637,7 @@ __global__ __launch_bounds__(256) void q8_gemm_join(GemmArgs a) {
                  static_cast<int64_t>(nt) * TL::BN + (wn * TL::TNW + j) * 32, acc, lane >> 5);
 }
 
-// Few rows (T <= 16).  A workgroup owns 16 output columns; its 16 waves take the
+// Few rows (T <= 8; the rows of one 16-row matrix tile).  A workgroup owns 16 output columns; its 16 waves take the
 // stages in turn and their sums meet in LDS.  The weight goes from global memory
 // straight into fragments of mfma 16x16x128, each row's 128 bytes of a stage by
 // two 16-byte loads of four lanes, four stages in flight a wave; the rows stay in
