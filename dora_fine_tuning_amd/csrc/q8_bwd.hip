@@ -21,13 +21,18 @@
 //                    or, for 8-bit X, the conversion of the next stage's panel
 //                    to 16 bits, once a value, into LDS.
 //
-// Measured at 8192^2 (whole calls, r = 384 / 128 / 16): compose, packed d_base
-// 121 / 76 / 68 us, 16-bit 127 / 85 / 80; gradient of A 89 / 41 / 31; and at 10240
-// x 27648, r = 512: 573, 580, 389.  What bounds it: at narrow r the bytes (r = 16
-// packed: 256 MiB of dy, base and d_base, 4.2 TB/s in the kernel); at wide r the
-// panel of Y, 24 KiB of DMA a stage into each CU for 4 KiB of the 8-bit X: the
-// return path is busy 63 % of the gradient's kernel, the matrix cores 28 %.
-// Measured and not kept (packed, 16-bit, gradient at r = 384): four waves of 64 x
+// Measured at 8192^2, bf16, whole calls back to back (r = 384 / 128 / 16): compose,
+// packed d_base 112 / 73 / 58 us, 16-bit 117 / 85 / 82 (from a 16-bit base, by
+// dora_lora_compose_bwd, 116 / 96 / 92); gradient of A 77 to 82 / 39 / 30; and at
+// 10240 x 27648, r = 512: 550, 577 (648), 369.  Under a kernel trace a call takes
+// longer (the gradient at r = 384: 85 from its first kernel's start to its second's
+// end), and after a read that evicts the caches 133 / 114 / 111, 137 / 117 / 116
+// (144 / 132 / 128) and 81 / 47 / 37.  What bounds it: at narrow r the bytes (r = 16
+// packed: 256 MiB of dy, base and d_base, 4.6 TB/s); at wide r the panel of Y, 24
+// KiB of DMA a stage into each CU for 4 KiB of the 8-bit X: the return path is busy
+// 63 % of the gradient's kernel, the matrix cores 28 %.
+// Measured and not kept (packed, 16-bit, gradient at r = 384, where the kept form
+// took 122 / 127 / 89 and 573 / 580 / 389 in the same session): four waves of 64 x
 // 64 TNW, each converting its own fragments of X, 129 / 125 / 87 and 645 / 584 /
 // 388 at 10240 x 27648; at r = 128 two workgroups a CU, with twice the token
 // slices, 92 / 105 / 45 against 75 / 85 / 40; a start of every workgroup at another

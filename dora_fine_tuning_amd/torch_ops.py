@@ -791,7 +791,8 @@ def q8_layer(x: Tensor, A: Tensor, B: Tensor, mag: Tensor, norm: Tensor, weight:
     """The layer on x [T x in] with 8-bit checkpoints: (y, then what the backward
     reads, itself without a gradient: x and base packed, and h).  ``weight`` is W0 [out x in] in 16 bits, or,
     with its exponents ``we``, packed: then both products with W0 run on packed
-    operands, x's being the checkpoint itself."""
+    operands, x's being the checkpoint itself.  Its matrices have one type (under
+    autocast they are cast to its); its backward has no backward."""
     xq, xe = q8_pack(x)
     base = F.linear(x, weight) if we is None else q8_linear(xq, xe, weight, we, B.shape[0], x.dtype)
     h = F.linear(x, A)
