@@ -1,0 +1,420 @@
+"""Operators around one frozen weight in 4 bits and several adapters over it: what each computes, on which sizes it is
+measured, and its value in 64 bits.
+
+The weight [out x in] is held in blocks of 32 columns of a row: e2m1 values (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their
+negatives) with a power-of-two scale 2^e a block, the smallest e from -23 to 13 for which the block's largest magnitude
+is at most 7 * 2^e.  The values are the nearest e2m1 values (ties to the even one of the eight, 6 at most) of v * 2^-e.
+A block that holds a value that is not finite is NaN as a whole.  The product y = x W^T and its gradient of x, dx = g W,
+take x and g in 16 bits.
+
+Slots (t, j) of T tokens with k adapters each are sorted by adapter: ``order`` lists the slots t * k + j by adapter,
+slots of one adapter in their own order, and behind them those without one (an id outside [0, n)) as their complement;
+``place`` is its inverse, and ``bounds`` says where each adapter's rows begin.  ``adapter_gather`` lays the tokens' rows out in that order
+(zeros for slots without an adapter), ``adapter_combine`` adds them up again per token with weights, onto a base.
+
+``run`` calls the framework's operators where ``own`` is true, and their plain form otherwise: elementary torch
+operations in fp32, rounded once at the end.  ``exact`` gives the same outputs in 64 bits.
+"""
+import math
+
+import torch
+
+own = False
+
+DT = {"bf16": torch.bfloat16, "fp16": torch.float16}
+DEV = "cuda"
+
+
+# ------------------------------------------------------------------ cases
+
+
+def listed():
+    return [
+        # single tokens of a serving loop: an attention projection, and a ~32B model's MLP up projection
+        {"name": "linear_token_attn", "op": "linear", "T": 1, "in": 4096, "out": 4096, "dtype": "bf16"},
+        {"name": "linear_token_mlp", "op": "linear", "T": 1, "in": 5120, "out": 27648, "dtype": "fp16"},
+        # the tokens of a ragged batch of requests, through the MLP down projection
+        {"name": "linear_ragged", "op": "linear", "T": 37, "in": 27648, "out": 5120, "dtype": "bf16"},
+        # a training batch through the 8192-wide module
+        {"name": "linear_wide", "op": "linear", "T": 8192, "in": 8192, "out": 8192, "dtype": "bf16"},
+        # gradient of the input: a short batch, and a long one through the MLP up projection's long contraction
+        {"name": "linear_bwd_short", "op": "linear_bwd", "T": 300, "in": 8192, "out": 8192, "dtype": "fp16"},
+        {"name": "linear_bwd_mlp", "op": "linear_bwd", "T": 10240, "in": 5120, "out": 27648, "dtype": "bf16"},
+        # a weight's way there and back (once when a model is loaded, and for its norm): the smallest, the largest
+        {"name": "pack_tiny", "op": "pack", "out": 512, "in": 512, "dtype": "bf16"},
+        {"name": "pack_mlp", "op": "pack", "out": 27648, "in": 5120, "dtype": "bf16"},
+        # tokens sorted by adapter: one token each of 37 requests, and a training batch with two adapters a token
+        {"name": "sort_requests", "op": "sort", "T": 37, "k": 1, "n": 8},
+        {"name": "sort_batch", "op": "sort", "T": 10240, "k": 2, "n": 64},
+        # rows to that order and back: the requests' (forward), the training batch's (forward and gradients)
+        {"name": "exchange_requests", "op": "exchange", "T": 37, "k": 1, "n": 8, "D": 5120, "dtype": "fp16", "train": False},
+        {"name": "exchange_batch", "op": "exchange", "T": 8192, "k": 2, "n": 16, "D": 8192, "dtype": "bf16", "train": True},
+    ]
+
+
+def _size(rng, lo, hi):
+    """Spread over the logarithm; a third each of whole blocks of 128, multiples of 8, and any size."""
+    n = int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+    step = (128, 8, 1)[rng.randrange(3)]
+    return min(hi, max(lo, n // step * step))
+
+
+def draw(rng):
+    op = rng.choice(["linear", "linear", "linear_bwd", "pack", "sort", "exchange"])
+    dtype = rng.choice(["bf16", "fp16"])
+    if op in ("linear", "linear_bwd", "pack"):
+        out, in_ = _size(rng, 512, 27648), _size(rng, 512, 27648)
+        if out * in_ > 27648 * 5120:  # no module is larger than the largest configured one
+            in_ = max(512, 27648 * 5120 // out)
+        if op == "pack":
+            return {"op": op, "out": out, "in": in_, "dtype": dtype}
+        return {"op": op, "T": _size(rng, 1, 10240), "in": in_, "out": out, "dtype": dtype}
+    k = rng.randint(1, 2)
+    if op == "sort":
+        return {"op": op, "T": _size(rng, 32, 10240), "k": k, "n": _size(rng, 4, 256)}
+    T, n, D = _size(rng, 1, 8192), _size(rng, 1, 256), _size(rng, 64, 8192)
+    return {"op": op, "T": T, "k": k, "n": n, "D": D, "dtype": dtype, "train": rng.random() < 0.6}
+
+
+def work(case):
+    """Each input read once and each output written once; 2 operations a multiply-add.  A weight in 4 bits is 17 / 32
+    bytes a value, its scales counted."""
+    op = case["op"]
+    if op in ("linear", "linear_bwd"):
+        T, i, o = case["T"], case["in"], case["out"]
+        return {"bytes": 2 * T * (i + o) + i * o * 17 // 32, "flops": 2 * T * i * o}
+    if op == "pack":  # 16 bits in, 4 bits out and in again, 16 bits out
+        n = case["out"] * case["in"]
+        return {"bytes": 4 * n + 2 * (n * 17 // 32), "flops": 4 * n}
+    T, k, n = case["T"], case["k"], case["n"]
+    if op == "sort":  # ids in, order, place and bounds out
+        return {"bytes": 16 * T * k + 4 * (n + 1), "flops": T * k}
+    D, R = case["D"], T * k
+    # tokens to rows (T in, R out); rows to tokens (rows and base in, y out)
+    b, f = 2 * D * (T + R) + 2 * D * (R + 2 * T), 2 * R * D
+    if case["train"]:  # the rows' gradients to tokens (R in, T out); dy and the rows in, the rows' gradients out
+        b, f = b + 2 * D * (R + T) + 2 * D * (T + 2 * R), f + 5 * R * D
+    return {"bytes": b + 12 * R, "flops": f}
+
+
+# ------------------------------------------------------------------ inputs
+
+
+def _gen(seed):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(int(seed))
+    return g
+
+
+def _normal(g, shape, scale=1.0):
+    return torch.randn(shape, generator=g, device=DEV) * scale
+
+
+def _acts(g, T, n, dt):
+    """Activations: unit normal, with one feature in about a hundred twenty times as large, as in trained models."""
+    big = torch.rand(n, generator=g, device=DEV) < 0.01
+    return (_normal(g, (T, n)) * torch.where(big, 20.0, 1.0)).to(dt)
+
+
+def _grads(g, T, n, dt):
+    """Upstream gradients: normal, each token's of its own size."""
+    tok = torch.exp2(_normal(g, (T, 1), 1.5)) * 2.0**-6
+    return (_normal(g, (T, n)) * tok).to(dt)
+
+
+def _ids(g, T, k, n):
+    """Adapters of the tokens, some far more often used than others; one slot in twenty has none."""
+    u = torch.rand((T, k), generator=g, device=DEV)
+    ids = (n * u * u).to(torch.int64).clamp(max=n - 1)
+    return torch.where(torch.rand((T, k), generator=g, device=DEV) < 0.05, torch.full_like(ids, -1), ids)
+
+
+def prepare(case, seed):
+    g, op = _gen(seed), case["op"]
+    st = {"case": case, "op": op}
+    if op in ("linear", "linear_bwd", "pack"):
+        dt = st["dt"] = DT[case["dtype"]]
+        # rows of their own size, as trained weights have
+        W = (_normal(g, (case["out"], case["in"]), 0.02) * torch.exp2(_normal(g, (case["out"], 1), 0.5))).to(dt)
+        if op == "pack":
+            st["W"] = W
+            return st
+        st["wq"], st["we"] = _pack(W)
+        st["x"] = _acts(g, case["T"], case["in"], dt) if op == "linear" else _grads(g, case["T"], case["out"], dt)
+        return st
+    T, k, n = case["T"], case["k"], case["n"]
+    st["ids"] = _ids(g, T, k, n)
+    if op == "sort":
+        return st
+    dt, D = DT[case["dtype"]], case["D"]
+    st["dt"] = dt
+    st["order"], st["place"], _ = _sort(st["ids"], n)
+    st["x"], st["base"] = _acts(g, T, D, dt), _acts(g, T, D, dt)
+    st["rows"] = _normal(g, (T * k, D)).to(dt)  # what the adapters made of the sorted rows
+    st["w"] = torch.softmax(_normal(g, (T, k)), dim=1) if k > 1 else torch.sigmoid(_normal(g, (T, k)))
+    if case["train"]:
+        st["dy"], st["dx_rows"] = _grads(g, T, D, dt), _grads(g, T * k, D, dt)
+        if own:  # the leaves of a training step
+            for name in ("x", "rows", "w"):
+                st[name].requires_grad_()
+    return st
+
+
+# ------------------------------------------------------------------ the 4-bit blocks, plain
+#
+# The layout is the framework's.  A tile is 32 rows x 128 columns, zeros outside the weight: q [row tiles, column
+# tiles, 2048 bytes] and e [row tiles, column tiles, 128 bytes].  Row 8 g + i (g < 4, i < 8) of a tile has its block b
+# (of four) in the 16 bytes at 256 i + 64 g + 16 (b ^ (i % 4)), the even column of a pair in the byte's low half, and
+# its exponent byte 127 + e (255: NaN) at 32 b + 8 g + 2 (i % 4) + i // 4.
+
+
+def _up(n, k):
+    return -(-n // k) * k
+
+
+def _where(device):
+    """Byte positions of a tile's blocks and exponents, [32 rows, 4 blocks]."""
+    r, b = torch.arange(32, device=device)[:, None], torch.arange(4, device=device)[None, :]
+    g, i = r // 8, r % 8
+    return 256 * i + 64 * g + 16 * (b ^ (i % 4)), 32 * b + 8 * g + 2 * (i % 4) + i // 4
+
+
+def _two_to(k):
+    """2^k in fp32, exactly, by its exponent field (k from -126 to 127)."""
+    return ((k + 127) << 23).to(torch.int32).view(torch.float32)
+
+
+def _codes(a):
+    """e2m1 codes 0 .. 7 of magnitudes: above each border, and on it where the upper neighbour is the even one."""
+    c = torch.zeros(a.shape, dtype=torch.uint8, device=a.device)
+    for border, up in ((0.25, False), (0.75, True), (1.25, False), (1.75, True), (2.5, False), (3.5, True), (5.0, False)):
+        c += (a >= border) if up else (a > border)
+    return c
+
+
+def _pack_plain(W):
+    o, i = W.shape
+    op, ip = _up(o, 32), _up(i, 128)
+    v = torch.zeros((op, ip), device=W.device)
+    v[:o, :i] = W.float()
+    v = v.view(op, ip // 32, 32)
+    amax = v.abs().amax(dim=2)
+    frac, ex = torch.frexp(amax)  # amax = frac * 2^ex, frac in [1/2, 1): 7 = 0.875 * 2^3
+    e = ex.to(torch.int32) - 3 + (frac > 0.875).to(torch.int32)
+    e = torch.where(amax > 0, e.clamp(-23, 13), torch.full_like(e, -23))
+    bad = ~torch.isfinite(v).all(dim=2)
+    s = v * _two_to(-torch.where(bad, torch.zeros_like(e), e))[:, :, None]
+    c = _codes(s.abs()) | (torch.signbit(s).to(torch.uint8) << 3)
+    c = torch.where(bad[:, :, None], torch.zeros_like(c), c)
+    byte = (c[:, :, 0::2] | (c[:, :, 1::2] << 4)).view(op // 32, 32, ip // 128, 4, 16).transpose(1, 2)
+    eb = torch.where(bad, torch.full_like(e, 255), e + 127).to(torch.uint8).view(op // 32, 32, ip // 128, 4).transpose(1, 2)
+    at, ea = _where(W.device)
+    q = torch.empty((op // 32, ip // 128, 2048), dtype=torch.uint8, device=W.device)
+    ex = torch.empty((op // 32, ip // 128, 128), dtype=torch.uint8, device=W.device)
+    q[:, :, (at[:, :, None] + torch.arange(16, device=W.device)).flatten()] = byte.flatten(2)
+    ex[:, :, ea.flatten()] = eb.flatten(2)
+    return q, ex
+
+
+def _unpack(q, e, o, i):
+    """The weight's values in fp32."""
+    at, ea = _where(q.device)
+    a, b = q.shape[:2]
+    byte = q[:, :, (at[:, :, None] + torch.arange(16, device=q.device)).flatten()].view(a, b, 32, 4, 16)
+    eb = e[:, :, ea.flatten()].view(a, b, 32, 4).to(torch.int32)
+    c = torch.stack((byte & 15, byte >> 4), dim=5).view(a, b, 32, 4, 32)
+    grid = torch.tensor([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0], device=q.device)
+    v = torch.cat((grid, -grid))[c.to(torch.int32)]
+    s = torch.where(eb == 255, torch.full_like(v[..., 0], math.nan), _two_to((eb - 127).clamp(-126, 127)))
+    return (v * s[..., None]).transpose(1, 2).reshape(a * 32, b * 128)[:o, :i]
+
+
+def _pack(W):
+    if own:
+        from dora_fine_tuning_amd import torch_ops
+
+        return torch_ops.q4_pack_weight(W)
+    return _pack_plain(W)
+
+
+def _sort_plain(ids, n):
+    flat = ids.flatten()
+    ok = (flat >= 0) & (flat < n)
+    _, slots = torch.sort(torch.where(ok, flat, torch.full_like(flat, n)), stable=True)
+    m = torch.arange(flat.numel(), device=flat.device)
+    order = torch.where(ok[slots], slots, -1 - slots)
+    place = torch.empty_like(slots)
+    place[slots] = torch.where(ok[slots], m, -1 - m)
+    at = torch.bincount(torch.where(ok, flat, torch.full_like(flat, n)), minlength=n + 1)
+    bounds = torch.cumsum(at, 0) - at
+    return order.to(torch.int32), place.to(torch.int32).view(ids.shape), bounds.to(torch.int32)
+
+
+def _sort(ids, n):
+    if own:
+        from dora_fine_tuning_amd import torch_ops
+
+        return torch_ops.adapter_sort(ids, n)
+    return _sort_plain(ids, n)
+
+
+# ------------------------------------------------------------------ one pass
+
+
+def run(st):
+    return _run_own(st) if own else _run_plain(st)
+
+
+def _run_own(st):
+    from dora_fine_tuning_amd import torch_ops as F
+
+    c, op = st["case"], st["op"]
+    if op == "pack":
+        return F.q4_unpack_weight(*F.q4_pack_weight(st["W"]), c["out"], c["in"], st["dt"])
+    if op == "linear":
+        return F.q4_linear(st["x"], st["wq"], st["we"], c["out"])
+    if op == "linear_bwd":
+        return F.q4_linear_backward(st["x"], st["wq"], st["we"], c["in"])
+    if op == "sort":
+        order, place, bounds = F.adapter_sort(st["ids"], c["n"])
+        return {"order": order, "place": place, "bounds": bounds}
+    order, place = st["order"], st["place"]
+    xs = F.adapter_gather(st["x"], order, place)
+    y = F.adapter_combine(st["rows"], st["w"], order, place, st["base"])
+    if not c["train"]:
+        return {"xs": xs, "y": y}
+    (dx,) = torch.autograd.grad(xs, (st["x"],), st["dx_rows"])
+    d_rows, d_w = torch.autograd.grad(y, (st["rows"], st["w"]), st["dy"])
+    return {"xs": xs.detach(), "y": y.detach(), "dx": dx, "d_rows": d_rows, "d_w": d_w}
+
+
+def _run_plain(st):
+    c, op = st["case"], st["op"]
+    if op == "pack":
+        return _unpack(*_pack_plain(st["W"]), c["out"], c["in"]).to(st["dt"])
+    if op == "linear":
+        return (st["x"].float() @ _unpack(st["wq"], st["we"], c["out"], c["in"]).t()).to(st["dt"])
+    if op == "linear_bwd":
+        return (st["x"].float() @ _unpack(st["wq"], st["we"], c["out"], c["in"])).to(st["dt"])
+    if op == "sort":
+        order, place, bounds = _sort_plain(st["ids"], c["n"])
+        return {"order": order, "place": place, "bounds": bounds}
+    order, place, dt, k = st["order"].long(), st["place"].long(), st["dt"], c["k"]
+    there, slot = (order >= 0)[:, None], torch.where(order >= 0, order, -1 - order)
+    used, at = (place >= 0)[:, :, None], torch.where(place >= 0, place, -1 - place)
+
+    def gathered(rows):  # [T, k, D] in fp32, zeros for slots without an adapter
+        v = rows.float()[at]
+        return torch.where(used, v, torch.zeros_like(v))
+
+    xs = torch.where(there, st["x"][slot // k], torch.zeros_like(st["x"][:1]))
+    w, r = st["w"], gathered(st["rows"])
+    y = (st["base"].float() + (w[:, :, None] * r).sum(dim=1)).to(dt)
+    if not c["train"]:
+        return {"xs": xs, "y": y}
+    dy = st["dy"].float()
+    dx = gathered(st["dx_rows"]).sum(dim=1).to(dt)
+    d_rows = w.flatten()[slot][:, None] * dy[slot // k]
+    d_rows = torch.where(there, d_rows, torch.zeros_like(d_rows)).to(dt)
+    return {"xs": xs, "y": y, "dx": dx, "d_rows": d_rows, "d_w": (dy[:, None, :] * r).sum(dim=2)}
+
+
+# ------------------------------------------------------------------ in 64 bits
+
+
+def _pow2(k):
+    """2^k in fp64, exactly."""
+    return ((k.to(torch.int64) + 1023) << 52).view(torch.float64)
+
+
+def _held(W):
+    """The values a weight is held as, from the definition."""
+    o, i = W.shape
+    v = torch.zeros((o, _up(i, 32)), dtype=torch.float64, device=W.device)
+    v[:, :i] = W
+    v = v.view(o, -1, 32)
+    a = v.abs().amax(dim=2, keepdim=True)
+    e = torch.ceil(torch.log2(a.clamp(min=1e-300) / 7.0)).clamp(-23.0, 13.0)
+    # the logarithm may be off by one next to a power of two: the smallest e with a <= 7 * 2^e
+    e = torch.where(a * _pow2(1 - e) <= 7.0, (e - 1).clamp(min=-23.0), e)
+    e = torch.where(a * _pow2(-e) > 7.0, (e + 1).clamp(max=13.0), e)
+    w = (v * _pow2(-e)).clamp(-6.0, 6.0)
+    # one bit after the leading one, and nothing finer than a half
+    _, k = torch.frexp(w)
+    step = _pow2((k - 2).clamp(min=-1))
+    w = torch.round(w / step) * step
+    w = torch.where(torch.isfinite(v).all(dim=2, keepdim=True), w * _pow2(e), torch.full_like(w, math.nan))
+    return w.view(o, -1)[:, :i]
+
+
+def _read(q, e, o, i):
+    """The values of a packed weight, block by block of a tile."""
+    a, b = q.shape[:2]
+    W = torch.empty((a, 32, b, 4, 16, 2), dtype=torch.float64, device=q.device)
+    for row in range(32):
+        g, r = divmod(row, 8)
+        for blk in range(4):
+            at = 256 * r + 64 * g + 16 * (blk ^ (r % 4))
+            byte = q[:, :, at : at + 16].long()
+            s = e[:, :, 32 * blk + 8 * g + 2 * (r % 4) + r // 4].long()
+            for half in (0, 1):
+                c = (byte >> (4 * half)) & 15
+                m, x = c % 2, c // 2 % 4  # a subnormal of the type is m / 2, the others (1 + m / 2) 2^(x - 1)
+                v = torch.where(x == 0, 0.5 * m, (1 + 0.5 * m) * _pow2(x - 1))
+                v = torch.where(c >= 8, -v, v) * _pow2(torch.where(s == 255, torch.zeros_like(s), s - 127))[:, :, None]
+                W[:, row, :, blk, :, half] = torch.where((s == 255)[:, :, None], torch.full_like(v, math.nan), v)
+    return W.view(a * 32, b * 128)[:o, :i]
+
+
+def exact(case, seed):
+    global own
+    was, own = own, False
+    try:
+        st = prepare(case, seed)
+    finally:
+        own = was
+    c, op = st["case"], st["op"]
+    if op == "pack":
+        return _held(st["W"])
+    if op in ("linear", "linear_bwd"):
+        W = _read(st["wq"], st["we"], c["out"], c["in"])
+        return st["x"].double() @ (W.t() if op == "linear" else W)
+    k, n = c["k"], c["n"]
+    ids = st["ids"].flatten()
+    N = ids.numel()
+    key = torch.where((ids >= 0) & (ids < n), ids, torch.full_like(ids, n))
+    # a slot's row: the slots of smaller adapters, and the earlier ones of its own
+    count = torch.zeros(n + 1, dtype=torch.int64, device=ids.device).scatter_add_(0, key, torch.ones_like(key))
+    first = torch.cumsum(count, 0) - count
+    row = torch.empty_like(key)
+    for a in range(n + 1):
+        mine = key == a
+        row = torch.where(mine, first[a] + torch.cumsum(mine.to(torch.int64), 0) - 1, row)
+    slots = torch.arange(N, device=ids.device)
+    if op == "sort":
+        order = torch.empty_like(slots)
+        order[row] = torch.where(key < n, slots, -1 - slots)
+        return {"order": order.to(torch.int32),
+                "place": torch.where(key < n, row, -1 - row).to(torch.int32).view(case["T"], k),
+                "bounds": first.to(torch.int32)}
+    T, D = c["T"], c["D"]
+    on = (key < n).view(T, k)
+
+    def to_rows(v):  # [T, k, D] to rows, zeros for slots without an adapter
+        out = torch.zeros((N, D), dtype=torch.float64, device=v.device)
+        out[row[on.flatten()]] = v.reshape(N, D)[on.flatten()]
+        return out
+
+    w, at = st["w"].double(), row.view(T, k)
+    y, xs = st["base"].double(), to_rows(st["x"].double()[:, None, :].expand(T, k, D))
+    for j in range(k):
+        y = y + torch.where(on[:, j, None], w[:, j, None] * st["rows"].double()[at[:, j]], torch.zeros_like(y))
+    if not c["train"]:
+        return {"xs": xs, "y": y}
+    dy, dx, d_w = st["dy"].double(), torch.zeros_like(y), []
+    for j in range(k):
+        m = on[:, j, None]
+        dx = dx + torch.where(m, st["dx_rows"].double()[at[:, j]], torch.zeros_like(y))
+        d_w.append(torch.where(m, dy * st["rows"].double()[at[:, j]], torch.zeros_like(y)).sum(dim=1))
+    d_rows = to_rows(w[:, :, None] * dy[:, None, :])
+    return {"xs": xs, "y": y, "dx": dx, "d_rows": d_rows, "d_w": torch.stack(d_w, dim=1)}
