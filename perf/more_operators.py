@@ -162,10 +162,10 @@ def prepare(case, seed):
 
 # ------------------------------------------------------------------ the 4-bit blocks, plain
 #
-# The layout is the framework's.  A tile is 32 rows x 128 columns, zeros outside the weight: q [row tiles, column
-# tiles, 2048 bytes] and e [row tiles, column tiles, 128 bytes].  Row 8 g + i (g < 4, i < 8) of a tile has its block b
-# (of four) in the 16 bytes at 256 i + 64 g + 16 (b ^ (i % 4)), the even column of a pair in the byte's low half, and
-# its exponent byte 127 + e (255: NaN) at 32 b + 8 g + 2 (i % 4) + i // 4.
+# The layout is the framework's.  A tile is 32 rows x 64 columns, zeros outside the weight: q [row tiles, column tiles,
+# 1024 bytes] and e [row tiles, column tiles, 64 bytes].  Row 8 g + i (g < 4, i < 8) of a tile has its block b (of two) in
+# the 16 bytes at 128 i + 32 g + 16 (b ^ (i / 2 % 2)), the even column of a pair in the byte's low half, and its exponent
+# byte 127 + e (255: NaN) at 32 b + 8 g + 2 (i % 4) + i / 4.
 
 
 def _up(n, k):
@@ -173,10 +173,10 @@ def _up(n, k):
 
 
 def _where(device):
-    """Byte positions of a tile's blocks and exponents, [32 rows, 4 blocks]."""
-    r, b = torch.arange(32, device=device)[:, None], torch.arange(4, device=device)[None, :]
+    """Byte positions of a tile's blocks and exponents, [32 rows, 2 blocks]."""
+    r, b = torch.arange(32, device=device)[:, None], torch.arange(2, device=device)[None, :]
     g, i = r // 8, r % 8
-    return 256 * i + 64 * g + 16 * (b ^ (i % 4)), 32 * b + 8 * g + 2 * (i % 4) + i // 4
+    return 128 * i + 32 * g + 16 * (b ^ (i // 2 % 2)), 32 * b + 8 * g + 2 * (i % 4) + i // 4
 
 
 def _two_to(k):
@@ -194,7 +194,7 @@ def _codes(a):
 
 def _pack_plain(W):
     o, i = W.shape
-    op, ip = _up(o, 32), _up(i, 128)
+    op, ip = _up(o, 32), _up(i, 64)
     v = torch.zeros((op, ip), device=W.device)
     v[:o, :i] = W.float()
     v = v.view(op, ip // 32, 32)
@@ -206,11 +206,11 @@ def _pack_plain(W):
     s = v * _two_to(-torch.where(bad, torch.zeros_like(e), e))[:, :, None]
     c = _codes(s.abs()) | (torch.signbit(s).to(torch.uint8) << 3)
     c = torch.where(bad[:, :, None], torch.zeros_like(c), c)
-    byte = (c[:, :, 0::2] | (c[:, :, 1::2] << 4)).view(op // 32, 32, ip // 128, 4, 16).transpose(1, 2)
-    eb = torch.where(bad, torch.full_like(e, 255), e + 127).to(torch.uint8).view(op // 32, 32, ip // 128, 4).transpose(1, 2)
+    byte = (c[:, :, 0::2] | (c[:, :, 1::2] << 4)).view(op // 32, 32, ip // 64, 2, 16).transpose(1, 2)
+    eb = torch.where(bad, torch.full_like(e, 255), e + 127).to(torch.uint8).view(op // 32, 32, ip // 64, 2).transpose(1, 2)
     at, ea = _where(W.device)
-    q = torch.empty((op // 32, ip // 128, 2048), dtype=torch.uint8, device=W.device)
-    ex = torch.empty((op // 32, ip // 128, 128), dtype=torch.uint8, device=W.device)
+    q = torch.empty((op // 32, ip // 64, 1024), dtype=torch.uint8, device=W.device)
+    ex = torch.empty((op // 32, ip // 64, 64), dtype=torch.uint8, device=W.device)
     q[:, :, (at[:, :, None] + torch.arange(16, device=W.device)).flatten()] = byte.flatten(2)
     ex[:, :, ea.flatten()] = eb.flatten(2)
     return q, ex
@@ -220,13 +220,13 @@ def _unpack(q, e, o, i):
     """The weight's values in fp32."""
     at, ea = _where(q.device)
     a, b = q.shape[:2]
-    byte = q[:, :, (at[:, :, None] + torch.arange(16, device=q.device)).flatten()].view(a, b, 32, 4, 16)
-    eb = e[:, :, ea.flatten()].view(a, b, 32, 4).to(torch.int32)
-    c = torch.stack((byte & 15, byte >> 4), dim=5).view(a, b, 32, 4, 32)
+    byte = q[:, :, (at[:, :, None] + torch.arange(16, device=q.device)).flatten()].view(a, b, 32, 2, 16)
+    eb = e[:, :, ea.flatten()].view(a, b, 32, 2).to(torch.int32)
+    c = torch.stack((byte & 15, byte >> 4), dim=5).view(a, b, 32, 2, 32)
     grid = torch.tensor([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0], device=q.device)
     v = torch.cat((grid, -grid))[c.to(torch.int32)]
     s = torch.where(eb == 255, torch.full_like(v[..., 0], math.nan), _two_to((eb - 127).clamp(-126, 127)))
-    return (v * s[..., None]).transpose(1, 2).reshape(a * 32, b * 128)[:o, :i]
+    return (v * s[..., None]).transpose(1, 2).reshape(a * 32, b * 64)[:o, :i]
 
 
 def _pack(W):
@@ -350,11 +350,11 @@ def _held(W):
 def _read(q, e, o, i):
     """The values of a packed weight, block by block of a tile."""
     a, b = q.shape[:2]
-    W = torch.empty((a, 32, b, 4, 16, 2), dtype=torch.float64, device=q.device)
+    W = torch.empty((a, 32, b, 2, 16, 2), dtype=torch.float64, device=q.device)
     for row in range(32):
         g, r = divmod(row, 8)
-        for blk in range(4):
-            at = 256 * r + 64 * g + 16 * (blk ^ (r % 4))
+        for blk in range(2):
+            at = 128 * r + 32 * g + 16 * (blk ^ (r // 2 % 2))
             byte = q[:, :, at : at + 16].long()
             s = e[:, :, 32 * blk + 8 * g + 2 * (r % 4) + r // 4].long()
             for half in (0, 1):
@@ -363,7 +363,7 @@ def _read(q, e, o, i):
                 v = torch.where(x == 0, 0.5 * m, (1 + 0.5 * m) * _pow2(x - 1))
                 v = torch.where(c >= 8, -v, v) * _pow2(torch.where(s == 255, torch.zeros_like(s), s - 127))[:, :, None]
                 W[:, row, :, blk, :, half] = torch.where((s == 255)[:, :, None], torch.full_like(v, math.nan), v)
-    return W.view(a * 32, b * 128)[:o, :i]
+    return W.view(a * 32, b * 64)[:o, :i]
 
 
 def exact(case, seed):
