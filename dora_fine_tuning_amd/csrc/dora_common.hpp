@@ -30,6 +30,11 @@ struct Dt<0> {
   __device__ static inline f32x16 mfma32(V8 a, V8 b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
   }
+  // D[16x16] += A[16x32] * B[32x16]; lane l holds A row l%16, k 8*(l/16)..+7 and
+  // B column l%16, the same k; D element (4*(l/16) + i, l%16) in reg i.
+  __device__ static inline f32x4 mfma16(V8 a, V8 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+  }
 };
 
 template <>
@@ -41,6 +46,9 @@ struct Dt<1> {
   __device__ static inline T from_d(double x) { return static_cast<T>(x); }
   __device__ static inline f32x16 mfma32(V8 a, V8 b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+  }
+  __device__ static inline f32x4 mfma16(V8 a, V8 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
   }
 };
 

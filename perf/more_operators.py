@@ -278,9 +278,8 @@ def _run_own(st):
     if op == "sort":
         order, place, bounds = F.adapter_sort(st["ids"], c["n"])
         return {"order": order, "place": place, "bounds": bounds}
-    order, place = st["order"], st["place"]
-    xs = F.adapter_gather(st["x"], order, place)
-    y = F.adapter_combine(st["rows"], st["w"], order, place, st["base"])
+    xs = F.adapter_gather(st["x"], st["place"])
+    y = F.adapter_combine(st["rows"], st["w"], st["place"], st["base"])
     if not c["train"]:
         return {"xs": xs, "y": y}
     (dx,) = torch.autograd.grad(xs, (st["x"],), st["dx_rows"])
