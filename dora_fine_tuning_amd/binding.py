@@ -48,6 +48,17 @@ EXPORTS = (
     "dora_q8_lora_compose_bwd",
     "dora_q8_grad_a_workspace_bytes",
     "dora_q8_grad_a",
+    "dora_q4_pack_weight",
+    "dora_q4_unpack_weight",
+    "dora_q4_linear_workspace_bytes",
+    "dora_q4_linear_fwd",
+    "dora_q4_linear_bwd_workspace_bytes",
+    "dora_q4_linear_bwd",
+    "dora_adapter_sort_workspace_bytes",
+    "dora_adapter_sort",
+    "dora_adapter_gather",
+    "dora_adapter_combine",
+    "dora_adapter_combine_bwd",
     "dora_last_error",
     "dora_version",
 )
@@ -108,6 +119,24 @@ def _load() -> ctypes.CDLL:
     lib.dora_q8_lora_compose_bwd.restype = i32
     lib.dora_q8_grad_a.argtypes = [vp, vp, vp, i64, i64, i64, i32, vp, vp, sz, vp]
     lib.dora_q8_grad_a.restype = i32
+    lib.dora_q4_pack_weight.argtypes = [vp, i64, i64, i32, vp, vp, vp]
+    lib.dora_q4_unpack_weight.argtypes = [vp, vp, i64, i64, i32, vp, vp]
+    lib.dora_q4_pack_weight.restype = lib.dora_q4_unpack_weight.restype = i32
+    for name in ("dora_q4_linear_workspace_bytes", "dora_q4_linear_bwd_workspace_bytes",
+                 "dora_adapter_sort_workspace_bytes"):
+        getattr(lib, name).argtypes = [i64, i64, i64]
+        getattr(lib, name).restype = sz
+    for name in ("dora_q4_linear_fwd", "dora_q4_linear_bwd"):
+        getattr(lib, name).argtypes = [vp, vp, vp, i64, i64, i64, i32, vp, vp, sz, vp]
+        getattr(lib, name).restype = i32
+    lib.dora_adapter_sort.argtypes = [vp, i32, i64, i64, i64, vp, vp, vp, vp, sz, vp]
+    lib.dora_adapter_sort.restype = i32
+    lib.dora_adapter_gather.argtypes = [vp, vp, i64, i64, i64, i32, vp, vp]
+    lib.dora_adapter_gather.restype = i32
+    lib.dora_adapter_combine.argtypes = [vp, vp, vp, vp, i64, i64, i64, i32, vp, vp]
+    lib.dora_adapter_combine.restype = i32
+    lib.dora_adapter_combine_bwd.argtypes = [vp, vp, vp, vp, i64, i64, i64, i32, vp, vp, vp]
+    lib.dora_adapter_combine_bwd.restype = i32
     lib.dora_last_error.argtypes = []
     lib.dora_last_error.restype = ctypes.c_char_p
     lib.dora_version.argtypes = []
@@ -594,3 +623,156 @@ def dora_q8_grad_a(dh, xq, xe, in_: int):
         _check(LIB.dora_q8_grad_a(_ptr(dh), _ptr(xq), _ptr(xe), T, in_, r, code, _ptr(d_A), _ptr(ws), need,
                                   _raw_stream(dev)))
     return d_A
+
+
+# ------------------------------------------------------------ the frozen weight in 4 bits
+#
+# A packed weight is a pair (q, e) of uint8 tensors in the layout of include/dora.h.
+
+Q4_ROWS, Q4_COLS = 32, 64  # a tile
+
+
+def q4_weight_shapes(out: int, in_: int):
+    """Shapes of (q, e) for a packed weight [out x in]."""
+    tiles = (-(-out // Q4_ROWS), -(-in_ // Q4_COLS))
+    return (*tiles, 1024), (*tiles, 64)
+
+
+def _q4_packed(q, e, shapes, device):
+    if (q.shape != shapes[0] or e.shape != shapes[1] or q.dtype != torch.uint8 or e.dtype != torch.uint8
+            or q.device != device or e.device != device or not q.is_contiguous() or not e.is_contiguous()):
+        _matrix(q, "the packed weight", shapes[0], torch.uint8, device)  # says which it is
+        _matrix(e, "the packed weight's exponents", shapes[1], torch.uint8, device)
+    if q.data_ptr() % 16 or e.data_ptr() % 16:
+        raise ValueError("the packed weight and its exponents must be 16-byte aligned")
+
+
+def dora_q4_pack_weight(W):
+    """(q, e): the weight W [out x in] in 4-bit blocks of 32 columns."""
+    code = _code(W)
+    out, in_ = W.shape
+    _matrix(W, "W", (out, in_))
+    with _on_device(W.device):
+        qs, es = q4_weight_shapes(out, in_)
+        q = torch.empty(qs, dtype=torch.uint8, device=W.device)
+        e = torch.empty(es, dtype=torch.uint8, device=W.device)
+        _check(LIB.dora_q4_pack_weight(_ptr(W), out, in_, code, _ptr(q), _ptr(e), _raw_stream(W.device)))
+    return q, e
+
+
+def dora_q4_unpack_weight(q, e, rows: int, cols: int, dtype):
+    """The values of the first ``rows`` rows of a packed weight of ``cols`` columns, in dtype."""
+    code, dev = _dtype_code(dtype), _on_gpu(q, "q")
+    if not 0 <= rows <= q.shape[0] * Q4_ROWS:
+        raise ValueError(f"rows {rows} out of range of a packed weight of {q.shape[0] * Q4_ROWS}")
+    _q4_packed(q, e, q4_weight_shapes(q.shape[0] * Q4_ROWS, cols), dev)
+    with _on_device(dev):
+        W = torch.empty((rows, cols), dtype=dtype, device=dev)
+        _check(LIB.dora_q4_unpack_weight(_ptr(q), _ptr(e), rows, cols, code, _ptr(W), _raw_stream(dev)))
+    return W
+
+
+def dora_q4_linear_fwd(x, q, e, out: int):
+    """y [T x out] = x W^T from x [T x in] and a packed weight [out x in]."""
+    code = _code(x)
+    (T, in_), dev = x.shape, x.device
+    _matrix(x, "x", (T, in_))
+    _q4_packed(q, e, q4_weight_shapes(out, in_), dev)
+    x = _aligned(x)
+    with _on_device(dev):
+        y = torch.empty((T, out), dtype=x.dtype, device=dev)
+        need = int(LIB.dora_q4_linear_workspace_bytes(T, out, in_))
+        ws = _workspace(need, dev)
+        _check(LIB.dora_q4_linear_fwd(_ptr(x), _ptr(q), _ptr(e), T, out, in_, code, _ptr(y), _ptr(ws), need,
+                                      _raw_stream(dev)))
+    return y
+
+
+def dora_q4_linear_bwd(g, q, e, in_: int):
+    """dx [T x in] = g W from g [T x out] and a packed weight [out x in]."""
+    code = _code(g)
+    (T, out), dev = g.shape, g.device
+    _matrix(g, "g", (T, out))
+    _q4_packed(q, e, q4_weight_shapes(out, in_), dev)
+    g = _aligned(g)
+    with _on_device(dev):
+        dx = torch.empty((T, in_), dtype=g.dtype, device=dev)
+        need = int(LIB.dora_q4_linear_bwd_workspace_bytes(T, out, in_))
+        ws = _workspace(need, dev)
+        _check(LIB.dora_q4_linear_bwd(_ptr(g), _ptr(q), _ptr(e), T, out, in_, code, _ptr(dx), _ptr(ws), need,
+                                      _raw_stream(dev)))
+    return dx
+
+
+# ------------------------------------------------------------ tokens sorted by adapter
+
+
+def _shape2(t, name):
+    if t.dim() != 2:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected two dimensions")
+    return t.shape
+
+
+def dora_adapter_sort(ids, adapters: int):
+    """(order [T k], place [T x k], bounds [adapters + 1]), int32, of ids [T x k] (int64 or int32)."""
+    if ids.dtype not in (torch.int64, torch.int32):
+        raise ValueError(f"ids are {ids.dtype}; int64 and int32 are taken")
+    dev = _on_gpu(ids, "ids")
+    T, k = _shape2(ids, "ids")
+    _matrix(ids, "ids", (T, k))
+    with _on_device(dev):
+        order = torch.empty(T * k, dtype=torch.int32, device=dev)
+        place = torch.empty((T, k), dtype=torch.int32, device=dev)
+        bounds = torch.empty(max(adapters, 0) + 1, dtype=torch.int32, device=dev)
+        need = int(LIB.dora_adapter_sort_workspace_bytes(T, k, adapters))
+        ws = _workspace(need, dev)
+        _check(LIB.dora_adapter_sort(_ptr(ids), ids.element_size(), T, k, adapters, _ptr(order), _ptr(place),
+                                     _ptr(bounds), _ptr(ws), need, _raw_stream(dev)))
+    return order, place, bounds
+
+
+def dora_adapter_gather(x, place):
+    """rows [T k x D]: x[t] at the row of each of its slots, zeros at those without an adapter."""
+    code = _code(x)
+    (T, D), dev = _shape2(x, "x"), x.device
+    k = _shape2(place, "place")[1]
+    _matrix(x, "x", (T, D))
+    _matrix(place, "place", (T, k), torch.int32, dev)
+    with _on_device(dev):
+        rows = torch.empty((T * k, D), dtype=x.dtype, device=dev)
+        _check(LIB.dora_adapter_gather(_ptr(x), _ptr(place), T, k, D, code, _ptr(rows), _raw_stream(dev)))
+    return rows
+
+
+def dora_adapter_combine(rows, weights, place, base=None):
+    """y [T x D]: base (or zeros) plus each token's rows times their weights (fp32 [T x k], or None for ones)."""
+    code = _code(rows)
+    (T, k), D, dev = _shape2(place, "place"), _shape2(rows, "rows")[1], rows.device
+    _matrix(rows, "rows", (T * k, D))
+    _matrix(place, "place", (T, k), torch.int32, dev)
+    if weights is not None:
+        _matrix(weights, "weights", (T, k), torch.float32, dev)
+    if base is not None:
+        _matrix(base, "base", (T, D), rows.dtype, dev)
+    with _on_device(dev):
+        y = torch.empty((T, D), dtype=rows.dtype, device=dev)
+        _check(LIB.dora_adapter_combine(_ptr(rows), _ptr(weights), _ptr(place), _ptr(base), T, k, D, code, _ptr(y),
+                                        _raw_stream(dev)))
+    return y
+
+
+def dora_adapter_combine_bwd(dy, rows, weights, place, want_rows: bool = True, want_weights: bool = True):
+    """(d_rows [T k x D], d_weights [T x k] fp32) of the combination, None where not wanted."""
+    code = _code(dy)
+    (T, D), k, dev = _shape2(dy, "dy"), _shape2(place, "place")[1], dy.device
+    _matrix(dy, "dy", (T, D))
+    _matrix(rows, "rows", (T * k, D), dy.dtype, dev)
+    _matrix(place, "place", (T, k), torch.int32, dev)
+    if weights is not None:
+        _matrix(weights, "weights", (T, k), torch.float32, dev)
+    with _on_device(dev):
+        d_rows = torch.empty((T * k, D), dtype=dy.dtype, device=dev) if want_rows else None
+        d_w = torch.empty((T, k), dtype=torch.float32, device=dev) if want_weights else None
+        _check(LIB.dora_adapter_combine_bwd(_ptr(dy), _ptr(rows), _ptr(weights), _ptr(place), T, k, D, code,
+                                            _ptr(d_rows), _ptr(d_w), _raw_stream(dev)))
+    return d_rows, d_w

@@ -1,0 +1,117 @@
+// C ABI of the 4-bit weight: argument validation, workspace queries, launch.
+// Every check runs before the first HIP call, so invalid calls touch no device.
+#include "../../include/dora.h"
+#include "abi_common.hpp"
+#include "q4_common.hpp"
+
+using namespace dora::abi;
+
+namespace {
+
+// Sizes up to here keep every product of two of them, and every byte count,
+// inside 63 bits, and 256 rows of 16-bit values inside one buffer resource.
+constexpr int64_t kMaxRows = int64_t(1) << 31;
+constexpr int64_t kMaxCols = (int64_t(1) << 22) - 128;
+
+int check_sizes(const char* fn, int dtype, int64_t T, int64_t out, int64_t in) {
+  if (!valid_dtype(dtype)) return fail(DORA_UNSUPPORTED, "%s: unknown dtype %d", fn, dtype);
+  if (T < 0 || out < 0 || in < 0)
+    return fail(DORA_INVALID_ARG, "%s: negative size (%lld, %lld, %lld)", fn, (long long)T, (long long)out,
+                (long long)in);
+  if (T >= kMaxRows || out > kMaxCols || in > kMaxCols)
+    return fail(DORA_UNSUPPORTED, "%s: sizes (%lld, %lld, %lld) beyond 2^31 rows or 2^22 columns", fn, (long long)T,
+                (long long)out, (long long)in);
+  if (dora::q4_ceil(out, dora::kQ4Rows) * dora::q4_ceil(in, dora::kQ4Cols) > INT32_MAX)
+    return fail(DORA_UNSUPPORTED, "%s: a weight of %lld x %lld has more tiles than one launch holds", fn,
+                (long long)out, (long long)in);
+  return DORA_OK;
+}
+
+size_t mat16(int64_t rows, int64_t cols) { return static_cast<size_t>(rows) * cols * 2; }
+size_t tiles(int64_t out, int64_t in) {
+  return static_cast<size_t>(dora::q4_ceil(out, dora::kQ4Rows)) * dora::q4_ceil(in, dora::kQ4Cols);
+}
+size_t weight_q(int64_t out, int64_t in) { return tiles(out, in) * dora::kQ4TileQ; }
+size_t weight_e(int64_t out, int64_t in) { return tiles(out, in) * dora::kQ4TileE; }
+
+int weight_ptrs(const char* fn, const void* q, const void* e) {
+  if (!q || !e) return fail(DORA_INVALID_ARG, "%s: the packed weight or its exponents are NULL", fn);
+  if (!aligned16(q) || !aligned16(e))
+    return fail(DORA_INVALID_ARG, "%s: the packed weight and its exponents need 16-byte alignment", fn);
+  return DORA_OK;
+}
+
+size_t workspace(int64_t T, int64_t out, int64_t in, bool trans) {
+  if (T <= 0 || out <= 0 || in <= 0 || T >= kMaxRows || out > kMaxCols || in > kMaxCols) return 0;
+  return dora::q4_gemm_workspace_bytes(T, out, in, trans);
+}
+
+int gemm_call(const char* fn, const void* x, const void* q, const void* e, int64_t T, int64_t out, int64_t in,
+              int dtype, bool trans, void* y, void* ws, size_t ws_bytes, hipStream_t stream) {
+  if (int st = check_sizes(fn, dtype, T, out, in)) return st;
+  const int64_t N = trans ? in : out, K = trans ? out : in;
+  if (T == 0 || N == 0) return ok();
+  if (!y) return fail(DORA_INVALID_ARG, "%s: the output is NULL", fn);
+  if (!aligned(y, 2)) return fail(DORA_INVALID_ARG, "%s: the output needs 2-byte alignment", fn);
+  if (K > 0) {
+    if (!x || !aligned16(x)) return fail(DORA_INVALID_ARG, "%s: the rows are NULL or not 16-byte aligned", fn);
+    if (int st = weight_ptrs(fn, q, e)) return st;
+  }
+  const size_t need = workspace(T, out, in, trans);
+  if (ws_bytes < need) return fail(DORA_INVALID_ARG, "%s: workspace of %zu bytes, %zu needed", fn, ws_bytes, need);
+  if (need > 0 && (!ws || !aligned16(ws)))
+    return fail(DORA_INVALID_ARG, "%s: workspace is NULL or not 16-byte aligned", fn);
+  const Range outs[2] = {{y, mat16(T, N)}, {ws, need}};
+  const Range ins[3] = {{x, mat16(T, K)}, {q, weight_q(out, in)}, {e, weight_e(out, in)}};
+  if (outputs_overlap(outs, ins)) return fail(DORA_INVALID_ARG, "%s: an output overlaps another argument", fn);
+  if (dora::q4_gemm_max_grid(T, out, in, trans) > INT32_MAX)
+    return fail(DORA_UNSUPPORTED, "%s: T=%lld out=%lld in=%lld needs more workgroups than one launch holds", fn,
+                (long long)T, (long long)out, (long long)in);
+  const dora::Q4GemmArgs a{x, q, e, T, out, in, dtype, trans, y, ws, stream};
+  return hip_status(dora::launch_q4_gemm(a), fn);
+}
+
+}  // namespace
+
+extern "C" {
+
+int dora_q4_pack_weight(const void* W, int64_t out, int64_t in, int dtype, void* q, void* e, hipStream_t stream) {
+  const char* fn = "dora_q4_pack_weight";
+  if (int st = check_sizes(fn, dtype, 0, out, in)) return st;
+  if (out == 0 || in == 0) return ok();
+  if (!W || !aligned(W, 2)) return fail(DORA_INVALID_ARG, "%s: the weight is NULL or not 2-byte aligned", fn);
+  if (int st = weight_ptrs(fn, q, e)) return st;
+  const Range outs[2] = {{q, weight_q(out, in)}, {e, weight_e(out, in)}};
+  const Range ins[1] = {{W, mat16(out, in)}};
+  if (outputs_overlap(outs, ins)) return fail(DORA_INVALID_ARG, "%s: an output overlaps another argument", fn);
+  return hip_status(dora::launch_q4_pack(W, out, in, dtype, in % 8 == 0 && aligned16(W), q, e, stream), fn);
+}
+
+int dora_q4_unpack_weight(const void* q, const void* e, int64_t rows, int64_t cols, int dtype, void* W,
+                          hipStream_t stream) {
+  const char* fn = "dora_q4_unpack_weight";
+  if (int st = check_sizes(fn, dtype, 0, rows, cols)) return st;
+  if (rows == 0 || cols == 0) return ok();
+  if (!W || !aligned(W, 2)) return fail(DORA_INVALID_ARG, "%s: the output is NULL or not 2-byte aligned", fn);
+  if (int st = weight_ptrs(fn, q, e)) return st;
+  const Range outs[1] = {{W, mat16(rows, cols)}};
+  const Range ins[2] = {{q, weight_q(rows, cols)}, {e, weight_e(rows, cols)}};
+  if (outputs_overlap(outs, ins)) return fail(DORA_INVALID_ARG, "%s: the output overlaps an input", fn);
+  return hip_status(dora::launch_q4_unpack(q, e, rows, cols, dtype, cols % 8 == 0 && aligned16(W), W, stream), fn);
+}
+
+size_t dora_q4_linear_workspace_bytes(int64_t T, int64_t out, int64_t in) { return workspace(T, out, in, false); }
+
+int dora_q4_linear_fwd(const void* x, const void* q, const void* e, int64_t T, int64_t out, int64_t in, int dtype,
+                       void* y, void* ws, size_t ws_bytes, hipStream_t stream) {
+  return gemm_call("dora_q4_linear_fwd", x, q, e, T, out, in, dtype, false, y, ws, ws_bytes, stream);
+}
+
+size_t dora_q4_linear_bwd_workspace_bytes(int64_t T, int64_t out, int64_t in) { return workspace(T, out, in, true); }
+
+int dora_q4_linear_bwd(const void* g, const void* q, const void* e, int64_t T, int64_t out, int64_t in, int dtype,
+                       void* dx, void* ws, size_t ws_bytes, hipStream_t stream) {
+  return gemm_call("dora_q4_linear_bwd", g, q, e, T, out, in, dtype, true, dx, ws, ws_bytes, stream);
+}
+
+}  // extern "C"

@@ -532,19 +532,29 @@ _Q8_LIB = torch.library.Library("dora_amd", "FRAGMENT")
 _BELOW_AUTOGRAD = torch._C._after_autograd_keyset
 
 
+def _refuse_tangents(name, args):
+    if fwad._current_level >= 0:
+        for a in args:
+            if isinstance(a, Tensor) and fwad.unpack_dual(a).tangent is not None:
+                raise RuntimeError(f"{name} has no forward-mode derivative")
+
+
 def _refuse_gradients(name, args):
     grad, duals = torch.is_grad_enabled(), fwad._current_level >= 0
     if grad or duals:
         for a in args:
             if isinstance(a, Tensor) and (grad and a.requires_grad
                                           or duals and fwad.unpack_dual(a).tangent is not None):
-                raise RuntimeError(f"{name} has no gradient of its own: pass detached tensors, or use q8_layer")
+                hint = ", or use q8_layer" if name.startswith("q8_") else ""
+                raise RuntimeError(f"{name} has no gradient of its own: pass detached tensors{hint}")
 
 
-def _q8_kernel(name):
+def _q8_kernel(name, gradient=None):
     """Register a function as the GPU kernel of the operator ``name``, the eager
     form of the same name as its CPU kernel (and for a call the library refuses
-    with DORA_UNSUPPORTED); the operator takes its place."""
+    with DORA_UNSUPPORTED); the operator takes its place.  ``gradient``, where the
+    operator has one, is an autograd function: it is given the call below autograd
+    and the operator's arguments."""
 
     def register(fn):
         eager = globals()["_eager_" + name]
@@ -561,7 +571,14 @@ def _q8_kernel(name):
         direct = {}  # by a key set's bits: the device's kernel where nothing else is left of it, else None
 
         def autograd(keyset, *args):
+            if gradient is not None and torch.is_grad_enabled() and any(
+                    isinstance(a, Tensor) and a.requires_grad for a in args):
+                _refuse_tangents(name, args)
+                return gradient.apply(functools.partial(below, keyset), *args)
             _refuse_gradients(name, args)
+            return below(keyset, *args)
+
+        def below(keyset, *args):
             bits = keyset.raw_repr()
             if bits not in direct:
                 direct[bits] = kernels.get((keyset & _BELOW_AUTOGRAD).highestPriorityTypeId())
@@ -731,14 +748,34 @@ def _slabs(wq, we, out, in_, dtype):
         yield slice(i, i + n), q8_unpack_weight(wq[rows], we[blocks], n, in_, dtype)
 
 
+def _norm_of_slabs(slabs, A, B, base_sq, s):
+    """``weight_norm_cached`` of a weight that comes in slabs of rows."""
+    n = torch.empty(B.shape[0], dtype=torch.float32, device=B.device)
+    for rows, W in slabs:
+        n[rows] = weight_norm_cached(W, A, B[rows], base_sq[rows], s)
+    return n
+
+
+def _norm_backward_of_slabs(slabs, A, B, norm, d_norm, s):
+    """``weight_norm_backward`` of a weight that comes in slabs of rows: (d_A, d_B),
+    the slabs' parts of d_A added in fp32 and rounded once."""
+    A, B, norm, d_norm = A.contiguous(), B.contiguous(), norm.contiguous().float(), d_norm.contiguous().float()
+    d_A, d_B = torch.zeros(A.shape, dtype=torch.float32, device=A.device), torch.empty_like(B)
+    for rows, W in slabs:
+        if _kernels_take(W, A, B):
+            d_B[rows] = binding.dora_norm_bwd_slab(W, A, B[rows], norm[rows], d_norm[rows], s, d_A, rows.start > 0)
+        else:
+            a, b = _eager_weight_norm_backward(W, A.float(), B[rows].float(), norm[rows], d_norm[rows], s)
+            d_A += a
+            d_B[rows] = b.to(B.dtype)
+    return d_A.to(A.dtype), d_B
+
+
 @torch.library.custom_op("dora_amd::q8_weight_norm", mutates_args=())
 @_without_autocast
 def q8_weight_norm(wq: Tensor, we: Tensor, A: Tensor, B: Tensor, base_sq: Tensor, s: float) -> Tensor:
     """``weight_norm_cached`` of a packed weight."""
-    n = torch.empty(B.shape[0], dtype=torch.float32, device=B.device)
-    for rows, W in _slabs(wq, we, B.shape[0], A.shape[1], A.dtype):
-        n[rows] = weight_norm_cached(W, A, B[rows], base_sq[rows], s)
-    return n
+    return _norm_of_slabs(_slabs(wq, we, B.shape[0], A.shape[1], A.dtype), A, B, base_sq, s)
 
 
 @q8_weight_norm.register_fake
@@ -750,18 +787,8 @@ def _q8_weight_norm_fake(wq, we, A, B, base_sq, s):
 @_without_autocast
 def q8_weight_norm_backward(wq: Tensor, we: Tensor, A: Tensor, B: Tensor, norm: Tensor, d_norm: Tensor,
                             s: float) -> tuple[Tensor, Tensor]:
-    """``weight_norm_backward`` of a packed weight: (d_A, d_B), the slabs' parts
-    of d_A added in fp32 and rounded once."""
-    A, B, norm, d_norm = A.contiguous(), B.contiguous(), norm.contiguous().float(), d_norm.contiguous().float()
-    d_A, d_B = torch.zeros(A.shape, dtype=torch.float32, device=A.device), torch.empty_like(B)
-    for rows, W in _slabs(wq, we, B.shape[0], A.shape[1], A.dtype):
-        if _kernels_take(W, A, B):
-            d_B[rows] = binding.dora_norm_bwd_slab(W, A, B[rows], norm[rows], d_norm[rows], s, d_A, rows.start > 0)
-        else:
-            a, b = _eager_weight_norm_backward(W, A.float(), B[rows].float(), norm[rows], d_norm[rows], s)
-            d_A += a
-            d_B[rows] = b.to(B.dtype)
-    return d_A.to(A.dtype), d_B
+    """``weight_norm_backward`` of a packed weight."""
+    return _norm_backward_of_slabs(_slabs(wq, we, B.shape[0], A.shape[1], A.dtype), A, B, norm, d_norm, s)
 
 
 @q8_weight_norm_backward.register_fake
@@ -790,11 +817,16 @@ def q8_layer(x: Tensor, A: Tensor, B: Tensor, mag: Tensor, norm: Tensor, weight:
              s: float) -> tuple[Tensor, Tensor, Tensor, Tensor, Tensor, Tensor]:
     """The layer on x [T x in] with 8-bit checkpoints: (y, then what the backward
     reads, itself without a gradient: x and base packed, and h).  ``weight`` is W0 [out x in] in 16 bits, or,
-    with its exponents ``we``, packed: then both products with W0 run on packed
-    operands, x's being the checkpoint itself.  Its matrices have one type (under
+    with its exponents ``we``, packed in 8 bits: then both products with W0 run on packed
+    operands, x's being the checkpoint itself; or packed in 4 bits (uint8).  Its matrices have one type (under
     autocast they are cast to its); its backward has no backward."""
     xq, xe = q8_pack(x)
-    base = F.linear(x, weight) if we is None else q8_linear(xq, xe, weight, we, B.shape[0], x.dtype)
+    if we is None:
+        base = F.linear(x, weight)
+    elif weight.dtype == torch.uint8:
+        base = q4_linear(x, weight, we, B.shape[0])
+    else:
+        base = q8_linear(xq, xe, weight, we, B.shape[0], x.dtype)
     h = F.linear(x, A)
     y = lora_compose(base, h, B, mag, norm, s, True)
     bq, be = q8_pack(base)
@@ -821,13 +853,13 @@ def _q8_layer_grad(ctx, dy, *_):
     if dy is None:  # a later function gave no gradient: zeros, as autograd hands them to the 16-bit layer
         dy = h.new_zeros((h.shape[0], B.shape[0]))
     dx = None
-    if need[0] and we is not None:
+    if need[0] and we is not None and weight.dtype != torch.uint8:
         dq, de, d_B, d_mag = q8_lora_compose_backward_packed(dy, bq, be, h, B, mag, norm, s, True)
         dx = q8_linear_backward(dq, de, weight, we, in_, dy.dtype)
     else:
         d_base, d_B, d_mag = q8_lora_compose_backward(dy, bq, be, h, B, mag, norm, s, True, bool(need[0]))
         if need[0]:
-            dx = d_base @ weight
+            dx = d_base @ weight if we is None else q4_linear_backward(d_base, weight, we, in_)
     d_A = None
     if need[0] or need[1]:
         gsB = ((mag / norm) * s)[:, None] * B.float()
@@ -850,6 +882,417 @@ def _q8_layer_autocast(x, A, B, mag, norm, weight, we, s):
 
 for _key in ("AutocastCUDA", "AutocastCPU"):
     _Q8_LIB.impl("q8_layer", _q8_layer_autocast, _key)
+
+
+# ------------------------------------------------------------ the frozen weight in 4 bits
+#
+# A packed weight is a pair (q, e) of uint8 tensors, tiles of 32 rows x 64 columns
+# laid out as include/dora.h says.  The rows it is multiplied with stay in 16 bits.
+
+
+def _q4_where(device) -> tuple[Tensor, Tensor]:
+    """Byte positions within a tile of each row's two blocks (16 bytes each) and of their exponents."""
+    r, b = torch.arange(32, device=device)[:, None], torch.arange(2, device=device)[None, :]
+    g, i = r // 8, r % 8
+    at = 128 * i + 32 * g + 16 * (b ^ (i // 2 % 2))
+    return (at[:, :, None] + torch.arange(16, device=device)).flatten(), (32 * b + 8 * g + 2 * (i % 4) + i // 4).flatten()
+
+
+def _q4_values(q, e, rows, cols) -> Tensor:
+    """The fp32 values of the first rows of a packed weight, which has to be laid out as the kernels ask for."""
+    shapes = binding.q4_weight_shapes(q.shape[0] * binding.Q4_ROWS, cols)
+    for t, what, shape in ((q, "the packed weight", shapes[0]), (e, "the packed weight's exponents", shapes[1])):
+        if tuple(t.shape) != shape or t.dtype != torch.uint8:
+            raise ValueError(f"{what} is {tuple(t.shape)} in {t.dtype}, expected {shape} in {torch.uint8}")
+    if not 0 <= rows <= q.shape[0] * binding.Q4_ROWS:
+        raise ValueError(f"rows {rows} out of range of a packed weight of {q.shape[0] * binding.Q4_ROWS}")
+    at, ea = _q4_where(q.device)
+    a, b = q.shape[:2]
+    byte = q[:, :, at].reshape(a, b, 32, 2, 16)
+    eb = e[:, :, ea].reshape(a, b, 32, 2).to(torch.int32)
+    c = torch.stack((byte & 15, byte >> 4), dim=5).reshape(a, b, 32, 2, 32).to(torch.int32)
+    grid = torch.tensor([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0], device=q.device)
+    scale = torch.where(eb == 255, torch.full((), math.nan, device=q.device), _exp2i((eb - 127).clamp(-126, 127)))
+    v = torch.cat((grid, -grid))[c] * scale[..., None]
+    return v.transpose(1, 2).reshape(a * 32, b * 64)[:rows, :cols]
+
+
+def _q4_rows(q, out):
+    """Refuse a packed weight of another number of row tiles."""
+    if q.dim() != 3 or q.shape[0] != -(-out // binding.Q4_ROWS):
+        raise ValueError(f"the packed weight is {tuple(q.shape)}, not one of {out} rows")
+
+
+@_q8_eager
+def _eager_q4_pack_weight(W):
+    o, i = W.shape
+    qs, es = binding.q4_weight_shapes(o, i)
+    q, e = W.new_empty(qs, dtype=torch.uint8), W.new_empty(es, dtype=torch.uint8)
+    if W.numel() == 0:
+        return q, e
+    v = F.pad(W.float(), (0, qs[1] * 64 - i, 0, qs[0] * 32 - o)).reshape(qs[0], 32, qs[1], 2, 32)
+    amax = v.abs().amax(dim=4)
+    bad = ~torch.isfinite(v).all(dim=4)
+    bits = torch.where(bad, torch.zeros_like(amax), amax).view(torch.int32)  # 7 = 1.75 * 2^2
+    k = ((bits >> 23) - 127 - 2 + ((bits & 0x7FFFFF) > 0x600000).to(torch.int32)).clamp(-23, 13)
+    s = v * _exp2i(-k)[..., None]
+    a = s.abs()
+    code = torch.zeros(v.shape, dtype=torch.uint8, device=v.device)
+    for border, even_above in ((0.25, 0), (0.75, 1), (1.25, 0), (1.75, 1), (2.5, 0), (3.5, 1), (5.0, 0)):
+        code += (a >= border) if even_above else (a > border)
+    code = torch.where(bad[..., None], torch.zeros_like(code), code | (torch.signbit(s).to(torch.uint8) << 3))
+    at, ea = _q4_where(W.device)
+    q[:, :, at] = (code[..., 0::2] | (code[..., 1::2] << 4)).transpose(1, 2).reshape(qs[0], qs[1], 1024)
+    e[:, :, ea] = torch.where(bad, torch.full_like(k, 255), k + 127).to(torch.uint8).transpose(1, 2).reshape(es)
+    return q, e
+
+
+@_q8_eager
+def _eager_q4_unpack_weight(q, e, rows, cols, dtype):
+    return _q4_values(q, e, rows, cols).to(dtype)
+
+
+@_q8_eager
+def _eager_q4_linear(x, q, e, out_features):
+    _q4_rows(q, out_features)
+    return (x.float() @ _q4_values(q, e, out_features, x.shape[1]).t()).to(x.dtype)
+
+
+@_q8_eager
+def _eager_q4_linear_backward(g, q, e, in_features):
+    _q4_rows(q, g.shape[1])
+    return (g.float() @ _q4_values(q, e, g.shape[1], in_features)).to(g.dtype)
+
+
+class _Q4Linear(torch.autograd.Function):
+    """y = x W^T: W is frozen, and the gradient of x is the other product."""
+
+    @staticmethod
+    def forward(ctx, below, x, q, e, out_features):
+        ctx.save_for_backward(q, e)
+        ctx.in_features = x.shape[1]
+        return below(x, q, e, out_features)
+
+    @staticmethod
+    def backward(ctx, dy):
+        return None, q4_linear_backward(dy, *ctx.saved_tensors, ctx.in_features), None, None, None
+
+
+class _Q4LinearBackward(torch.autograd.Function):
+    """dx = g W, whose gradient of g is the first product again."""
+
+    @staticmethod
+    def forward(ctx, below, g, q, e, in_features):
+        ctx.save_for_backward(q, e)
+        ctx.out_features = g.shape[1]
+        return below(g, q, e, in_features)
+
+    @staticmethod
+    def backward(ctx, d):
+        return None, q4_linear(d, *ctx.saved_tensors, ctx.out_features), None, None, None
+
+
+@_q8_kernel("q4_pack_weight")
+def q4_pack_weight(W: Tensor) -> tuple[Tensor, Tensor]:
+    """(q, e): a weight [out x in] in 4-bit blocks of 32 columns of a row (once: it is frozen)."""
+    if not _kernels_take(W):
+        return _eager_q4_pack_weight(W)
+    return binding.dora_q4_pack_weight(W.contiguous())
+
+
+@torch.library.register_fake("dora_amd::q4_pack_weight")
+def _q4_pack_weight_fake(W):
+    qs, es = binding.q4_weight_shapes(W.shape[0], W.shape[1])
+    return W.new_empty(qs, dtype=torch.uint8), W.new_empty(es, dtype=torch.uint8)
+
+
+@_q8_kernel("q4_unpack_weight")
+def q4_unpack_weight(q: Tensor, e: Tensor, rows: int, cols: int, dtype: torch.dtype) -> Tensor:
+    """The values of the first ``rows`` rows of a packed weight, [rows x cols] in dtype (exact in 16 bits)."""
+    if dtype not in binding.DTYPE_CODE:
+        return _eager_q4_unpack_weight(q, e, rows, cols, dtype)
+    return binding.dora_q4_unpack_weight(q.contiguous(), e.contiguous(), rows, cols, dtype)
+
+
+@torch.library.register_fake("dora_amd::q4_unpack_weight")
+def _q4_unpack_weight_fake(q, e, rows, cols, dtype):
+    return q.new_empty((rows, cols), dtype=dtype)
+
+
+@_q8_kernel("q4_linear", gradient=_Q4Linear)
+def q4_linear(x: Tensor, q: Tensor, e: Tensor, out_features: int) -> Tensor:
+    """y [T x out] = x W^T from rows x [T x in] and a packed weight; differentiable in x."""
+    if not _kernels_take(x):
+        return _eager_q4_linear(x, q, e, out_features)
+    return binding.dora_q4_linear_fwd(x.contiguous(), q.contiguous(), e.contiguous(), out_features)
+
+
+@torch.library.register_fake("dora_amd::q4_linear")
+def _q4_linear_fake(x, q, e, out_features):
+    return x.new_empty((x.shape[0], out_features))
+
+
+@_q8_kernel("q4_linear_backward", gradient=_Q4LinearBackward)
+def q4_linear_backward(g: Tensor, q: Tensor, e: Tensor, in_features: int) -> Tensor:
+    """dx [T x in] = g W from g [T x out] and the same packed weight; differentiable in g."""
+    if not _kernels_take(g):
+        return _eager_q4_linear_backward(g, q, e, in_features)
+    return binding.dora_q4_linear_bwd(g.contiguous(), q.contiguous(), e.contiguous(), in_features)
+
+
+@torch.library.register_fake("dora_amd::q4_linear_backward")
+def _q4_linear_backward_fake(g, q, e, in_features):
+    return g.new_empty((g.shape[0], in_features))
+
+
+def _q4_linear_autocast(x, q, e, out_features):
+    return _without_autocast(q4_linear)(*_autocast(x), q, e, out_features)
+
+
+for _key in ("AutocastCUDA", "AutocastCPU"):
+    _Q8_LIB.impl("q4_linear", _q4_linear_autocast, _key)
+
+
+def _q4_slabs(q, e, out, in_, dtype):
+    """As ``_slabs``, of a weight in 4 bits."""
+    for i in range(0, out, _Q8_SLAB):
+        n = min(_Q8_SLAB, out - i)
+        tiles = slice(i // binding.Q4_ROWS, -(-(i + n) // binding.Q4_ROWS))
+        yield slice(i, i + n), q4_unpack_weight(q[tiles], e[tiles], n, in_, dtype)
+
+
+@torch.library.custom_op("dora_amd::q4_weight_norm", mutates_args=())
+@_without_autocast
+def q4_weight_norm(q: Tensor, e: Tensor, A: Tensor, B: Tensor, base_sq: Tensor, s: float) -> Tensor:
+    """``weight_norm_cached`` of a weight packed in 4 bits."""
+    return _norm_of_slabs(_q4_slabs(q, e, B.shape[0], A.shape[1], A.dtype), A, B, base_sq, s)
+
+
+@q4_weight_norm.register_fake
+def _q4_weight_norm_fake(q, e, A, B, base_sq, s):
+    return B.new_empty((B.shape[0],), dtype=torch.float32)
+
+
+@torch.library.custom_op("dora_amd::q4_weight_norm_backward", mutates_args=())
+@_without_autocast
+def q4_weight_norm_backward(q: Tensor, e: Tensor, A: Tensor, B: Tensor, norm: Tensor, d_norm: Tensor,
+                            s: float) -> tuple[Tensor, Tensor]:
+    """``weight_norm_backward`` of a weight packed in 4 bits."""
+    return _norm_backward_of_slabs(_q4_slabs(q, e, B.shape[0], A.shape[1], A.dtype), A, B, norm, d_norm, s)
+
+
+@q4_weight_norm_backward.register_fake
+def _q4_weight_norm_backward_fake(q, e, A, B, norm, d_norm, s):
+    return A.new_empty(A.shape), B.new_empty(B.shape)
+
+
+def _q4_norm_grad(ctx, d_norm):
+    q, e, A, B, n = ctx.saved_tensors
+    d_A, d_B = q4_weight_norm_backward(q, e, A, B, n, d_norm, ctx.s)
+    need = ctx.needs_input_grad
+    return None, None, d_A if need[2] else None, d_B if need[3] else None, None, None
+
+
+q4_weight_norm.register_autograd(_q4_norm_grad, setup_context=_q8_norm_setup)
+
+
+# ------------------------------------------------------------ tokens sorted by adapter
+#
+# Several adapters over one frozen weight: token t of a batch has k slots, each with
+# the number of an adapter or none.  adapter_sort gives every slot a row, adapter by
+# adapter (place, int32 [T x k]; the complement of the row for a slot without one);
+# adapter_gather and adapter_combine go to the rows and back.
+
+
+@_q8_eager
+def _eager_adapter_sort(ids, adapters):
+    if adapters < 0 or ids.dim() != 2:
+        raise ValueError(f"{adapters} adapters, ids of {ids.dim()} dimensions: expected ids [T x k]")
+    flat = ids.flatten().to(torch.int64)
+    has = (flat >= 0) & (flat < adapters)
+    key = torch.where(has, flat, torch.full_like(flat, adapters))
+    slots = torch.sort(key, stable=True).indices
+    row = torch.arange(flat.numel(), device=flat.device)
+    there = has[slots]
+    order = torch.where(there, slots, -1 - slots)
+    place = torch.empty_like(row)
+    place[slots] = torch.where(there, row, -1 - row)
+    count = torch.zeros(adapters + 1, dtype=torch.int64, device=flat.device).index_add_(0, key, torch.ones_like(key))
+    bounds = torch.cumsum(count, 0) - count
+    return order.to(torch.int32), place.to(torch.int32).reshape(ids.shape), bounds.to(torch.int32)
+
+
+def _rows_of(place, R):
+    """(row of each slot, R where it is out of range; whether it is a row of an adapter) as flat int64 and bool."""
+    p = place.flatten().to(torch.int64)
+    row = torch.where(p < 0, -1 - p, p)
+    return torch.where(row < R, row, torch.full_like(row, R)), (p >= 0) & (row < R)
+
+
+def _check_place(place, T, what):
+    if place.dim() != 2 or place.dtype != torch.int32 or place.shape[0] != T:
+        raise ValueError(f"place is {tuple(place.shape)} in {place.dtype}, expected int32 [{T} x k], as for {what}")
+
+
+@_q8_eager
+def _eager_adapter_gather(x, place):
+    _check_place(place, x.shape[0], "x")
+    R, k = place.numel(), place.shape[1]
+    row, has = _rows_of(place, R)
+    rows = x.new_zeros((R + 1, x.shape[1]))
+    v = x.repeat_interleave(k, dim=0)
+    rows[row] = torch.where(has[:, None], v, torch.zeros_like(v))
+    return rows[:R]
+
+
+def _slot_rows(rows, place):
+    """[T, k, D] in fp32: the rows of the slots, zeros for those without an adapter."""
+    row, has = _rows_of(place, rows.shape[0])
+    padded = F.pad(rows, (0, 0, 0, 1)).float()[row]
+    return torch.where(has[:, None], padded, torch.zeros_like(padded)).reshape(*place.shape, rows.shape[1])
+
+
+def _check_rows(rows, weights, place, base=None):
+    if rows.dim() != 2 or rows.shape[0] != place.numel():
+        raise ValueError(f"rows are {tuple(rows.shape)}, expected one for each of {place.numel()} slots")
+    if weights is not None and weights.shape != place.shape:
+        raise ValueError(f"weights are {tuple(weights.shape)}, expected {tuple(place.shape)}")
+    if base is not None and (tuple(base.shape) != (place.shape[0], rows.shape[1]) or base.dtype != rows.dtype):
+        raise ValueError(f"base is {tuple(base.shape)} in {base.dtype}, expected {(place.shape[0], rows.shape[1])} "
+                         f"in {rows.dtype}")
+
+
+@_q8_eager
+def _eager_adapter_combine(rows, weights, place, base):
+    _check_place(place, place.shape[0], "rows")
+    _check_rows(rows, weights, place, base)
+    v = _slot_rows(rows, place)
+    if weights is not None:
+        _, has = _rows_of(place, rows.shape[0])
+        w = torch.where(has.reshape(place.shape), weights.float(), torch.zeros_like(weights, dtype=torch.float32))
+        v = v * w[:, :, None]
+    y = v.sum(dim=1)
+    return (y if base is None else y + base.float()).to(rows.dtype)
+
+
+@_q8_eager
+def _eager_adapter_combine_backward(dy, rows, weights, place, want_rows, want_weights):
+    _check_place(place, dy.shape[0], "dy")
+    _check_rows(rows, weights, place)
+    R, (T, k) = place.numel(), place.shape
+    d = dy.float()
+    d_rows, d_w = dy.new_empty((0,)), dy.new_empty((0,), dtype=torch.float32)
+    if want_rows:
+        row, has = _rows_of(place, R)
+        v = d[:, None, :].expand(T, k, d.shape[1])
+        if weights is not None:
+            v = v * weights.float()[:, :, None]
+        v = v.reshape(R, d.shape[1])
+        d_rows = dy.new_zeros((R + 1, d.shape[1]))
+        d_rows[row] = torch.where(has[:, None], v, torch.zeros_like(v)).to(dy.dtype)
+        d_rows = d_rows[:R]
+    if want_weights:
+        _, has = _rows_of(place, R)
+        d_w = (d[:, None, :] * _slot_rows(rows, place)).sum(dim=2)
+        d_w = torch.where(has.reshape(place.shape), d_w, torch.zeros_like(d_w))
+    return d_rows, d_w
+
+
+class _AdapterGather(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, below, x, place):
+        ctx.save_for_backward(place)
+        return below(x, place)
+
+    @staticmethod
+    def backward(ctx, d_rows):
+        return None, adapter_combine(d_rows, None, ctx.saved_tensors[0], None), None
+
+
+class _AdapterCombine(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, below, rows, weights, place, base):
+        ctx.save_for_backward(rows, weights, place)
+        return below(rows, weights, place, base)
+
+    @staticmethod
+    def backward(ctx, dy):
+        rows, weights, place = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        d_rows = d_w = None
+        if need[1] or need[2]:
+            d_rows, d_w = adapter_combine_backward(dy, rows, weights, place, need[1], need[2])
+        return (None, d_rows if need[1] else None, d_w.to(weights.dtype) if need[2] else None, None,
+                dy if need[4] else None)
+
+
+@_q8_kernel("adapter_sort")
+def adapter_sort(ids: Tensor, adapters: int) -> tuple[Tensor, Tensor, Tensor]:
+    """(order [T k], place [T x k], bounds [adapters + 1]), int32: the slots of ids
+    [T x k] sorted by adapter, stably, those of any number outside [0, adapters)
+    behind them all.  order holds the slot t * k + j of each row, place the row of
+    each slot, both as complements for slots without an adapter; adapter a has rows
+    bounds[a] to bounds[a + 1]."""
+    if ids.dtype not in (torch.int64, torch.int32):
+        ids = ids.to(torch.int64)
+    return binding.dora_adapter_sort(ids.contiguous(), adapters)
+
+
+@torch.library.register_fake("dora_amd::adapter_sort")
+def _adapter_sort_fake(ids, adapters):
+    T, k = ids.shape
+    return (ids.new_empty((T * k,), dtype=torch.int32), ids.new_empty((T, k), dtype=torch.int32),
+            ids.new_empty((adapters + 1,), dtype=torch.int32))
+
+
+@_q8_kernel("adapter_gather", gradient=_AdapterGather)
+def adapter_gather(x: Tensor, place: Tensor) -> Tensor:
+    """rows [T k x D] of x [T x D]: x[t] at the row of each of token t's slots, zeros at
+    those of slots without an adapter; differentiable in x."""
+    if not _kernels_take(x):
+        return _eager_adapter_gather(x, place)
+    return binding.dora_adapter_gather(x.contiguous(), place.contiguous())
+
+
+@torch.library.register_fake("dora_amd::adapter_gather")
+def _adapter_gather_fake(x, place):
+    return x.new_empty((place.shape[0] * place.shape[1], x.shape[1]))
+
+
+@_q8_kernel("adapter_combine", gradient=_AdapterCombine)
+def adapter_combine(rows: Tensor, weights: Optional[Tensor], place: Tensor, base: Optional[Tensor]) -> Tensor:
+    """y [T x D]: base (or zeros) plus each token's rows times weights [T x k] (or ones),
+    summed in fp32; slots without an adapter add nothing.  Differentiable in rows,
+    weights and base."""
+    if not _kernels_take(rows):
+        return _eager_adapter_combine(rows, weights, place, base)
+    return binding.dora_adapter_combine(rows.contiguous(), None if weights is None else weights.contiguous().float(),
+                                        place.contiguous(), None if base is None else base.contiguous())
+
+
+@torch.library.register_fake("dora_amd::adapter_combine")
+def _adapter_combine_fake(rows, weights, place, base):
+    return rows.new_empty((place.shape[0], rows.shape[1]))
+
+
+@_q8_kernel("adapter_combine_backward")
+def adapter_combine_backward(dy: Tensor, rows: Tensor, weights: Optional[Tensor], place: Tensor, want_rows: bool,
+                             want_weights: bool) -> tuple[Tensor, Tensor]:
+    """(d_rows, d_weights in fp32) of ``adapter_combine``; an empty tensor stands in
+    for one that is not wanted."""
+    if not _kernels_take(dy, rows):
+        return _eager_adapter_combine_backward(dy, rows, weights, place, want_rows, want_weights)
+    d_rows, d_w = binding.dora_adapter_combine_bwd(
+        dy.contiguous(), rows.contiguous(), None if weights is None else weights.contiguous().float(),
+        place.contiguous(), want_rows, want_weights)
+    return (dy.new_empty((0,)) if d_rows is None else d_rows,
+            dy.new_empty((0,), dtype=torch.float32) if d_w is None else d_w)
+
+
+@torch.library.register_fake("dora_amd::adapter_combine_backward")
+def _adapter_combine_backward_fake(dy, rows, weights, place, want_rows, want_weights):
+    return (rows.new_empty(rows.shape if want_rows else (0,)),
+            dy.new_empty(place.shape if want_weights else (0,), dtype=torch.float32))
 
 
 # -------------------------------------------------------------------------- layer
@@ -880,12 +1323,17 @@ class DoRALinear(torch.nn.Module):
     buffers ``weight_q``, ``weight_e``; ``weight`` is None) and runs both products
     with W0 on packed operands.  n is the norm of the values W0 is held as, so the
     layer still starts out with g = 1.  Under autocast both compute in its type.
+    ``q4_weight`` holds W0 in 4-bit blocks instead (the same buffers) and multiplies
+    it with x and d_base in 16 bits; with ``q8_checkpoint`` x and base are kept in 8.
     """
 
     def __init__(self, in_features: int, out_features: int, r: int, alpha: float = 32.0,
                  weight: Tensor | None = None, dtype: torch.dtype = torch.bfloat16, device=None,
-                 detach_norm: bool = True, q8_weight: bool = False, q8_checkpoint: bool = False):
+                 detach_norm: bool = True, q8_weight: bool = False, q8_checkpoint: bool = False,
+                 q4_weight: bool = False):
         super().__init__()
+        if q8_weight and q4_weight:
+            raise ValueError("the weight is held in 8 bits or in 4, not both")
         self.detach_norm = detach_norm
         if dtype not in (torch.bfloat16, torch.float16, torch.float32):
             raise ValueError(f"unsupported dtype {dtype}; bf16 and fp16 (HIP kernels) and fp32 (eager tier) are")
@@ -893,16 +1341,16 @@ class DoRALinear(torch.nn.Module):
         self.s = float(np.float32(alpha / math.sqrt(r)))
         if weight is None:
             weight = torch.randn(out_features, in_features, device=device) / math.sqrt(in_features)
-        self.q8_weight, self.q8_checkpoint = q8_weight, q8_weight or q8_checkpoint
+        self.q8_weight, self.q8_checkpoint, self.q4_weight = q8_weight, q8_weight or q8_checkpoint, q4_weight
         weight = weight.to(device=device, dtype=dtype).contiguous()
-        if q8_weight:
+        if q8_weight or q4_weight:
             # bytes, so that a change of the module's dtype leaves them alone
             weight = weight.detach()  # it may be another layer's parameter
-            q, e = q8_pack_weight(weight)
+            q, e = (q4_pack_weight if q4_weight else q8_pack_weight)(weight)
             self.register_buffer("weight", None)
             self.register_buffer("weight_q", q.view(torch.uint8))
             self.register_buffer("weight_e", e)
-            weight = q8_unpack_weight(q, e, out_features, in_features, dtype)
+            weight = (q4_unpack_weight if q4_weight else q8_unpack_weight)(q, e, out_features, in_features, dtype)
         else:
             self.register_buffer("weight", weight)
         self.lora_A = torch.nn.Parameter(
@@ -914,15 +1362,16 @@ class DoRALinear(torch.nn.Module):
             self.reset_magnitude()
 
     def _packed_weight(self) -> tuple[Tensor, Tensor]:
-        return self.weight_q.view(_F8), self.weight_e
+        return self.weight_q if self.q4_weight else self.weight_q.view(_F8), self.weight_e
 
     @torch.no_grad()
     def refresh_weight_cache(self) -> None:
         """Recompute ||W0_i||^2 (after ``weight`` changed)."""
-        if self.q8_weight:
+        if self.q8_weight or self.q4_weight:
             wq, we = self._packed_weight()
             n = torch.empty(self.out_features, dtype=torch.float32, device=wq.device)
-            for rows, W in _slabs(wq, we, self.out_features, self.in_features, self.lora_A.dtype):
+            slabs = _q4_slabs if self.q4_weight else _slabs
+            for rows, W in slabs(wq, we, self.out_features, self.in_features, self.lora_A.dtype):
                 n[rows] = row_sqnorm(W)
             self.weight_sqnorm = n
         else:
@@ -941,21 +1390,25 @@ class DoRALinear(torch.nn.Module):
         A, B = (self.lora_A.detach(), self.lora_B.detach()) if self.detach_norm else (self.lora_A, self.lora_B)
         if self.q8_weight:
             return q8_weight_norm(*self._packed_weight(), A, B, self.weight_sqnorm, self.s)
+        if self.q4_weight:
+            return q4_weight_norm(*self._packed_weight(), A, B, self.weight_sqnorm, self.s)
         return weight_norm_cached(self.weight, A, B, self.weight_sqnorm, self.s)
 
     def forward(self, x: Tensor) -> Tensor:
         lead = x.shape[:-1]
         x2 = x.reshape(-1, self.in_features)
-        weight, we = self._packed_weight() if self.q8_weight else (self.weight, None)
+        weight, we = self._packed_weight() if self.q8_weight or self.q4_weight else (self.weight, None)
         n = self.weight_norm()
         trained = (x2, self.lora_A, self.lora_B, self.magnitude, n)
         if self.q8_checkpoint and torch.is_grad_enabled() and any(t.requires_grad for t in trained):
             y = q8_layer(x2, self.lora_A, self.lora_B, self.magnitude, n, weight, we, self.s)[0]
             return y.reshape(*lead, self.out_features)
         B = self.lora_B
-        if self.q8_checkpoint:  # inference: the types of the training tier
+        if self.q8_checkpoint or self.q4_weight:  # the types of the training tier
             x2, B = _autocast(x2, B)
-        if self.q8_weight:  # x is packed for the product alone
+        if self.q4_weight:
+            base = q4_linear(x2, weight, we, self.out_features)
+        elif self.q8_weight:  # x is packed for the product alone
             base = q8_linear(*q8_pack(x2), weight, we, self.out_features, x2.dtype)
         else:
             base = F.linear(x2, weight)
@@ -964,4 +1417,91 @@ class DoRALinear(torch.nn.Module):
         # training tier autograd records it and its backward (lora_compose_backward)
         # never forms lora or d_lora either, so nothing T x out is saved for lora
         y = lora_compose(base, h, B, self.magnitude, n, self.s, True)
+        return y.reshape(*lead, self.out_features)
+
+
+class DoRAAdapters(torch.nn.Module):
+    """Several DoRA adapters over one frozen weight W0 [out x in]: adapter a has its own
+    A [r x in], B [out x r] and magnitude [out] (slices of ``lora_A``, ``lora_B`` and
+    ``magnitude``), and each token of a batch says which it uses, as in a batch of
+    requests to different adapters, or a mixture of them:
+
+      y_t = x_t W0^T + sum_j w_tj * delta_{id_tj}(x_t),
+      delta_a(x) = (g_a - 1) * (x W0^T) + g_a * s * (x A_a^T B_a^T),  g_a = m_a / n_a.
+
+    ``forward(x, ids, weights)``: x [.. x in], ids whole numbers [..] or [.. x k] (any
+    outside [0, adapters) is no adapter), weights like ids, or None for ones.  The
+    product with W0 runs once for all tokens; tokens are then sorted by adapter, each
+    adapter's rows go through ``lora_compose`` together, and come back per token with
+    their weights.  The rows' bounds are read by the host once a call.  W0 in 16 bits,
+    or with ``q4_weight`` in 4-bit blocks; initialisation, ``detach_norm`` and the cache
+    of ||W0_i||^2 as in ``DoRALinear``.
+    """
+
+    def __init__(self, in_features: int, out_features: int, r: int, adapters: int, alpha: float = 32.0,
+                 weight: Tensor | None = None, dtype: torch.dtype = torch.bfloat16, device=None,
+                 detach_norm: bool = True, q4_weight: bool = False):
+        super().__init__()
+        if adapters < 1:
+            raise ValueError(f"{adapters} adapters")
+        one = DoRALinear(in_features, out_features, r, alpha, weight, dtype, device, detach_norm, q4_weight=q4_weight)
+        self.in_features, self.out_features, self.r, self.adapters = in_features, out_features, r, adapters
+        self.s, self.detach_norm, self.q4_weight = one.s, detach_norm, q4_weight
+        for name in ("weight", "weight_q", "weight_e", "weight_sqnorm"):
+            if hasattr(one, name):
+                self.register_buffer(name, getattr(one, name))
+        A = torch.randn(adapters, r, in_features, device=device) / math.sqrt(in_features)
+        self.lora_A = torch.nn.Parameter(A.to(dtype))
+        self.lora_B = torch.nn.Parameter(torch.zeros(adapters, out_features, r, device=device, dtype=dtype))
+        self.magnitude = torch.nn.Parameter(one.magnitude.detach().repeat(adapters, 1))
+
+    q8_weight = False
+    _packed_weight = DoRALinear._packed_weight
+    refresh_weight_cache = DoRALinear.refresh_weight_cache
+
+    @torch.no_grad()
+    def reset_magnitude(self) -> None:
+        """m_a = ||W0 + s*B_a*A_a|| per row, of every adapter."""
+        for a in range(self.adapters):
+            self.magnitude[a].copy_(self.weight_norm(a))
+
+    def weight_norm(self, adapter: int) -> Tensor:
+        """n_a = ||W0 + s*B_a*A_a|| per output row."""
+        if self.weight_sqnorm is None or self.weight_sqnorm.device != self.lora_A.device:
+            self.refresh_weight_cache()
+        A, B = self.lora_A[adapter], self.lora_B[adapter]
+        if self.detach_norm:
+            A, B = A.detach(), B.detach()
+        if self.q4_weight:
+            return q4_weight_norm(*self._packed_weight(), A, B, self.weight_sqnorm, self.s)
+        return weight_norm_cached(self.weight, A, B, self.weight_sqnorm, self.s)
+
+    def forward(self, x: Tensor, ids: Tensor, weights: Tensor | None = None) -> Tensor:
+        lead = x.shape[:-1]
+        if ids.shape[: len(lead)] != lead or ids.dim() > len(lead) + 1:
+            raise ValueError(f"ids are {tuple(ids.shape)}, expected {tuple(lead)} or {tuple(lead)} x k")
+        if weights is not None and weights.shape != ids.shape:
+            raise ValueError(f"weights are {tuple(weights.shape)}, expected {tuple(ids.shape)}")
+        k = ids.shape[-1] if ids.dim() > len(lead) else 1
+        x2 = x.reshape(-1, self.in_features)
+        T = x2.shape[0]
+        (x2,) = _autocast(x2)
+        if self.q4_weight:
+            base = q4_linear(x2, *self._packed_weight(), self.out_features)
+        else:
+            base = F.linear(x2, self.weight)
+        order, place, bounds = adapter_sort(ids.reshape(T, k), self.adapters)
+        xs, bs = adapter_gather(x2, place), adapter_gather(base, place)
+        ends = bounds.tolist()
+        parts = []
+        for a in range(self.adapters):
+            rows = slice(ends[a], ends[a + 1])
+            if rows.start < rows.stop:
+                h = F.linear(xs[rows], self.lora_A[a])
+                (B,) = _autocast(self.lora_B[a])
+                parts.append(lora_compose(bs[rows], h, B, self.magnitude[a], self.weight_norm(a), self.s, False))
+        if ends[-1] < T * k:  # the rows of slots without an adapter: not used
+            parts.append(base.new_zeros((T * k - ends[-1], self.out_features)))
+        rows = torch.cat(parts) if parts else base.new_zeros((0, self.out_features))
+        y = adapter_combine(rows, None if weights is None else weights.reshape(T, k), place, base)
         return y.reshape(*lead, self.out_features)

@@ -46,7 +46,21 @@
  *   dora_q8_linear_fwd, dora_q8_linear_bwd
  *                              x W0^T and g W0 on packed operands;
  *   dora_q8_lora_compose_bwd   dora_lora_compose_bwd from a packed base;
- *   dora_q8_grad_a             d_A from packed x.
+ *   dora_q8_grad_a             d_A from packed x;
+ *
+ * and, for a frozen W0 in 4 bits:
+ *
+ *   dora_q4_pack_weight, dora_q4_unpack_weight
+ *                              blocks of 32 of e2m1 with a power-of-two scale;
+ *   dora_q4_linear_fwd, dora_q4_linear_bwd
+ *                              x W0^T and g W0 with 16-bit x and g;
+ *
+ * and, for a batch whose tokens use different adapters over the one W0:
+ *
+ *   dora_adapter_sort          tokens' slots sorted by adapter;
+ *   dora_adapter_gather        tokens' rows in that order;
+ *   dora_adapter_combine       rows added up per token, with weights;
+ *   dora_adapter_combine_bwd   its gradients of the rows and the weights.
  *
  * Conventions shared by every entry point
  *  - Matrices are row-major and contiguous.  W0 is [out x in], A is [r x in],
@@ -99,8 +113,10 @@ extern "C" {
  *    and T * r above 2^20 (its slow path runs T * r products in order in one
  *    thread per output column);
  *  - dora_compose_bwd_noalloc with sizes whose partials exceed its scratch;
- *  - in the 8-bit operators (dora_q8_*), 2^31 rows or more, more than 2^22 - 128
- *    columns, or a rank above 2^20.
+ *  - in the 8-bit and 4-bit operators (dora_q8_*, dora_q4_*), 2^31 rows or more,
+ *    more than 2^22 - 128 columns, or a rank above 2^20;
+ *  - in the operators on sorted tokens (dora_adapter_*), more than 2^31 - 1 slots,
+ *    1000 adapters or 2^22 columns, or ids of neither 4 nor 8 bytes.
  */
 enum dora_status {
   DORA_OK = 0,
@@ -458,6 +474,116 @@ DORA_API size_t dora_q8_grad_a_workspace_bytes(int64_t T, int64_t in, int64_t r)
  */
 DORA_API int dora_q8_grad_a(const void* dh, const void* xq, const void* xe, int64_t T, int64_t in, int64_t r, int dtype,
                             void* d_A, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/*
+ * ---- The frozen weight in 4 bits ------------------------------------------
+ *
+ * W0 [out x in] in blocks of 32 consecutive columns of a row: e2m1 values (0, 0.5,
+ * 1, 1.5, 2, 3, 4, 6 and their negatives) with one power-of-two scale 2^e a block,
+ * the smallest e in [-23, 13] for which the block's largest magnitude is at most
+ * 7 * 2^e.  The value held is v * 2^-e rounded to the nearest e2m1 value, ties to
+ * the one of even code, 6 at most, times 2^e: exact in bf16 and in fp16.
+ * Magnitudes below 2^-25 are held as 0, and 6 * 2^13 is the largest.  A block with
+ * a value that is not finite is NaN as a whole.  17 bits hold 4 values.
+ *
+ * Layout: tiles of 32 rows x 64 columns, zeros outside W0, row tiles outermost,
+ *   q  bytes [out / 32 rounded up, in / 64 rounded up, 1024],
+ *   e  bytes [out / 32 rounded up, in / 64 rounded up, 64].
+ * Row 8g + i (g < 4, i < 8) of a tile has its block b (of two) in the 16 bytes of q
+ * at 128 i + 32 g + 16 (b ^ (i/2 % 2)), codes of 4 bits (sign above the magnitude's
+ * number in the list above), even columns in the low halves, and the byte 127 + e
+ * (255: NaN) in e at 32 b + 8 g + 2 (i % 4) + i/4.  q and e are 16-byte aligned.
+ * Only bytes written by dora_q4_pack_weight are valid ones.
+ *
+ * Sizes: fewer than 2^31 rows of x, at most 2^22 - 128 rows and columns of W0 and
+ * 2^31 - 1 tiles (else DORA_UNSUPPORTED).  No output may overlap an input or
+ * another output.
+ */
+
+/* Pack W [out x in] (device, dtype) into q, e (once: it is frozen).  Empty sizes are no-ops. */
+DORA_API int dora_q4_pack_weight(const void* W, int64_t out, int64_t in, int dtype, void* q, void* e,
+                                 hipStream_t stream);
+
+/* The values that the first `rows` rows of a packed weight of `cols` columns are held as, in dtype (exact). */
+DORA_API int dora_q4_unpack_weight(const void* q, const void* e, int64_t rows, int64_t cols, int dtype, void* W,
+                                   hipStream_t stream);
+
+/* Bytes of device workspace dora_q4_linear_fwd needs (fp32 tiles of a split contraction, rows padded to 8; often 0). */
+DORA_API size_t dora_q4_linear_workspace_bytes(int64_t T, int64_t out, int64_t in);
+
+/*
+ * y [T x out] = x W0^T with x [T x in] (device, dtype, 16-byte aligned) and a packed
+ * weight: 16-bit operands, products and sums in fp32, rounded once to dtype.  For
+ * few rows (single tokens as they are generated) the weight is streamed once.
+ * in == 0 gives y = 0.  A NaN in a row of x gives NaN in that row of y alone, a NaN
+ * block of W0 in its column of y.  ws: 16-byte aligned, at least
+ * dora_q4_linear_workspace_bytes bytes.
+ */
+DORA_API int dora_q4_linear_fwd(const void* x, const void* q, const void* e, int64_t T, int64_t out, int64_t in,
+                                int dtype, void* y, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* Bytes of device workspace dora_q4_linear_bwd needs. */
+DORA_API size_t dora_q4_linear_bwd_workspace_bytes(int64_t T, int64_t out, int64_t in);
+
+/*
+ * dx [T x in] = g W0 with g [T x out] and the same packed weight, which is
+ * transposed on the way to the matrix instructions.  W0 is frozen, so there is no
+ * gradient of the weight.  out == 0 gives dx = 0.
+ */
+DORA_API int dora_q4_linear_bwd(const void* g, const void* q, const void* e, int64_t T, int64_t out, int64_t in,
+                                int dtype, void* dx, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/*
+ * ---- Tokens sorted by adapter ---------------------------------------------
+ *
+ * Several adapters over one W0: token t of a batch has k slots (t, j), each with
+ * the number of an adapter in [0, n), or any other number for none.  Slots are
+ * numbered t * k + j.  Each slot owns one of R = T k rows: rows are sorted by
+ * adapter, an adapter's rows in the order of its slots, and the rows of slots
+ * without one come last.
+ *   order [R]      the slot of each row; the complement ~slot (negative) where the
+ *                  slot has no adapter;
+ *   place [T x k]  the row of each slot; its complement where it has none;
+ *   bounds [n + 1] adapter a has rows [bounds[a], bounds[a + 1]).
+ * The operators on rows take place as dora_adapter_sort leaves it.  (Numbers
+ * outside [-R, R) in it are left out, so that no call reads or writes beyond its
+ * matrices; a row that no slot owns is then not written.)
+ *
+ * Sizes: at most 2^31 - 1 slots, 1000 adapters, rows of 2^22 elements (else
+ * DORA_UNSUPPORTED).  Matrices are device, dtype, row-major; any alignment of their
+ * elements is taken, 16 bytes and D % 8 == 0 faster.  No output may overlap an
+ * input or another output, but y of dora_adapter_combine may be base itself.
+ */
+
+/* Bytes of device workspace dora_adapter_sort needs (counts of its workgroups; 0 for up to 4096 slots). */
+DORA_API size_t dora_adapter_sort_workspace_bytes(int64_t T, int64_t k, int64_t n);
+
+/* ids [T x k]: device, int64 (id_bytes 8) or int32 (4).  order, place, bounds: device int32.  No slots: bounds = 0. */
+DORA_API int dora_adapter_sort(const void* ids, int id_bytes, int64_t T, int64_t k, int64_t n, int32_t* order,
+                               int32_t* place, int32_t* bounds, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* rows [T k x D]: the row of slot (t, j) is x[t], zeros for a slot without an adapter. */
+DORA_API int dora_adapter_gather(const void* x, const int32_t* place, int64_t T, int64_t k, int64_t D, int dtype,
+                                 void* rows, hipStream_t stream);
+
+/*
+ * y[t] = base[t] + sum over the slots j with an adapter of weights[t, j] * (their
+ * rows), in fp32, rounded once.  weights: fp32 [T x k], NULL for ones; base: NULL
+ * for zeros.  What stands in the rows and weights of other slots is not used.
+ * Without weights and base this is the gradient of dora_adapter_gather.
+ */
+DORA_API int dora_adapter_combine(const void* rows, const float* weights, const int32_t* place, const void* base,
+                                  int64_t T, int64_t k, int64_t D, int dtype, void* y, hipStream_t stream);
+
+/*
+ * The gradients of dora_adapter_combine: d_rows [T k x D], the row of slot (t, j)
+ * weights[t, j] * dy[t], and d_weights [T x k] (fp32) = <dy[t], that row of rows>;
+ * both zeros for a slot without an adapter.  Either may be NULL (not computed), and
+ * rows without d_weights.  The gradient of base is dy.
+ */
+DORA_API int dora_adapter_combine_bwd(const void* dy, const void* rows, const float* weights, const int32_t* place,
+                                      int64_t T, int64_t k, int64_t D, int dtype, void* d_rows, float* d_weights,
+                                      hipStream_t stream);
 
 /* Message of the calling thread's last non-OK status ("" if none).  Valid until the next call. */
 DORA_API const char* dora_last_error(void);
