@@ -12,19 +12,21 @@
 
 #include "dma_common.hpp"
 #include "q4_common.hpp"
+#include "tile_units.hpp"
 
 namespace dora {
 
 namespace {
 
-struct GemmArgs {
+struct GemmArgs : TileGrid {
   const void* x;     // [T x K], rows of xp elements (a multiple of 8), zeros behind K
   int64_t xp;
   const uint8_t *wq, *we;
-  int64_t T, N, K;
+  int64_t T, N;
   int rt, ct;  // row and column tiles of the weight
   void* y;
   int vec;  // 16-byte stores of y
+  float* part;
 };
 
 // Eight consecutive output columns of a row, from column c on.
@@ -196,6 +198,480 @@ __global__ __launch_bounds__(64 * NW) void q4_few_bwd(GemmArgs a) {
   }
 }
 
+// ------------------------------------------------------------------ tiles
+//
+// Tile geometry: 2 x 2 waves, each TMW x TNW matrix tiles of 16 x 16 with their
+// accumulators in registers; a ring of NS slots of one stage, 64 contraction steps
+// of both operands.  x goes to LDS as rows of 128 bytes, logical 16-byte chunk c of
+// row p in place c ^ ((p/2) % 8), so that 16 consecutive rows at one chunk fall in 16
+// distinct bank groups; the weight's 4-bit tiles as they are, 64 bytes apart from
+// their neighbours (the backward's lanes read two tiles at once).
+template <int TMW_, int TNW_, int NS_, bool TRANS_>
+struct Q4Tile {
+  static constexpr int TMW = TMW_, TNW = TNW_, NS = NS_;
+  static constexpr bool TRANS = TRANS_;
+  static constexpr int WM = 2, WN = 2, NW = 4, NT = 256;
+  static constexpr int BM = 16 * TMW * WM, BN = 16 * TNW * WN, BK = 64;
+  static constexpr int WT = BN / 32, WSTEP = static_cast<int>(kQ4TileQ) + 64;  // weight tiles of a stage
+  static constexpr int X_BYTES = BM * BK * 2, W_BYTES = WT * WSTEP, E_BYTES = NW * 256;
+  static constexpr int SLOT_BYTES = X_BYTES + W_BYTES + E_BYTES;
+  static constexpr int LDS_BYTES = NS * SLOT_BYTES;
+  static constexpr int XQ = BM / 8 / NW, WQ = WT / NW, L = XQ + WQ + 1;  // DMA instructions a wave
+  static constexpr int CT = BN / 64;  // column tiles of the backward's stage (two row tiles)
+  static constexpr int NM = TMW * TNW;  // matrix instructions of a step of 32
+  static constexpr int NST = NM / 2;    // 16-byte stores of a wave's tile
+  static constexpr int WAIT = (NS - 2) * L;   // DMA instructions younger than the slot waited for
+  static constexpr int LA = (L + 1) / 2;      // a slot's loads stand in the step after it is free and in the next one
+  static constexpr int RELAX = NS - 2;        // stages whose slot was loaded before a tile's stores
+  static_assert(XQ * 8 * NW == BM && WQ * NW == WT, "whole DMA instructions per wave");
+  static_assert(WT * 16 <= NW * 64, "exponents of a stage in one DMA instruction a wave");
+  static_assert(!TRANS || TNW == 8 || TNW == 4, "a backward lane's columns");
+  static_assert(TNW % 2 == 0 && NS >= 3, "pairs of half tiles; the ring");
+  static_assert(WAIT + NST < 64, "vmcnt range");
+  static_assert(LDS_BYTES <= 160 * 1024, "LDS");
+};
+
+template <int OFF>
+__device__ inline u32x2 lds_read8_at(uint32_t base) {
+  static_assert(OFF >= 0 && OFF < 65536, "ds offset field");
+  u32x2 v;
+  asm volatile("ds_read_b64 %0, %1 offset:%2" : "=v"(v) : "v"(base), "n"(OFF) : "memory");
+  return v;
+}
+template <int OFF>
+__device__ inline uint32_t lds_read4_at(uint32_t base) {
+  static_assert(OFF >= 0 && OFF < 65536, "ds offset field");
+  uint32_t v;
+  asm volatile("ds_read_b32 %0, %1 offset:%2" : "=v"(v) : "v"(base), "n"(OFF) : "memory");
+  return v;
+}
+template <int OFF>
+__device__ inline uint32_t lds_read2_at(uint32_t base) {
+  static_assert(OFF >= 0 && OFF < 65536, "ds offset field");
+  uint32_t v;
+  asm volatile("ds_read_u16 %0, %1 offset:%2" : "=v"(v) : "v"(base), "n"(OFF) : "memory");
+  return v;
+}
+__device__ inline void tie1(uint32_t& v) { asm volatile("" : "+v"(v)); }
+
+// Eight output columns of a row; stores past the matrix are dropped by the buffer
+// resource, so that a tile is always the same number of stores.
+template <int DT>
+__device__ inline void store8_to(__amdgpu_buffer_rsrc_t ry, int vec, uint32_t row, uint32_t n, uint32_t c,
+                                 const float (&f)[8]) {
+  const Chunk o = f32_to_chunk<DT>(f);
+  const uint32_t at = (row * n + c) * 2;
+  if (vec) {
+    __builtin_amdgcn_raw_buffer_store_b128(u32x4{o.w[0], o.w[1], o.w[2], o.w[3]}, ry, c < n ? at : kOob, 0, 0);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      __builtin_amdgcn_raw_buffer_store_b16(static_cast<uint16_t>(o.w[i >> 1] >> (16 * (i & 1))), ry,
+                                            c + i < n ? at + 2 * i : kOob, 0, 0);
+  }
+}
+// Rows [m, m + most) of y, as far as they exist.
+__device__ inline __amdgpu_buffer_rsrc_t rows_of_y(const GemmArgs& a, int64_t m, int most) {
+  const int64_t rows = min(max(a.T - m, int64_t(0)), static_cast<int64_t>(most));
+  return buffer_of(static_cast<char*>(a.y) + (rows > 0 ? m * a.N * 2 : 0), rows * a.N * 2);
+}
+
+// The fragments of a group of matrix tiles (two forward, TNW backward) of one row of
+// them, as the 16-byte pieces of y they are.  Forward: register q of half tile h is
+// column 8 g + 4 h + q (g = lane / 16).  Backward: register q of fragment f is
+// column TNW * (4 g + q) + f.
+template <int DT, class TL>
+__device__ inline void store_group(__amdgpu_buffer_rsrc_t ry, int vec, uint32_t row, int64_t N, int64_t c0, int lane,
+                                   const f32x4* acc) {
+  const uint32_t g = static_cast<uint32_t>(lane) >> 4, n = static_cast<uint32_t>(N), c = static_cast<uint32_t>(c0);
+  if constexpr (!TL::TRANS) {
+    const float f[8] = {acc[0][0], acc[0][1], acc[0][2], acc[0][3], acc[1][0], acc[1][1], acc[1][2], acc[1][3]};
+    store8_to<DT>(ry, vec, row, n, c + 8 * g, f);
+  } else if constexpr (TL::TNW == 8) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const float f[8] = {acc[0][q], acc[1][q], acc[2][q], acc[3][q], acc[4][q], acc[5][q], acc[6][q], acc[7][q]};
+      store8_to<DT>(ry, vec, row, n, c + 32 * g + 8 * q, f);
+    }
+  } else {
+#pragma unroll
+    for (int q = 0; q < 4; q += 2) {
+      const float f[8] = {acc[0][q],     acc[1][q],     acc[2][q],     acc[3][q],
+                          acc[0][q + 1], acc[1][q + 1], acc[2][q + 1], acc[3][q + 1]};
+      store8_to<DT>(ry, vec, row, n, c + 16 * g + 4 * q, f);
+    }
+  }
+}
+
+// One workgroup a CU, each taking its units in turn (tile_units.hpp).  The ring runs
+// on from one unit to the next: while a unit's last slots are worked on, the next
+// one's first ones load, and its stores are under way while the next one's products
+// run.  A step of 32 works on fragments that were read and converted during the step
+// before: reads stand behind its first matrix instructions, the conversions behind
+// its last ones.
+template <int DT, class TL>
+__global__ __launch_bounds__(TL::NT, 1) void q4_gemm_tile(GemmArgs a) {
+  using V8 = typename Dt<DT>::V8;
+  __shared__ __attribute__((aligned(1024))) char smem[TL::LDS_BYTES];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / TL::WN, wn = wave % TL::WN;
+  const uint32_t lds0 = static_cast<uint32_t>(reinterpret_cast<uintptr_t>((lds_char_t*)smem));
+
+  Unit cu;
+  if (!unit_of(0, a, cu)) return;
+
+  // ---- the issuing side: its unit, and that unit's buffer resources (what lies
+  // past an operand reads zero; past the last unit everything does, so that every
+  // step issues the same instructions and the waits count them exactly)
+  const int xr = wave * 8 + (lane >> 3);  // x row of DMA instruction 0
+  const int xc = (lane & 7) ^ ((xr >> 1) & 7);  // its logical chunk
+  const uint32_t xo = static_cast<uint32_t>(xr * a.xp) * 2 + 16 * xc;
+  const uint32_t xstep = static_cast<uint32_t>(TL::NW * 8 * a.xp) * 2;
+  const int et = (wave * 64 + lane) >> 4;  // weight tile whose exponents this lane loads
+  const uint32_t rowq = static_cast<uint32_t>(a.ct) * kQ4TileQ, rowe = static_cast<uint32_t>(a.ct) * kQ4TileE;
+
+  int ik = 0, ist = 0, iend = 0;
+  bool live = true;
+  __amdgpu_buffer_rsrc_t rx, rw, re;
+  int in0 = 0;  // backward: the first column tile
+  uint32_t xat = 0, wat[TL::WQ], eat = 0;
+  auto issue_stage = [&]() {
+    // columns past the row are no part of it
+    xat = static_cast<int64_t>(ist) * 64 + 8 * xc < a.xp ? static_cast<uint32_t>(ist) * 128 : 0x80000000u;
+    if constexpr (TL::TRANS) {
+      const int64_t r0 = 2 * static_cast<int64_t>(ist), n = live ? min(max(a.rt - r0, int64_t(0)), int64_t(2)) : 0;
+      rw = buffer_of(a.wq + (n > 0 ? r0 * rowq : 0), n * rowq);
+      re = buffer_of(a.we + (n > 0 ? r0 * rowe : 0), n * rowe);
+    } else {
+#pragma unroll
+      for (int q = 0; q < TL::WQ; ++q)
+        wat[q] = static_cast<uint32_t>(q * TL::NW + wave) * rowq + static_cast<uint32_t>(ist) * kQ4TileQ + 16 * lane;
+      eat = et < TL::WT ? static_cast<uint32_t>(et) * rowe + static_cast<uint32_t>(ist) * kQ4TileE + 4 * (lane & 15) : kOob;
+    }
+  };
+  auto issue_unit = [&](Unit u) {
+    ist = u.st0;
+    iend = u.st1;
+    const int64_t m0 = static_cast<int64_t>(u.rb) * TL::BM;
+    const int64_t xrows = live ? min(a.T - m0, static_cast<int64_t>(TL::BM)) : 0;
+    rx = buffer_of(static_cast<const char*>(a.x) + m0 * a.xp * 2, xrows * a.xp * 2);
+    if constexpr (TL::TRANS) {
+      in0 = u.nt * TL::CT;
+#pragma unroll
+      for (int q = 0; q < TL::WQ; ++q) {
+        const int t = q * TL::NW + wave, c = in0 + t % TL::CT;
+        wat[q] = c < a.ct ? (t / TL::CT) * rowq + static_cast<uint32_t>(c) * kQ4TileQ + 16 * lane : kOob;
+      }
+      const int c = in0 + et % TL::CT;
+      eat = et < TL::WT && c < a.ct ? (et / TL::CT) * rowe + static_cast<uint32_t>(c) * kQ4TileE + 4 * (lane & 15) : kOob;
+    } else {
+      const int64_t r0 = static_cast<int64_t>(u.nt) * TL::WT, n = live ? min(a.rt - r0, static_cast<int64_t>(TL::WT)) : 0;
+      rw = buffer_of(a.wq + r0 * rowq, n * rowq);
+      re = buffer_of(a.we + r0 * rowe, n * rowe);
+    }
+  };
+  // DMA instruction k of the issuing side's stage (k compile time)
+  auto issue1 = [&](int slot, auto kk) {
+    constexpr int k = decltype(kk)::value;
+    char* so = smem + slot * TL::SLOT_BYTES;
+    if constexpr (k < TL::XQ) {
+      dma16(rx, so + (k * TL::NW + wave) * 1024, xo + k * xstep + xat);
+    } else if constexpr (k < TL::XQ + TL::WQ) {
+      constexpr int q = k - TL::XQ;
+      dma16(rw, so + TL::X_BYTES + (q * TL::NW + wave) * TL::WSTEP, wat[q]);
+    } else {
+      char* d = so + TL::X_BYTES + TL::W_BYTES + wave * 256;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(re, (lds_void_t*)d, 4, eat, 0, 0, 0);
+    }
+  };
+  auto issue_next = [&]() {  // to the next stage, or the next unit's first
+    if (++ist == iend) {
+      Unit u;
+      live = unit_of(++ik, a, u);
+      if (!live) u = Unit{0, 0, 0, 1 << 30, 0, -1};
+      issue_unit(u);
+    }
+    issue_stage();
+  };
+
+  // ---- fragment read addresses within a slot.  Lane l holds row l % 16 of a
+  // matrix tile and eight contraction steps.  Forward, step s: columns 16 g + 8 s
+  // (g = l / 16), half a block's 16 bytes of the weight for both steps of the stage.
+  // Backward, step s: rows 8 g of the stage's row tile s.
+  const int l16 = lane & 15, g = lane >> 4;
+  uint32_t xa[2];
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    const int c = TL::TRANS ? 4 * s + g : 2 * g + s;
+    xa[s] = lds0 + static_cast<uint32_t>((wm * TL::TMW * 16 + l16) * 128 + 16 * (c ^ ((l16 >> 1) & 7)));
+  }
+  const uint32_t w0 = lds0 + TL::X_BYTES, e0 = w0 + TL::W_BYTES;
+  uint32_t wa[TL::TRANS ? 2 : 1], ea;
+  if constexpr (TL::TRANS) {
+    const int col = wn * TL::TNW * 16 + TL::TNW * l16;  // the lane's first column of the tile
+    const int t = col >> 6, b = (col >> 5) & 1;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)  // rows 8g + i with (i / 2) % 2 == h
+      wa[h] = w0 + static_cast<uint32_t>(t * TL::WSTEP) + q4_unit(2 * h, g, b) - 256 * h + ((col >> 1) & 15);
+    ea = e0 + static_cast<uint32_t>(t * 64 + 32 * b + 8 * g);
+  } else {
+    wa[0] = w0 + static_cast<uint32_t>(wn * TL::TNW / 2 * TL::WSTEP) + q4_unit(l16 & 3, l16 >> 2, g >> 1) + 8 * (g & 1);
+    ea = e0 + static_cast<uint32_t>(wn * TL::TNW / 2 * 64 + 32 * (g >> 1) + 2 * l16);
+  }
+
+  f32x4 acc[TL::TMW][TL::TNW];
+  u32x4 fx[2][TL::TMW], fw[2][TL::TNW];  // fragments of the two steps of a stage
+  u32x2 rawf[TL::TRANS ? 1 : TL::TNW];   // forward: the stage's weight, both steps
+  uint32_t rawe[TL::TRANS ? 1 : TL::TNW / 2];
+  uint32_t rawb[TL::TRANS ? 8 : 1];      // backward: the next step's
+  u32x2 rawbe;
+  float scale[8];
+  constexpr int NRX = TL::TMW, NRW = TL::TRANS ? 9 : TL::TNW + TL::TNW / 2;
+  // Read n of the step before step s: first the weight (forward: once a stage).
+  auto read1 = [&](uint32_t so, auto ss, auto nn) {
+    constexpr int s = decltype(ss)::value;
+    constexpr int n = decltype(nn)::value - ((TL::TRANS || s == 0) ? NRW : 0);
+    if constexpr (n >= 0) {
+      fx[s][n] = lds_read16_at<n * 16 * 128>(xa[s] + so);
+    } else if constexpr (TL::TRANS) {
+      constexpr int i = n + NRW;
+      constexpr int st = s * TL::CT * TL::WSTEP;
+      if constexpr (i == 8)
+        rawbe = lds_read8_at<s * TL::CT * 64>(ea + so);
+      else if constexpr (TL::TNW == 8)
+        rawb[i] = lds_read4_at<st + 128 * i>(wa[(i >> 1) & 1] + so);
+      else
+        rawb[i] = lds_read2_at<st + 128 * i>(wa[(i >> 1) & 1] + so);
+    } else {
+      constexpr int j = n + NRW;
+      if constexpr (j < TL::TNW)
+        rawf[j] = lds_read8_at<(j / 2) * TL::WSTEP + (j % 2) * 512>(wa[0] + so);
+      else
+        rawe[j - TL::TNW] = lds_read2_at<(j - TL::TNW) * 64>(ea + so);
+    }
+  };
+  // after lds_wait()
+  auto tie_reads = [&](auto ss) {
+    constexpr int s = decltype(ss)::value;
+#pragma unroll
+    for (int i = 0; i < TL::TMW; ++i) tie(fx[s][i]);
+    if constexpr (TL::TRANS) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) tie1(rawb[i]);
+      tie2(rawbe);
+    } else if constexpr (s == 0) {
+#pragma unroll
+      for (int j = 0; j < TL::TNW; ++j) tie2(rawf[j]);
+#pragma unroll
+      for (int j = 0; j < TL::TNW / 2; ++j) tie1(rawe[j]);
+    }
+  };
+  // Conversion piece p of step s: forward a fragment, backward the two of a pair of
+  // columns.
+  constexpr int NP = TL::TRANS ? TL::TNW / 2 : TL::TNW;
+  auto convert1 = [&](auto ss, auto pp) {
+    constexpr int s = decltype(ss)::value, p = decltype(pp)::value;
+    if constexpr (TL::TRANS) {
+      if constexpr (p == 0) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) scale[i] = scale_of_row(rawbe, i);
+      }
+      uint32_t v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = q4_decode2<DT, p>(rawb[i], scale[i]);
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        fw[s][2 * p][h] = lows(v[2 * h], v[2 * h + 1]);
+        fw[s][2 * p + 1][h] = highs(v[2 * h], v[2 * h + 1]);
+      }
+    } else {
+      const uint32_t e = rawe[p / 2];
+      const float sc = q4_scale(p % 2 ? e >> 8 : e & 255u);
+      fw[s][p] = __builtin_bit_cast(u32x4, q4_decode8<DT>(rawf[p][s], sc));
+    }
+  };
+  // The accumulators are named here, so the products above stay above (the
+  // compiler would otherwise sink them past the barrier to their next use).
+  auto pin_acc = [&]() {
+#pragma unroll
+    for (int i = 0; i < TL::TMW; ++i)
+#pragma unroll
+      for (int j = 0; j < TL::TNW; ++j) asm volatile("" : "+a"(acc[i][j]));
+  };
+  // An accumulator is cleared by a product of zeros, which takes its zero addend as
+  // an inline constant.
+  auto clear = [&](int i, int j) {
+    uint32_t z = 0;
+    asm volatile("" : "+v"(z));
+    const V8 zv = __builtin_bit_cast(V8, u32x4{z, z, z, z});
+    acc[i][j] = Dt<DT>::mfma16(zv, zv, f32x4{});
+    asm volatile("" : "+a"(acc[i][j]));
+  };
+
+  // ---- fill the ring
+  issue_unit(cu);
+  issue_stage();
+#pragma unroll
+  for (int s = 0; s < TL::NS; ++s) {
+    if (s + 1 < TL::NS) {
+      unrolled<TL::L>([&](auto kk) { issue1(s, kk); });
+      issue_next();
+    } else {
+      unrolled<TL::LA>([&](auto kk) { issue1(s, kk); });
+    }
+  }
+  wait_vmcnt<(TL::NS - 2) * TL::L + TL::LA>();
+  __builtin_amdgcn_s_barrier();
+  using S0 = std::integral_constant<int, 0>;
+  using S1 = std::integral_constant<int, 1>;
+  unrolled<NRX + NRW>([&](auto nn) { read1(0u, S0{}, nn); });
+  lds_wait();
+  tie_reads(S0{});
+  unrolled<NP>([&](auto pp) { convert1(S0{}, pp); });
+
+  int ck = 0;
+  bool more = false;
+  auto look_ahead = [&]() {
+    Unit n;
+    more = unit_of(ck + 1, a, n);
+  };
+  look_ahead();
+#pragma unroll
+  for (int i = 0; i < TL::TMW; ++i)
+#pragma unroll
+    for (int j = 0; j < TL::TNW; ++j) clear(i, j);
+
+  // The products of step s, while the other step's fragments (of the slot at rd) come
+  // in and the issuing side's loads into slot wr go out.
+  constexpr int NM = TL::NM, MID = NM / 2;
+  auto step = [&](auto ss, uint32_t rd, int wr) {
+    constexpr int s = decltype(ss)::value, o = 1 - s;
+    using O = std::integral_constant<int, o>;
+    constexpr int NR = NRX + ((TL::TRANS || o == 0) ? NRW : 0);
+    constexpr int RA = (NR + MID - 1) / MID;
+    constexpr int k0 = s == 1 ? 0 : TL::LA, k1 = s == 1 ? TL::LA : TL::L, DA = (k1 - k0 + NM - 1) / NM;
+    unrolled<NM>([&](auto mm) {
+      constexpr int m = decltype(mm)::value;
+      constexpr int i = m % TL::TMW, j = m / TL::TMW;
+      acc[i][j] = Dt<DT>::mfma16(__builtin_bit_cast(V8, fw[s][j]), __builtin_bit_cast(V8, fx[s][i]), acc[i][j]);
+      unrolled<RA>([&](auto rr) {
+        constexpr int n = m * RA + decltype(rr)::value;
+        if constexpr (m < MID && n < NR) read1(rd, O{}, std::integral_constant<int, n>{});
+      });
+      unrolled<DA>([&](auto dd) {
+        constexpr int k = k0 + m * DA + decltype(dd)::value;
+        if constexpr (k < k1) issue1(wr, std::integral_constant<int, k>{});
+      });
+      if constexpr (m == MID) {
+        lds_wait();
+        tie_reads(O{});
+      }
+      if constexpr (m >= MID) {  // piece p behind instruction MID + p (NM - MID) / NP
+        unrolled<NP>([&](auto pp) {
+          constexpr int p = decltype(pp)::value;
+          if constexpr (MID + p * (NM - MID) / NP == m) convert1(O{}, pp);
+        });
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    });
+    pin_acc();
+  };
+
+  int st = cu.st0, slot = 0;
+  int relax = 0;  // stages until the last tile's stores must be done
+  while (true) {
+    const int s1 = slot + 1 == TL::NS ? 0 : slot + 1;
+    const bool last = st + 1 == cu.st1;
+    step(S0{}, static_cast<uint32_t>(slot * TL::SLOT_BYTES), slot == 0 ? TL::NS - 1 : slot - 1);
+    issue_next();
+    // this wave has read the slot; the next slot has landed; when that holds for
+    // all waves, the slot takes the issuing side's next stage
+    if (relax > 0) {
+      --relax;
+      wait_vmcnt<TL::WAIT + TL::NST>();
+    } else {
+      wait_vmcnt<TL::WAIT>();
+    }
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    step(S1{}, static_cast<uint32_t>(s1 * TL::SLOT_BYTES), slot);
+    slot = s1;
+    ++st;
+    if (!last) continue;
+
+    // lane coordinates taken anew, so that nothing but the accumulators and the
+    // loop's own values is live across the loop
+    int el = static_cast<int>(threadIdx.x) & 63;
+    asm volatile("" : "+v"(el));
+    const uint32_t er = static_cast<uint32_t>(el & 15);
+    const bool part = cu.tail >= 0 && a.nSplit > 1;
+    // a split's fp32 tile: 16 bytes a lane, in the order the join reads it
+    f32x4* p = reinterpret_cast<f32x4*>(a.part) +
+               ((static_cast<int64_t>(cu.split) * (a.nRB * a.nTiles - a.whole) + cu.tail) * TL::NW + wave) * (NM * 64) + el;
+    const int64_t m0 = static_cast<int64_t>(cu.rb) * TL::BM + wm * TL::TMW * 16;
+    const __amdgpu_buffer_rsrc_t ry = rows_of_y(a, m0, TL::TMW * 16);
+    const int64_t c0 = static_cast<int64_t>(cu.nt) * TL::BN + wn * TL::TNW * 16;
+    constexpr int GJ = TL::TRANS ? TL::TNW : 2;
+#pragma unroll
+    for (int i = 0; i < TL::TMW; ++i)
+#pragma unroll
+      for (int j = 0; j < TL::TNW; j += GJ) {
+        // one group at a time leaves the accumulator registers
+#pragma unroll
+        for (int q = 0; q < GJ; ++q) asm volatile("" : "+a"(acc[i][j + q]));
+        if (part) {
+          if (m0 + i * 16 < a.T)
+#pragma unroll
+            for (int q = 0; q < GJ; ++q) p[(i * TL::TNW + j + q) * 64] = acc[i][j + q];
+        } else {
+          store_group<DT, TL>(ry, a.vec, i * 16 + er, a.N, c0 + j * 16, el, &acc[i][j]);
+        }
+#pragma unroll
+        for (int q = 0; q < GJ; ++q) clear(i, j + q);
+      }
+    if (!part && a.vec)
+      relax = TL::RELAX;
+    else
+      wait_vmcnt<0>();
+    if (!more) break;
+    ++ck;
+    unit_of(ck, a, cu);
+    look_ahead();
+    st = cu.st0;
+  }
+  wait_vmcnt<0>();  // the DMA past the last unit is done before the workgroup's LDS is given up
+}
+
+// One wave a group of matrix tiles of the output: its splits' sums added in order.
+template <int DT, class TL>
+__global__ __launch_bounds__(256) void q4_gemm_join(GemmArgs a) {
+  const int lane = threadIdx.x & 63;
+  constexpr int GJ = TL::TRANS ? TL::TNW : 2, PT = TL::NW * TL::NM / GJ;  // groups of a workgroup tile
+  const int64_t ntail = static_cast<int64_t>(a.nRB) * a.nTiles - a.whole;
+  const int64_t w = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
+  if (w >= ntail * PT) return;
+  const int64_t tail = w / PT;
+  const int sub = static_cast<int>(w % PT) * GJ;  // its first matrix tile
+  const int wave = sub / TL::NM, ij = sub % TL::NM, i = ij / TL::TNW, j = ij % TL::TNW;
+  int rb, nt;
+  tile_of(static_cast<uint32_t>(a.whole + tail), a, rb, nt);
+  const int wm = wave / TL::WN, wn = wave % TL::WN;
+  const int64_t m = static_cast<int64_t>(rb) * TL::BM + (wm * TL::TMW + i) * 16;
+  if (m >= a.T) return;  // rows past the last: not written either
+  const f32x4* p = reinterpret_cast<const f32x4*>(a.part) + (tail * TL::NW * TL::NM + sub) * 64 + lane;
+  f32x4 s[GJ];
+#pragma unroll
+  for (int q = 0; q < GJ; ++q) s[q] = p[q * 64];
+  for (int k = 1; k < a.nSplit; ++k) {
+    const f32x4* pk = p + static_cast<int64_t>(k) * ntail * TL::NW * TL::NM * 64;
+#pragma unroll
+    for (int q = 0; q < GJ; ++q) s[q] += pk[q * 64];
+  }
+  store_group<DT, TL>(rows_of_y(a, m, 16), a.vec, static_cast<uint32_t>(lane & 15), a.N,
+                      static_cast<int64_t>(nt) * TL::BN + (wn * TL::TNW + j) * 16, lane, s);
+}
+
 // An empty contraction: zeros (the kernels above need at least one step).
 __global__ __launch_bounds__(256) void q4_zero(uint16_t* y, int64_t n) {
   for (int64_t e = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; e < n;
@@ -220,10 +696,24 @@ __global__ __launch_bounds__(256) void q4_pad_rows(const uint16_t* x, int64_t T,
   }
 }
 
+template <bool TRANS>
+using BigTile = Q4Tile<8, 8, 3, TRANS>;  // 256 x 256
+template <bool TRANS>
+using TallTile = Q4Tile<8, 4, 4, TRANS>;  // 256 x 128
+template <bool TRANS>
+using MidTile = Q4Tile<4, 4, 6, TRANS>;  // 128 x 128
+template <bool TRANS>
+using LowTile = Q4Tile<2, 4, 8, TRANS>;  // 64 x 128, a deep ring: the weight's stream
+
+constexpr int64_t kFewRows = 16;
+
 struct GemmPlan {
+  enum Path { kLow, kMid, kTall, kBig, kFew } path = kBig;
   int64_t N = 0, K = 0, xp = 0;
+  int S = 0, nSplit = 1;
+  int64_t nRB = 0, nTiles = 0, whole = 0;
   int64_t grid = 0;
-  size_t pad = 0, bytes = 0;
+  size_t pad = 0, bytes = 0;  // of padded rows; of a split's fp32 tiles
 };
 
 GemmPlan gemm_plan(int64_t T, int64_t out, int64_t in, bool trans) {
@@ -231,28 +721,72 @@ GemmPlan gemm_plan(int64_t T, int64_t out, int64_t in, bool trans) {
   p.N = trans ? in : out;
   p.K = trans ? out : in;
   p.xp = q4_ceil(p.K, 8) * 8;
-  p.pad = p.xp != p.K ? static_cast<size_t>(T) * p.xp * 2 : 0;
-  p.bytes = p.pad;
-  const int64_t groups = q4_ceil(T, 16);
-  p.grid = trans ? q4_ceil(in, 128) * groups : q4_ceil(out, kQ4Rows) * groups;
-  return p;
+  p.pad = p.xp != p.K ? (static_cast<size_t>(T) * p.xp * 2 + 255) / 256 * 256 : 0;
+  p.S = static_cast<int>(q4_ceil(p.K, kQ4Cols));
+  if (T <= kFewRows) {
+    p.path = GemmPlan::kFew;
+    p.grid = trans ? q4_ceil(in, 128) : q4_ceil(out, kQ4Rows);
+    return p;
+  }
+  static constexpr struct {
+    GemmPlan::Path path;
+    int64_t bm, bn;
+    double us;
+  } tiles[] = {{GemmPlan::kLow, 64, 128, 0.30},
+               {GemmPlan::kMid, 128, 128, 0.40},
+               {GemmPlan::kTall, 256, 128, 0.70},
+               {GemmPlan::kBig, 256, 256, 1.30}};
+  GemmPlan best;
+  double least = 0.0;
+  for (const auto& t : tiles) {
+    GemmPlan q = p;
+    q.path = t.path;
+    const double us = split_plan(q, T, t.bm, t.bn, t.us);
+    if (least == 0.0 || us < least) least = us, best = q;
+  }
+  return best;
 }
 
-template <int DT>
-void launch_typed(const GemmArgs& g, const GemmPlan& p, bool trans, hipStream_t stream) {
+template <int DT, class TL>
+void launch_tile(const GemmArgs& g, const GemmPlan& p, hipStream_t stream) {
+  hipLaunchKernelGGL((q4_gemm_tile<DT, TL>), dim3(static_cast<unsigned>(p.grid)), dim3(TL::NT), 0, stream, g);
+  if (p.nSplit > 1) {
+    const int64_t waves = (p.nRB * p.nTiles - p.whole) * TL::NW * TL::NM / (TL::TRANS ? TL::TNW : 2);
+    hipLaunchKernelGGL((q4_gemm_join<DT, TL>), dim3(static_cast<unsigned>(q4_ceil(waves, 4))), dim3(256), 0, stream, g);
+  }
+}
+
+template <int DT, bool TRANS>
+void launch_typed(const GemmArgs& g, const GemmPlan& p, hipStream_t stream) {
   const dim3 grid(static_cast<unsigned>(p.grid));
-  if (trans)
-    hipLaunchKernelGGL((q4_few_bwd<DT, 1, 8>), grid, dim3(512), 0, stream, g);
-  else
-    hipLaunchKernelGGL((q4_few<DT, 1, 16>), grid, dim3(1024), 0, stream, g);
+  switch (p.path) {
+    case GemmPlan::kFew:
+      if constexpr (TRANS)
+        hipLaunchKernelGGL((q4_few_bwd<DT, 1, 8>), grid, dim3(512), 0, stream, g);
+      else
+        hipLaunchKernelGGL((q4_few<DT, 1, 16>), grid, dim3(1024), 0, stream, g);
+      return;
+    case GemmPlan::kLow:
+      return launch_tile<DT, LowTile<TRANS>>(g, p, stream);
+    case GemmPlan::kMid:
+      return launch_tile<DT, MidTile<TRANS>>(g, p, stream);
+    case GemmPlan::kTall:
+      return launch_tile<DT, TallTile<TRANS>>(g, p, stream);
+    case GemmPlan::kBig:
+      return launch_tile<DT, BigTile<TRANS>>(g, p, stream);
+  }
 }
 
 }  // namespace
 
 size_t q4_gemm_workspace_bytes(int64_t T, int64_t out, int64_t in, bool trans) {
-  return gemm_plan(T, out, in, trans).bytes;
+  const GemmPlan p = gemm_plan(T, out, in, trans);
+  return p.pad + p.bytes;
 }
-int64_t q4_gemm_max_grid(int64_t T, int64_t out, int64_t in, bool trans) { return gemm_plan(T, out, in, trans).grid; }
+int64_t q4_gemm_max_grid(int64_t T, int64_t out, int64_t in, bool trans) {
+  const GemmPlan p = gemm_plan(T, out, in, trans);
+  return std::max(p.grid, p.nRB * p.nTiles * 16);  // units of work (tiles in up to 16 ranges) are numbered in 32 bits
+}
 
 hipError_t launch_q4_gemm(const Q4GemmArgs& p) {
   const GemmPlan plan = gemm_plan(p.T, p.out, p.in, p.trans);
@@ -277,15 +811,21 @@ hipError_t launch_q4_gemm(const Q4GemmArgs& p) {
   g.we = static_cast<const uint8_t*>(p.we);
   g.T = p.T;
   g.N = plan.N;
-  g.K = plan.K;
   g.rt = static_cast<int>(q4_ceil(p.out, kQ4Rows));
   g.ct = static_cast<int>(q4_ceil(p.in, kQ4Cols));
+  g.S = plan.S;
+  g.nRB = static_cast<int>(plan.nRB);
+  g.nTiles = static_cast<int>(plan.nTiles);
+  g.nSplit = plan.nSplit;
+  g.whole = static_cast<int>(plan.whole);
+  g.group = 8;
   g.y = p.y;
   g.vec = plan.N % 8 == 0 && (reinterpret_cast<uintptr_t>(p.y) & 15u) == 0;
+  g.part = reinterpret_cast<float*>(static_cast<char*>(p.ws) + plan.pad);
   if (p.dtype == 0)
-    launch_typed<0>(g, plan, p.trans, p.stream);
+    p.trans ? launch_typed<0, true>(g, plan, p.stream) : launch_typed<0, false>(g, plan, p.stream);
   else
-    launch_typed<1>(g, plan, p.trans, p.stream);
+    p.trans ? launch_typed<1, true>(g, plan, p.stream) : launch_typed<1, false>(g, plan, p.stream);
   return hipGetLastError();
 }
 

@@ -44,6 +44,7 @@
 
 #include "dma_common.hpp"
 #include "q8_common.hpp"
+#include "tile_units.hpp"
 
 namespace dora {
 
@@ -110,69 +111,16 @@ struct Q8Tile {
   static_assert(LDS_BYTES <= 160 * 1024, "LDS");
 };
 
-constexpr int kCUs = 256;
-
-struct GemmArgs {
+struct GemmArgs : TileGrid {
   const uint8_t *xq, *xe, *wq, *we;
   int64_t T, N;      // output rows and columns
   int64_t xp, wp;    // bytes of a row of xq and wq
   int64_t xep, wep;  // bytes of a row of exponents
   int64_t wrows;     // rows of wq (whole tiles)
-  int S;             // stages (of 128) of the contraction
-  // units of work: tiles [0, whole) over the whole contraction, then tiles
-  // [whole, nRB * nTiles) in nSplit ranges of its stages each
-  int nRB, nTiles, whole, nSplit;
-  uint32_t group;  // column tiles of a group of the tile order
   void* y;
   int vec;  // 16-byte stores of y
   float* part;
 };
-
-// Tile order: groups of `group` column tiles, row blocks within a group, on
-// XCD-contiguous ranges: an XCD's concurrent tiles form a block of rows and
-// columns whose panels its L2 holds for all of them.
-__device__ inline void tile_of(uint32_t v, const GemmArgs& a, int& rb, int& nt) {
-  const uint32_t nRB = static_cast<uint32_t>(a.nRB), nTl = static_cast<uint32_t>(a.nTiles), G = a.group;
-  const uint32_t grp = v / (G * nRB);
-  const uint32_t gn = min(G, nTl - grp * G);
-  const uint32_t loc = v - grp * G * nRB;
-  rb = static_cast<int>(loc / gn);
-  nt = static_cast<int>(grp * G + loc % gn);
-}
-
-// The k-th unit of work of this workgroup (of the 8 XCDs x gridDim.x/8): false
-// past its last.  An XCD takes contiguous ranges of the whole tiles and of the
-// split ones.
-struct Unit {
-  int rb, nt, st0, st1, split, tail;  // tail: index among the split tiles, -1 for a whole tile
-};
-__device__ inline bool unit_of(int k, const GemmArgs& a, Unit& u) {
-  // (opaque, so that nothing of this moves out of the rare branches it stands in)
-  asm volatile("" : "+s"(k));
-  const int x = blockIdx.x & 7, i = blockIdx.x >> 3, per = gridDim.x >> 3;
-  const int wpx = (a.whole + 7) >> 3;  // whole tiles of an XCD
-  const int w0 = min(x * wpx, a.whole), w1 = min(w0 + wpx, a.whole);
-  const int rounds = (w1 - w0 + per - 1 - i) / per;  // whole tiles of this workgroup
-  int v;
-  if (k < rounds) {
-    v = w0 + k * per + i;
-    u.st0 = 0;
-    u.st1 = a.S;
-    u.split = 0;
-    u.tail = -1;
-  } else {
-    const int ntail = a.nRB * a.nTiles - a.whole, nun = ntail * a.nSplit, upx = (nun + 7) >> 3;
-    const int j = (k - rounds) * per + i, n = x * upx + j;
-    if (j >= upx || n >= nun) return false;
-    u.split = n / ntail;
-    u.tail = n - u.split * ntail;
-    v = a.whole + u.tail;
-    u.st0 = a.S * u.split / a.nSplit;  // S <= 2^16
-    u.st1 = a.S * (u.split + 1) / a.nSplit;
-  }
-  tile_of(static_cast<uint32_t>(v), a, u.rb, u.nt);
-  return true;
-}
 
 // Rows of y from a wave's accumulators: register q of lane l is output column
 // 8*(q/4) + 4*(l/32) + q%4 of its tile, row l%32.  Packed in pairs, two groups
@@ -213,10 +161,6 @@ __device__ inline void store_tile(__amdgpu_buffer_rsrc_t ry, int vec, uint32_t r
   }
 }
 
-__device__ inline __amdgpu_buffer_rsrc_t buffer_of(const void* p, int64_t bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), static_cast<short>(0), static_cast<int>(bytes),
-                                           kBufferWord3);
-}
 // Rows [m, m + most) of y, as far as they exist.
 __device__ inline __amdgpu_buffer_rsrc_t rows_of_y(const GemmArgs& a, int64_t m, int most) {
   const int64_t rows = min(max(a.T - m, int64_t(0)), static_cast<int64_t>(most));
@@ -744,37 +688,6 @@ struct GemmPlan {
   int64_t grid = 0;
   size_t bytes = 0;
 };
-
-// Tiles of bm x bn: as many rounds of one whole tile a CU as there are, and the
-// rest in up to 16 ranges of stages each (at least four stages), whichever number
-// is expected to be fastest.  Returns the expected microseconds: a stage of the
-// tile (13 % more where the reads transpose), 1.4 for the start and end of a
-// unit, and for a split 3.0 + 0.43 a range for the join's launch and sums and
-// 0.25 a MB of fp32 partials, written and read.
-double split_plan(GemmPlan& p, int64_t T, int64_t bm, int64_t bn, double stage_us) {
-  p.nRB = q8_ceil(T, bm);
-  p.nTiles = q8_ceil(p.N, bn);
-  const int64_t tiles = p.nRB * p.nTiles;
-  const int64_t rounds = tiles / kCUs, rest = tiles - rounds * kCUs;
-  p.whole = rounds * kCUs;
-  p.nSplit = 1;
-  const double unit_us = 1.4;
-  double best = 0.0;
-  if (rest > 0) {
-    best = p.S * stage_us + unit_us;
-    // a tile's rows that exist are written, on the mean of the tiles
-    const double mb = static_cast<double>(rest) * bn * 4e-6 * static_cast<double>(T) / static_cast<double>(p.nRB);
-    for (int s = 2; s <= 16 && p.S / s >= 4; ++s) {
-      const double c =
-          static_cast<double>(q8_ceil(rest * s, kCUs)) * (static_cast<double>(q8_ceil(p.S, s)) * stage_us + unit_us) +
-          3.0 + 0.43 * s + 0.25 * mb * s;
-      if (c < best) best = c, p.nSplit = s;
-    }
-  }
-  p.grid = std::min<int64_t>(kCUs, q8_ceil(p.whole + rest * p.nSplit, 8) * 8);
-  p.bytes = p.nSplit > 1 ? static_cast<size_t>(rest) * p.nSplit * bm * bn * 4 : 0;
-  return static_cast<double>(rounds) * (p.S * stage_us + unit_us) + best;
-}
 
 // The tile is the one expected to be fastest.  The times are fitted to 5257 calls
 // (six weights from 1024 x 8192 to 27648 x 5120, both directions, 9 to 8192 rows,
