@@ -44,71 +44,181 @@ __device__ inline void store8(const GemmArgs& a, int64_t row, int64_t c, const f
   }
 }
 
-// Few rows, forward.  A workgroup owns one row of tiles (32 output columns) and
-// 16 * NT tokens; its waves take the steps of 128 columns in turn and their sums
-// meet in LDS.  The weight goes from global memory straight into the fragments of
-// mfma 16x16x32: lane l holds row l % 16 of a half tile and block l / 16 of the
-// four, 16 bytes, and the rows' values at the same 32 columns.
-template <int DT, int NT, int NW>
-__global__ __launch_bounds__(64 * NW) void q4_few(GemmArgs a) {
+// ------------------------------------------------------------------ few rows
+//
+// The weight is streamed once, from global memory straight into the fragments of mfma
+// 16x16x32; the rows of x come through the caches.  A workgroup owns a group of
+// outputs and one of `splits` ranges of the contraction, whose steps its waves take
+// in turn; their sums meet in LDS, those of the ranges in q4_few_join.
+
+// The outputs of an entry (a register quad of lane l) of a forward group: register q
+// is row 8 * (l / 16) + 4 * half + q of the row tile, for token l % 16.
+template <int DT>
+__device__ inline void store4(const GemmArgs& a, int64_t row, int64_t c, f32x4 v) {
+  using T16 = typename Dt<DT>::T;
+  typedef T16 t4 __attribute__((ext_vector_type(4)));
+  if (row >= a.T || c >= a.N) return;
+  T16* y = static_cast<T16*>(a.y) + row * a.N + c;
+  const t4 o = {Dt<DT>::from_f(v[0]), Dt<DT>::from_f(v[1]), Dt<DT>::from_f(v[2]), Dt<DT>::from_f(v[3])};
+  if (a.vec) {  // N % 8 == 0
+    *reinterpret_cast<t4*>(y) = o;
+  } else {
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (c + q < a.N) y[q] = o[q];
+  }
+}
+
+// Chunk i of lane group g (of 16 lanes) changes places with chunk g of group i.
+__device__ inline void turn4(Chunk (&x)[4]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const auto a = __builtin_amdgcn_permlane32_swap(x[0].w[j], x[2].w[j], false, false);
+    const auto b = __builtin_amdgcn_permlane32_swap(x[1].w[j], x[3].w[j], false, false);
+    const auto c = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
+    const auto d = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
+    x[0].w[j] = c[0], x[1].w[j] = c[1], x[2].w[j] = d[0], x[3].w[j] = d[1];
+  }
+}
+
+// Forward: R row tiles (of 32 output columns) and NT token tiles (of 16) a group,
+// steps of 128 columns, U of them in registers.  Lane l holds row l % 16 of a half row
+// tile and block l / 16 of the step's four, 16 bytes, and x at the same 32 columns.
+// x is loaded 64 consecutive bytes of a row an instruction, each lane group a quarter
+// of a block, and then turned between the groups (with each group's own block at once,
+// 64 pieces of 16 bytes an instruction: 2 to 6 % slower from 32 rows on).
+template <int NT_, int R_, int NW_, int U_>
+struct FewFwd {
+  static constexpr int NT = NT_, R = R_, NW = NW_, U = U_;
+  static constexpr int ENTRIES = R * NT * 2 * 64;  // register quads of a group
+};
+
+template <int DT, class FW>
+__global__ __launch_bounds__(64 * FW::NW) void q4_few(GemmArgs a) {
   using V8 = typename Dt<DT>::V8;
   using T16 = typename Dt<DT>::T;
-  __shared__ f32x4 red[NW][2][64];
+  constexpr int NT = FW::NT, R = FW::R, NW = FW::NW, U = FW::U;
+  __shared__ f32x4 red[NW][NT * 2 * 64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const uint32_t n = lane & 15, gb = lane >> 4;
-  const uint32_t rb = blockIdx.x % static_cast<uint32_t>(a.rt);
-  const int64_t t0 = static_cast<int64_t>(blockIdx.x / static_cast<uint32_t>(a.rt)) * (16 * NT);
-  const uint32_t at = q4_unit(n & 3, n >> 2, gb & 1), eat = 32 * (gb & 1) + 2 * n;
-  const uint8_t* wq = a.wq + static_cast<int64_t>(rb) * a.ct * kQ4TileQ + at;
-  const uint8_t* we = a.we + static_cast<int64_t>(rb) * a.ct * kQ4TileE + eat;
-  f32x4 acc[NT][2];
-#pragma unroll
-  for (int t = 0; t < NT; ++t) acc[t][0] = acc[t][1] = f32x4{};
+  const uint32_t groups = static_cast<uint32_t>(a.rt + R - 1) / R;
+  const uint32_t grp = blockIdx.x % groups, split = blockIdx.x / groups;
   const int steps = (a.ct + 1) / 2;
-  for (int s = wave; s < steps; s += NW) {
+  const int s0 = static_cast<int>(static_cast<int64_t>(steps) * split / a.nSplit);
+  const int s1 = static_cast<int>(static_cast<int64_t>(steps) * (split + 1) / a.nSplit);
+  const uint32_t at = q4_unit(n & 3, n >> 2, gb & 1), eat = 32 * (gb & 1) + 2 * n;
+  const uint8_t *wq[R], *we[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {  // past the last row tile: that one again, not stored
+    const int64_t rt = min(static_cast<int64_t>(grp) * R + r, static_cast<int64_t>(a.rt - 1));
+    wq[r] = a.wq + rt * a.ct * kQ4TileQ + at;
+    we[r] = a.we + rt * a.ct * kQ4TileE + eat;
+  }
+  const T16* xr[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t)  // past the last row: that one again, not stored
+    xr[t] = static_cast<const T16*>(a.x) + min(static_cast<int64_t>(16 * t + n), a.T - 1) * a.xp + 8 * gb;
+  f32x4 acc[R][NT][2];
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int t = 0; t < NT; ++t) acc[r][t][0] = acc[r][t][1] = f32x4{};
+  u32x4 w[U][R][2];
+  uint32_t e[U][R];
+  Chunk x[U][NT][4];
+  auto load = [&](auto uu, int s) {
+    constexpr int u = decltype(uu)::value;
     // past the last tile: that one again, against zeros
     const int64_t tile = min(2 * s + static_cast<int>(gb >> 1), a.ct - 1);
-    const u32x4 w0 = *reinterpret_cast<const u32x4*>(wq + tile * kQ4TileQ);
-    const u32x4 w1 = *reinterpret_cast<const u32x4*>(wq + tile * kQ4TileQ + 512);
-    const uint32_t e = *reinterpret_cast<const uint16_t*>(we + tile * kQ4TileE);
-    const float s0 = q4_scale(e & 255), s1 = q4_scale(e >> 8);
-    const int64_t k = static_cast<int64_t>(s) * 128 + 32 * gb;
-    Chunk x[NT][4];
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const int64_t row = t0 + 16 * t + n;
-      const T16* xr = static_cast<const T16*>(a.x) + row * a.xp + k;
-#pragma unroll
-      for (int m = 0; m < 4; ++m)
-        x[t][m] = row < a.T && k + 8 * m < a.xp ? *reinterpret_cast<const Chunk*>(xr + 8 * m) : zero_chunk();
+    for (int r = 0; r < R; ++r) {
+      w[u][r][0] = *reinterpret_cast<const u32x4*>(wq[r] + tile * kQ4TileQ);
+      w[u][r][1] = *reinterpret_cast<const u32x4*>(wq[r] + tile * kQ4TileQ + 512);
+      e[u][r] = *reinterpret_cast<const uint16_t*>(we[r] + tile * kQ4TileE);
     }
+    if (static_cast<int64_t>(s + 1) * 128 <= a.xp) {
 #pragma unroll
-    for (int m = 0; m < 4; ++m) {
-      const V8 f0 = __builtin_bit_cast(V8, q4_decode8<DT>(w0[m], s0));
-      const V8 f1 = __builtin_bit_cast(V8, q4_decode8<DT>(w1[m], s1));
+      for (int t = 0; t < NT; ++t)
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        acc[t][0] = Dt<DT>::mfma16(f0, __builtin_bit_cast(V8, x[t][m]), acc[t][0]);
-        acc[t][1] = Dt<DT>::mfma16(f1, __builtin_bit_cast(V8, x[t][m]), acc[t][1]);
+        for (int m = 0; m < 4; ++m) x[u][t][m] = *reinterpret_cast<const Chunk*>(xr[t] + s * 128 + 32 * m);
+    } else {  // the step that the rows end in
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+          x[u][t][m] = s * 128 + 32 * m + static_cast<int>(8 * gb) < a.xp
+                           ? *reinterpret_cast<const Chunk*>(xr[t] + s * 128 + 32 * m)
+                           : zero_chunk();
+    }
+  };
+  auto multiply = [&](auto uu) {
+    constexpr int u = decltype(uu)::value;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) turn4(x[u][t]);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const float sc0 = q4_scale(e[u][r] & 255u), sc1 = q4_scale(e[u][r] >> 8);
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        const V8 f0 = __builtin_bit_cast(V8, q4_decode8<DT>(w[u][r][0][m], sc0));
+        const V8 f1 = __builtin_bit_cast(V8, q4_decode8<DT>(w[u][r][1][m], sc1));
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          acc[r][t][0] = Dt<DT>::mfma16(f0, __builtin_bit_cast(V8, x[u][t][m]), acc[r][t][0]);
+          acc[r][t][1] = Dt<DT>::mfma16(f1, __builtin_bit_cast(V8, x[u][t][m]), acc[r][t][1]);
+        }
+      }
+    }
+  };
+  // U - 1 steps are in flight while one is multiplied
+  unrolled<U - 1>([&](auto uu) {
+    if (s0 + wave + decltype(uu)::value * NW < s1) load(uu, s0 + wave + decltype(uu)::value * NW);
+  });
+  for (int s = s0 + wave; s < s1; s += NW * U) {
+    unrolled<U>([&](auto uu) {
+      constexpr int u = decltype(uu)::value, nu = (u + U - 1) % U;
+      if (s + u * NW < s1) {
+        if (s + (u + U - 1) * NW < s1) load(std::integral_constant<int, nu>{}, s + (u + U - 1) * NW);
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(uu);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    });
+  }
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    if (r > 0) __syncthreads();
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) red[wave][(t * 2 + h) * 64 + lane] = acc[r][t][h];
+    __syncthreads();
+    for (int i = threadIdx.x; i < NT * 2 * 64; i += 64 * NW) {
+      f32x4 v = red[0][i];
+#pragma unroll
+      for (int w = 1; w < NW; ++w) v += red[w][i];
+      if (a.nSplit > 1) {
+        reinterpret_cast<f32x4*>(a.part)[(static_cast<int64_t>(blockIdx.x) * R + r) * (NT * 2 * 64) + i] = v;
+      } else {
+        const int l = i & 63, h = (i >> 6) & 1, t = i >> 7;
+        store4<DT>(a, 16 * t + (l & 15), (static_cast<int64_t>(grp) * R + r) * 32 + 8 * (l >> 4) + 4 * h, v);
       }
     }
   }
-  // register q of lane l is row 4 * (l / 16) + q of its half tile, for token l % 16:
-  // rows 8 * (l / 16) + 0 .. 7 of the tile with the other half's
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    if (t > 0) __syncthreads();
-    red[wave][0][lane] = acc[t][0];
-    red[wave][1][lane] = acc[t][1];
-    __syncthreads();
-    if (wave == 0) {
-      f32x4 s0 = red[0][0][lane], s1 = red[0][1][lane];
-#pragma unroll
-      for (int w = 1; w < NW; ++w) s0 += red[w][0][lane], s1 += red[w][1][lane];
-      const float f[8] = {s0[0], s0[1], s0[2], s0[3], s1[0], s1[1], s1[2], s1[3]};
-      store8<DT>(a, t0 + 16 * t + n, static_cast<int64_t>(rb) * 32 + 8 * gb, f);
-    }
-  }
+}
+
+// One thread an entry: its ranges' sums added in order.
+template <int DT, class FW>
+__global__ __launch_bounds__(256) void q4_few_join(GemmArgs a) {
+  const int64_t groups = (a.rt + FW::R - 1) / FW::R, all = groups * FW::ENTRIES;
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= all) return;
+  const f32x4* p = reinterpret_cast<const f32x4*>(a.part) + i;
+  f32x4 v = p[0];
+  for (int k = 1; k < a.nSplit; ++k) v += p[k * all];
+  const int64_t rt = i / (FW::NT * 2 * 64);
+  const int j = static_cast<int>(i % (FW::NT * 2 * 64)), l = j & 63, h = (j >> 6) & 1, t = j >> 7;
+  store4<DT>(a, 16 * t + (l & 15), rt * 32 + 8 * (l >> 4) + 4 * h, v);
 }
 
 // Two 16-bit values of two words: their low halves, their high halves.
@@ -121,29 +231,44 @@ __device__ inline float scale_of_row(const u32x2& e, int i) {
   return q4_scale((w >> (16 * (i & 1) + 8 * (i >> 2))) & 255u);
 }
 
-// Few rows, backward.  A workgroup owns 128 output columns (two tiles) and 16 * NT
-// tokens; its waves take the rows of tiles in turn.  Lane l holds eight columns,
-// 8 * (l % 16) .. + 7, of rows 8 * (l / 16) .. + 7: a row's eight values are
-// converted with its scale, two rows' then paired by column, and fragment f has
-// columns 8 n + f.
-template <int DT, int NT, int NW>
-__global__ __launch_bounds__(64 * NW) void q4_few_bwd(GemmArgs a) {
+// Few rows, backward.  A group is 128 output columns (two tiles) and NT token tiles;
+// a step is a row of tiles.  Lane l holds eight columns, 8 * (l % 16) .. + 7, of rows
+// 8 * (l / 16) .. + 7: a row's eight values are converted with its scale, two rows' then
+// paired by column, and fragment f has columns 8 n + f.
+template <int NT_, int NW_>
+struct FewBwd {
+  static constexpr int NT = NT_, NW = NW_;
+  static constexpr int ENTRIES = NT * 8 * 64;  // register quads of a group
+};
+
+// Register q of lane l of the eight fragments: columns 8 * (4 * (l / 16) + q) + 0 .. 7
+// of token l % 16.
+template <int DT>
+__device__ inline void store_few_bwd(const GemmArgs& a, int64_t grp, int t, int q, int l, const float (&v)[8]) {
+  store8<DT>(a, 16 * t + (l & 15), grp * 128 + 32 * (l >> 4) + 8 * q, v);
+}
+
+template <int DT, class FW>
+__global__ __launch_bounds__(64 * FW::NW) void q4_few_bwd(GemmArgs a) {
   using V8 = typename Dt<DT>::V8;
   using T16 = typename Dt<DT>::T;
-  __shared__ f32x4 red[NW][8][64];
+  constexpr int NT = FW::NT, NW = FW::NW;
+  __shared__ f32x4 red[NW][8 * 64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const uint32_t n = lane & 15, g = lane >> 4;
-  const uint32_t pairs = static_cast<uint32_t>(a.ct + 1) / 2;
-  const uint32_t cb = blockIdx.x % pairs;
-  const int64_t t0 = static_cast<int64_t>(blockIdx.x / pairs) * (16 * NT);
+  const uint32_t groups = static_cast<uint32_t>(a.ct + 1) / 2;
+  const uint32_t grp = blockIdx.x % groups, split = blockIdx.x / groups;
+  const int r0 = static_cast<int>(static_cast<int64_t>(a.rt) * split / a.nSplit);
+  const int r1 = static_cast<int>(static_cast<int64_t>(a.rt) * (split + 1) / a.nSplit);
   const uint32_t b = (n >> 2) & 1;
-  const int64_t col_tile = min(static_cast<int64_t>(2 * cb + (n >> 3)), static_cast<int64_t>(a.ct - 1));
+  // past the last tile: that one again, not stored
+  const int64_t col_tile = min(2 * static_cast<int>(grp) + static_cast<int>(n >> 3), a.ct - 1);
   f32x4 acc[NT][8];
 #pragma unroll
   for (int t = 0; t < NT; ++t)
 #pragma unroll
     for (int f = 0; f < 8; ++f) acc[t][f] = f32x4{};
-  for (int rt = wave; rt < a.rt; rt += NW) {
+  for (int rt = r0 + wave; rt < r1; rt += NW) {
     const int64_t tile = static_cast<int64_t>(rt) * a.ct + col_tile;
     const uint8_t* wq = a.wq + tile * kQ4TileQ + 4 * (n & 3);
     uint32_t w[8];
@@ -154,7 +279,7 @@ __global__ __launch_bounds__(64 * NW) void q4_few_bwd(GemmArgs a) {
     Chunk x[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      const int64_t row = t0 + 16 * t + n;
+      const int64_t row = 16 * t + n;
       x[t] = row < a.T && k < a.xp ? *reinterpret_cast<const Chunk*>(static_cast<const T16*>(a.x) + row * a.xp + k)
                                    : zero_chunk();
     }
@@ -177,58 +302,80 @@ __global__ __launch_bounds__(64 * NW) void q4_few_bwd(GemmArgs a) {
       }
     }
   }
-  // register q of lane l and fragment f is column 8 * (4 * (l / 16) + q) + f of token l % 16
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
     if (t > 0) __syncthreads();
 #pragma unroll
-    for (int f = 0; f < 8; ++f) red[wave][f][lane] = acc[t][f];
+    for (int f = 0; f < 8; ++f) red[wave][f * 64 + lane] = acc[t][f];
     __syncthreads();
-    // a quarter of the columns a wave
-    if (wave < 4) {
-      float v[8];
+    static_assert(NW == 8, "one register quad a thread");
+    const int i = threadIdx.x;
+    f32x4 v = red[0][i];
 #pragma unroll
-      for (int f = 0; f < 8; ++f) {
-        v[f] = reinterpret_cast<const float*>(&red[0][f][lane])[wave];
+    for (int w = 1; w < NW; ++w) v += red[w][i];
+    if (a.nSplit > 1) {
+      reinterpret_cast<f32x4*>(a.part)[(static_cast<int64_t>(blockIdx.x) * NT + t) * (8 * 64) + i] = v;
+    } else {
+      red[0][i] = v;
+      __syncthreads();
+      if (wave < 4) {  // a quarter of the columns a wave
+        float o[8];
 #pragma unroll
-        for (int w = 1; w < NW; ++w) v[f] += reinterpret_cast<const float*>(&red[w][f][lane])[wave];
+        for (int f = 0; f < 8; ++f) o[f] = reinterpret_cast<const float*>(&red[0][f * 64 + lane])[wave];
+        store_few_bwd<DT>(a, grp, t, wave, lane, o);
       }
-      store8<DT>(a, t0 + 16 * t + n, static_cast<int64_t>(cb) * 128 + 32 * g + 8 * wave, v);
     }
   }
 }
 
+// One thread eight columns: their ranges' sums added in order.
+template <int DT, class FW>
+__global__ __launch_bounds__(256) void q4_few_bwd_join(GemmArgs a) {
+  const int64_t groups = (a.ct + 1) / 2, all = groups * FW::ENTRIES;
+  const int64_t tile = blockIdx.x;  // of a group: its token tile
+  const int q = threadIdx.x >> 6, l = threadIdx.x & 63;
+  const float* p = a.part + ((tile * 8) * 64 + l) * 4 + q;
+  float v[8];
+#pragma unroll
+  for (int f = 0; f < 8; ++f) v[f] = p[f * 256];
+  for (int k = 1; k < a.nSplit; ++k)
+#pragma unroll
+    for (int f = 0; f < 8; ++f) v[f] += p[k * all * 4 + f * 256];
+  store_few_bwd<DT>(a, tile / FW::NT, static_cast<int>(tile % FW::NT), q, l, v);
+}
+
 // ------------------------------------------------------------------ tiles
 //
-// Tile geometry: 2 x 2 waves, each TMW x TNW matrix tiles of 16 x 16 with their
+// Tile geometry: WM x WN waves (four), each TMW x TNW matrix tiles of 16 x 16 with their
 // accumulators in registers; a ring of NS slots of one stage, 64 contraction steps
 // of both operands.  x goes to LDS as rows of 128 bytes, logical 16-byte chunk c of
 // row p in place c ^ ((p/2) % 8), so that 16 consecutive rows at one chunk fall in 16
 // distinct bank groups; the weight's 4-bit tiles as they are, 64 bytes apart from
 // their neighbours (the backward's lanes read two tiles at once).
-template <int TMW_, int TNW_, int NS_, bool TRANS_>
+template <int WM_, int WN_, int TMW_, int TNW_, int NS_, int OCC_, bool TRANS_>
 struct Q4Tile {
-  static constexpr int TMW = TMW_, TNW = TNW_, NS = NS_;
+  static constexpr int WM = WM_, WN = WN_, TMW = TMW_, TNW = TNW_, NS = NS_, OCC = OCC_;
   static constexpr bool TRANS = TRANS_;
-  static constexpr int WM = 2, WN = 2, NW = 4, NT = 256;
+  static constexpr int NW = 4, NT = 256;
   static constexpr int BM = 16 * TMW * WM, BN = 16 * TNW * WN, BK = 64;
   static constexpr int WT = BN / 32, WSTEP = static_cast<int>(kQ4TileQ) + 64;  // weight tiles of a stage
-  static constexpr int X_BYTES = BM * BK * 2, W_BYTES = WT * WSTEP, E_BYTES = NW * 256;
+  static constexpr int XQ = (BM / 8 + NW - 1) / NW;  // x rows come eight an instruction
+  static constexpr int X_BYTES = XQ * NW * 1024, W_BYTES = WT * WSTEP, E_BYTES = NW * 256;
   static constexpr int SLOT_BYTES = X_BYTES + W_BYTES + E_BYTES;
   static constexpr int LDS_BYTES = NS * SLOT_BYTES;
-  static constexpr int XQ = BM / 8 / NW, WQ = WT / NW, L = XQ + WQ + 1;  // DMA instructions a wave
+  static constexpr int WQ = WT / NW, L = XQ + WQ + 1;  // DMA instructions a wave
   static constexpr int CT = BN / 64;  // column tiles of the backward's stage (two row tiles)
   static constexpr int NM = TMW * TNW;  // matrix instructions of a step of 32
   static constexpr int NST = NM / 2;    // 16-byte stores of a wave's tile
   static constexpr int WAIT = (NS - 2) * L;   // DMA instructions younger than the slot waited for
   static constexpr int LA = (L + 1) / 2;      // a slot's loads stand in the step after it is free and in the next one
   static constexpr int RELAX = NS - 2;        // stages whose slot was loaded before a tile's stores
-  static_assert(XQ * 8 * NW == BM && WQ * NW == WT, "whole DMA instructions per wave");
+  static_assert(WM * WN == NW && WQ * NW == WT, "whole DMA instructions per wave");
   static_assert(WT * 16 <= NW * 64, "exponents of a stage in one DMA instruction a wave");
   static_assert(!TRANS || TNW == 8 || TNW == 4, "a backward lane's columns");
   static_assert(TNW % 2 == 0 && NS >= 3, "pairs of half tiles; the ring");
   static_assert(WAIT + NST < 64, "vmcnt range");
-  static_assert(LDS_BYTES <= 160 * 1024, "LDS");
+  static_assert(LDS_BYTES * OCC <= 160 * 1024, "LDS");
 };
 
 template <int OFF>
@@ -310,7 +457,7 @@ __device__ inline void store_group(__amdgpu_buffer_rsrc_t ry, int vec, uint32_t 
 // before: reads stand behind its first matrix instructions, the conversions behind
 // its last ones.
 template <int DT, class TL>
-__global__ __launch_bounds__(TL::NT, 1) void q4_gemm_tile(GemmArgs a) {
+__global__ __launch_bounds__(TL::NT, TL::OCC) void q4_gemm_tile(GemmArgs a) {
   using V8 = typename Dt<DT>::V8;
   __shared__ __attribute__((aligned(1024))) char smem[TL::LDS_BYTES];
   const int tid = threadIdx.x, lane = tid & 63;
@@ -696,19 +843,23 @@ __global__ __launch_bounds__(256) void q4_pad_rows(const uint16_t* x, int64_t T,
   }
 }
 
+// Two or three workgroups a CU, with a wave an SIMD each, whose waits the others' work
+// covers.  (One of 256 x 256 a CU: 734 and 741 us forward at 8192^2 x 8192, 854 and 806
+// backward; one of 64 x 256, with a ring of twice the slots, 8 to 12 % slower.)
 template <bool TRANS>
-using BigTile = Q4Tile<8, 8, 3, TRANS>;  // 256 x 256
+using WideTile = Q4Tile<1, 4, 8, 4, 3, 2, TRANS>;  // 128 x 256
 template <bool TRANS>
-using TallTile = Q4Tile<8, 4, 4, TRANS>;  // 256 x 128
+using BroadTile = Q4Tile<1, 4, 6, 4, 3, 2, TRANS>;  // 96 x 256
 template <bool TRANS>
-using MidTile = Q4Tile<4, 4, 6, TRANS>;  // 128 x 128
+using FlatTile = Q4Tile<1, 4, 4, 4, 4, 2, TRANS>;  // 64 x 256
 template <bool TRANS>
-using LowTile = Q4Tile<2, 4, 8, TRANS>;  // 64 x 128, a deep ring: the weight's stream
-
-constexpr int64_t kFewRows = 16;
+using ThinTile = Q4Tile<1, 4, 3, 4, 4, 2, TRANS>;  // 48 x 256
+template <bool TRANS>
+using LowTile = Q4Tile<2, 2, 2, 4, 3, 3, TRANS>;  // 64 x 128
 
 struct GemmPlan {
-  enum Path { kLow, kMid, kTall, kBig, kFew } path = kBig;
+  enum Path { kLow, kThin, kFlat, kBroad, kWide, kFew } path = kWide;
+  int R = 1;  // row tiles of a group of few rows
   int64_t N = 0, K = 0, xp = 0;
   int S = 0, nSplit = 1;
   int64_t nRB = 0, nTiles = 0, whole = 0;
@@ -716,6 +867,81 @@ struct GemmPlan {
   size_t pad = 0, bytes = 0;  // of padded rows; of a split's fp32 tiles
 };
 
+// Few rows: groups of R row tiles (forward) or 128 columns (backward), each in so many
+// ranges of the contraction.
+void few_plan(GemmPlan& p, int64_t T, int64_t out, int64_t in, bool trans, int R, int splits) {
+  const int64_t groups = trans ? q4_ceil(in, 128) : q4_ceil(q4_ceil(out, kQ4Rows), R);
+  p.path = GemmPlan::kFew;
+  p.R = R;
+  p.nSplit = splits;
+  p.grid = groups * splits;
+  const int64_t entries = (trans ? 8 : 2 * R) * 64 * q4_ceil(T, 16);  // register quads of a group
+  p.bytes = splits > 1 ? static_cast<size_t>(p.grid * entries) * 16 : 0;
+}
+
+// Expected microseconds of few rows.  A workgroup's waves take `steps` steps each, a
+// step as long as its matrix tiles ask for, on every CU as many workgroups at once as
+// its registers allow; the weight's and the rows' bytes into the CUs come on top, and
+// for ranges the join's launch, its sums and the partial sums written and read.
+double few_us(const GemmPlan& p, int64_t T, int64_t out, int64_t in, bool trans) {
+  const int64_t nt = q4_ceil(T, 16), groups = p.grid / p.nSplit;
+  const double w_mb = static_cast<double>(out) * in * 17e-6 / 32, x_mb = 2e-6 * groups * T * p.K;
+  const double part_mb = static_cast<double>(p.bytes) * 1e-6;
+  if (trans) {
+    const int64_t steps = q4_ceil(q4_ceil(q4_ceil(out, kQ4Rows), p.nSplit), 8);
+    return 2.65 + 0.104 * (w_mb + 0.34 * x_mb) + q4_ceil(p.grid, 2 * kCUs) * steps * (0.351 + 0.218 * nt) +
+           (p.nSplit > 1 ? 1.13 + 0.43 * p.nSplit + 0.42 * part_mb : 0.0);
+  }
+  const int64_t rnt = p.R * nt, steps = q4_ceil(q4_ceil(q4_ceil(in, 128), p.nSplit), rnt == 1 ? 16 : 8);
+  return 2.95 + 0.069 * (w_mb + 0.77 * x_mb) + q4_ceil(p.grid, (rnt == 2 ? 2 : 1) * kCUs) * steps * (0.788 + 0.237 * rnt) +
+         (p.nSplit > 1 ? 1.27 + 0.25 * p.nSplit + 0.58 * part_mb : 0.0);
+}
+
+struct TileKind {
+  GemmPlan::Path path;
+  int64_t bm, bn, occ;
+  double us[2][3];  // a stage forward and backward, with one to three workgroups on a CU
+};
+constexpr TileKind kTiles[] = {
+    {GemmPlan::kLow, 64, 128, 3, {{0.368, 0.522, 0.685}, {0.576, 0.813, 0.954}}},
+    {GemmPlan::kThin, 48, 256, 2, {{0.443, 0.627, 0.0}, {0.639, 0.843, 0.0}}},
+    {GemmPlan::kFlat, 64, 256, 2, {{0.509, 0.748, 0.0}, {0.682, 0.940, 0.0}}},
+    {GemmPlan::kBroad, 96, 256, 2, {{0.669, 1.035, 0.0}, {0.841, 1.163, 0.0}}},
+    {GemmPlan::kWide, 128, 256, 2, {{0.804, 1.386, 0.0}, {0.981, 1.501, 0.0}}},
+};
+
+// Tiles of one kind: as many rounds of one whole tile a workgroup as there are, and the
+// rest in up to 16 ranges of stages each (at least four stages), whichever number is
+// expected to be fastest.  Returns the expected microseconds.
+double tile_us(GemmPlan& p, int64_t T, const TileKind& t, bool trans) {
+  const double* us = t.us[trans ? 1 : 0];
+  const int64_t slots = kCUs * t.occ;
+  p.path = t.path;
+  p.nRB = q4_ceil(T, t.bm);
+  p.nTiles = q4_ceil(p.N, t.bn);
+  const int64_t tiles = p.nRB * p.nTiles, rounds = tiles / slots, rest = tiles - rounds * slots;
+  p.whole = rounds * slots;
+  p.nSplit = 1;
+  double least = 0.0;
+  // a tile's rows that exist are written, on the mean of the tiles
+  const double mb = static_cast<double>(rest) * t.bn * 4e-6 * static_cast<double>(T) / static_cast<double>(p.nRB);
+  for (int s = 1; rest > 0 && s <= 16 && (s == 1 || p.S / s >= 4); ++s) {
+    double c = s > 1 ? 2.65 + 0.29 * s + 0.235 * mb * s : 0.0;
+    for (int64_t left = rest * s; left > 0; left -= slots)
+      c += static_cast<double>(q4_ceil(p.S, s)) * us[q4_ceil(std::min(left, slots), kCUs) - 1];
+    if (s == 1 || c < least) least = c, p.nSplit = s;
+  }
+  p.grid = std::min<int64_t>(slots, q4_ceil(p.whole + rest * p.nSplit, 8) * 8);
+  p.bytes = p.nSplit > 1 ? static_cast<size_t>(rest) * p.nSplit * t.bm * t.bn * 4 : 0;
+  return 5.0 + static_cast<double>(rounds) * p.S * us[t.occ - 1] + least;
+}
+
+// The kernel, its tile and its ranges are those expected to be fastest.  The times are
+// fitted to 5600 calls (nine weights from 512 x 512 to 27648 x 5120, both directions, 1
+// to 8192 rows, every kind with 1 to 16 ranges, weights out of the caches); over them
+// the plan's call takes 1.1 % more than the fastest measured one on the mean with the
+// tiles (12 % at most) and 2.8 % forward, 1.2 % backward with the kernels for few rows
+// (21 % at most).
 GemmPlan gemm_plan(int64_t T, int64_t out, int64_t in, bool trans) {
   GemmPlan p;
   p.N = trans ? in : out;
@@ -723,26 +949,24 @@ GemmPlan gemm_plan(int64_t T, int64_t out, int64_t in, bool trans) {
   p.xp = q4_ceil(p.K, 8) * 8;
   p.pad = p.xp != p.K ? (static_cast<size_t>(T) * p.xp * 2 + 255) / 256 * 256 : 0;
   p.S = static_cast<int>(q4_ceil(p.K, kQ4Cols));
-  if (T <= kFewRows) {
-    p.path = GemmPlan::kFew;
-    p.grid = trans ? q4_ceil(in, 128) : q4_ceil(out, kQ4Rows);
-    return p;
-  }
-  static constexpr struct {
-    GemmPlan::Path path;
-    int64_t bm, bn;
-    double us;
-  } tiles[] = {{GemmPlan::kLow, 64, 128, 0.30},
-               {GemmPlan::kMid, 128, 128, 0.40},
-               {GemmPlan::kTall, 256, 128, 0.70},
-               {GemmPlan::kBig, 256, 256, 1.30}};
   GemmPlan best;
-  double least = 0.0;
-  for (const auto& t : tiles) {
+  double least = -1.0;
+  auto take = [&](const GemmPlan& q, double us) {
+    if (least < 0.0 || us < least) least = us, best = q;
+  };
+  if (T <= (trans ? 32 : 48)) {
+    for (int R = 1; R <= (trans ? 1 : 4); R *= 2)
+      for (int splits : {1, 2, 3, 4, 6, 8, 12, 16}) {
+        if (splits > 1 && p.S / splits < 8) break;
+        GemmPlan q = p;
+        few_plan(q, T, out, in, trans, R, splits);
+        take(q, few_us(q, T, out, in, trans));
+      }
+  }
+  for (const TileKind& t : kTiles) {
     GemmPlan q = p;
-    q.path = t.path;
-    const double us = split_plan(q, T, t.bm, t.bn, t.us);
-    if (least == 0.0 || us < least) least = us, best = q;
+    const double us = tile_us(q, T, t, trans);
+    take(q, us);
   }
   return best;
 }
@@ -756,24 +980,59 @@ void launch_tile(const GemmArgs& g, const GemmPlan& p, hipStream_t stream) {
   }
 }
 
+template <int DT, class FW>
+void launch_few_as(const GemmArgs& g, const GemmPlan& p, hipStream_t stream) {
+  hipLaunchKernelGGL((q4_few<DT, FW>), dim3(static_cast<unsigned>(p.grid)), dim3(64 * FW::NW), 0, stream, g);
+  if (p.nSplit > 1) {
+    const int64_t entries = p.grid / p.nSplit * FW::ENTRIES;
+    hipLaunchKernelGGL((q4_few_join<DT, FW>), dim3(static_cast<unsigned>(q4_ceil(entries, 256))), dim3(256), 0, stream, g);
+  }
+}
+template <int DT, int NT>
+void launch_few_nt(const GemmArgs& g, const GemmPlan& p, hipStream_t stream) {
+  switch (p.R) {
+    case 1:
+      return launch_few_as<DT, FewFwd<NT, 1, NT == 1 ? 16 : 8, 2>>(g, p, stream);
+    case 2:
+      return launch_few_as<DT, FewFwd<NT, 2, 8, 2>>(g, p, stream);
+    default:
+      return launch_few_as<DT, FewFwd<NT, 4, 8, NT <= 2 ? 2 : 1>>(g, p, stream);
+  }
+}
+template <int DT, int NT>
+void launch_few_bwd(const GemmArgs& g, const GemmPlan& p, hipStream_t stream) {
+  using FW = FewBwd<NT, 8>;
+  hipLaunchKernelGGL((q4_few_bwd<DT, FW>), dim3(static_cast<unsigned>(p.grid)), dim3(64 * FW::NW), 0, stream, g);
+  if (p.nSplit > 1)
+    hipLaunchKernelGGL((q4_few_bwd_join<DT, FW>), dim3(static_cast<unsigned>(p.grid / p.nSplit * NT)), dim3(256), 0,
+                       stream, g);
+}
+template <int DT, bool TRANS>
+void launch_few(const GemmArgs& g, const GemmPlan& p, hipStream_t stream) {
+  const int nt = static_cast<int>((g.T + 15) / 16);
+  if constexpr (TRANS)
+    return nt == 1 ? launch_few_bwd<DT, 1>(g, p, stream) : launch_few_bwd<DT, 2>(g, p, stream);
+  else
+    return nt == 1   ? launch_few_nt<DT, 1>(g, p, stream)
+           : nt == 2 ? launch_few_nt<DT, 2>(g, p, stream)
+                     : launch_few_nt<DT, 3>(g, p, stream);
+}
+
 template <int DT, bool TRANS>
 void launch_typed(const GemmArgs& g, const GemmPlan& p, hipStream_t stream) {
-  const dim3 grid(static_cast<unsigned>(p.grid));
   switch (p.path) {
     case GemmPlan::kFew:
-      if constexpr (TRANS)
-        hipLaunchKernelGGL((q4_few_bwd<DT, 1, 8>), grid, dim3(512), 0, stream, g);
-      else
-        hipLaunchKernelGGL((q4_few<DT, 1, 16>), grid, dim3(1024), 0, stream, g);
-      return;
+      return launch_few<DT, TRANS>(g, p, stream);
     case GemmPlan::kLow:
       return launch_tile<DT, LowTile<TRANS>>(g, p, stream);
-    case GemmPlan::kMid:
-      return launch_tile<DT, MidTile<TRANS>>(g, p, stream);
-    case GemmPlan::kTall:
-      return launch_tile<DT, TallTile<TRANS>>(g, p, stream);
-    case GemmPlan::kBig:
-      return launch_tile<DT, BigTile<TRANS>>(g, p, stream);
+    case GemmPlan::kThin:
+      return launch_tile<DT, ThinTile<TRANS>>(g, p, stream);
+    case GemmPlan::kFlat:
+      return launch_tile<DT, FlatTile<TRANS>>(g, p, stream);
+    case GemmPlan::kBroad:
+      return launch_tile<DT, BroadTile<TRANS>>(g, p, stream);
+    case GemmPlan::kWide:
+      return launch_tile<DT, WideTile<TRANS>>(g, p, stream);
   }
 }
 

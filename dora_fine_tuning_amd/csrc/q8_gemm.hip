@@ -689,6 +689,37 @@ struct GemmPlan {
   size_t bytes = 0;
 };
 
+// Tiles of bm x bn: as many rounds of one whole tile a CU as there are, and the
+// rest in up to 16 ranges of stages each (at least four stages), whichever number
+// is expected to be fastest.  Returns the expected microseconds: a stage of the
+// tile (13 % more where the reads transpose), 1.4 for the start and end of a
+// unit, and for a split 3.0 + 0.43 a range for the join's launch and sums and
+// 0.25 a MB of fp32 partials, written and read.
+double split_plan(GemmPlan& p, int64_t T, int64_t bm, int64_t bn, double stage_us) {
+  p.nRB = q8_ceil(T, bm);
+  p.nTiles = q8_ceil(p.N, bn);
+  const int64_t tiles = p.nRB * p.nTiles;
+  const int64_t rounds = tiles / kCUs, rest = tiles - rounds * kCUs;
+  p.whole = rounds * kCUs;
+  p.nSplit = 1;
+  const double unit_us = 1.4;
+  double best = 0.0;
+  if (rest > 0) {
+    best = p.S * stage_us + unit_us;
+    // a tile's rows that exist are written, on the mean of the tiles
+    const double mb = static_cast<double>(rest) * bn * 4e-6 * static_cast<double>(T) / static_cast<double>(p.nRB);
+    for (int s = 2; s <= 16 && p.S / s >= 4; ++s) {
+      const double c =
+          static_cast<double>(q8_ceil(rest * s, kCUs)) * (static_cast<double>(q8_ceil(p.S, s)) * stage_us + unit_us) +
+          3.0 + 0.43 * s + 0.25 * mb * s;
+      if (c < best) best = c, p.nSplit = s;
+    }
+  }
+  p.grid = std::min<int64_t>(kCUs, q8_ceil(p.whole + rest * p.nSplit, 8) * 8);
+  p.bytes = p.nSplit > 1 ? static_cast<size_t>(rest) * p.nSplit * bm * bn * 4 : 0;
+  return static_cast<double>(rounds) * (p.S * stage_us + unit_us) + best;
+}
+
 // The tile is the one expected to be fastest.  The times are fitted to 5257 calls
 // (six weights from 1024 x 8192 to 27648 x 5120, both directions, 9 to 8192 rows,
 // every tile, 1 to 16 ranges); over them the plan's call takes 0.8 % more than the

@@ -5,8 +5,6 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include <algorithm>
-
 #include "dma_common.hpp"
 
 namespace dora {
@@ -70,39 +68,6 @@ __device__ inline bool unit_of(int k, const TileGrid& a, Unit& u) {
 __device__ inline __amdgpu_buffer_rsrc_t buffer_of(const void* p, int64_t bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(p), static_cast<short>(0), static_cast<int>(bytes),
                                            kBufferWord3);
-}
-
-// Tiles of bm x bn: as many rounds of one whole tile a CU as there are, and the
-// rest in up to 16 ranges of stages each (at least four stages), whichever number
-// is expected to be fastest.  Returns the expected microseconds: a stage of the
-// tile (13 % more where the reads transpose), 1.4 for the start and end of a
-// unit, and for a split 3.0 + 0.43 a range for the join's launch and sums and
-// 0.25 a MB of fp32 partials, written and read.
-template <class Plan>
-double split_plan(Plan& p, int64_t T, int64_t bm, int64_t bn, double stage_us) {
-  const auto ceil_of = [](int64_t n, int64_t k) { return (n + k - 1) / k; };
-  p.nRB = ceil_of(T, bm);
-  p.nTiles = ceil_of(p.N, bn);
-  const int64_t tiles = p.nRB * p.nTiles;
-  const int64_t rounds = tiles / kCUs, rest = tiles - rounds * kCUs;
-  p.whole = rounds * kCUs;
-  p.nSplit = 1;
-  const double unit_us = 1.4;
-  double best = 0.0;
-  if (rest > 0) {
-    best = p.S * stage_us + unit_us;
-    // a tile's rows that exist are written, on the mean of the tiles
-    const double mb = static_cast<double>(rest) * bn * 4e-6 * static_cast<double>(T) / static_cast<double>(p.nRB);
-    for (int s = 2; s <= 16 && p.S / s >= 4; ++s) {
-      const double c =
-          static_cast<double>(ceil_of(rest * s, kCUs)) * (static_cast<double>(ceil_of(p.S, s)) * stage_us + unit_us) +
-          3.0 + 0.43 * s + 0.25 * mb * s;
-      if (c < best) best = c, p.nSplit = s;
-    }
-  }
-  p.grid = std::min<int64_t>(kCUs, ceil_of(p.whole + rest * p.nSplit, 8) * 8);
-  p.bytes = p.nSplit > 1 ? static_cast<size_t>(rest) * p.nSplit * bm * bn * 4 : 0;
-  return static_cast<double>(rounds) * (p.S * stage_us + unit_us) + best;
 }
 
 }  // namespace dora
