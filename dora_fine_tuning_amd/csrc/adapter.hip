@@ -34,8 +34,7 @@ namespace {
 // each other by ballots over the keys' bits, the lowest of them moves the
 // counter, and a lane's rank is the number of such lanes below it.
 constexpr int kSortWaves = 16, kSortThreads = 64 * kSortWaves;
-constexpr int kSortRounds = 4;       // of 64 slots a wave, at least
-constexpr int64_t kSortChunks = 256;  // workgroups, at most
+constexpr int kSortRounds = 4;  // of 64 slots a wave, whose keys stay in registers
 
 struct SortArgs {
   const void* ids;
@@ -58,12 +57,22 @@ __device__ inline int key_of(const SortArgs& a, int64_t slot) {
   return v >= 0 && v < a.n ? v : a.n;
 }
 
-// Counts of the workgroup's waves: cnt[wave * (n + 1) + key].
-__device__ inline void count_keys(const SortArgs& a, int32_t* cnt, int64_t first, int wave, int lane) {
+// The wave's keys of its first rounds, -1 past the last slot, and the counts of the
+// workgroup's waves: cnt[wave * (n + 1) + key].
+__device__ inline void count_keys(const SortArgs& a, int32_t* cnt, int64_t first, int wave, int lane,
+                                  int (&mine)[kSortRounds]) {
   const int keys = a.n + 1;
+#pragma unroll
+  for (int r = 0; r < kSortRounds; ++r) {
+    const int64_t slot = first + r * 64 + lane;
+    mine[r] = r < a.rounds && slot < a.N ? key_of(a, slot) : -1;
+  }
   for (int i = threadIdx.x; i < keys * kSortWaves; i += kSortThreads) cnt[i] = 0;
   __syncthreads();
-  for (int r = 0; r < a.rounds; ++r) {
+#pragma unroll
+  for (int r = 0; r < kSortRounds; ++r)
+    if (mine[r] >= 0) atomicAdd(&cnt[wave * keys + mine[r]], 1);
+  for (int r = kSortRounds; r < a.rounds; ++r) {
     const int64_t slot = first + r * 64 + lane;
     if (slot < a.N) atomicAdd(&cnt[wave * keys + key_of(a, slot)], 1);
   }
@@ -77,9 +86,11 @@ __device__ inline int64_t first_slot(const SortArgs& a, int wave) {
 __global__ __launch_bounds__(kSortThreads) void adapter_count(SortArgs a) {
   extern __shared__ int32_t cnt[];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, keys = a.n + 1;
-  count_keys(a, cnt, first_slot(a, wave), wave, lane);
+  int mine[kSortRounds];
+  count_keys(a, cnt, first_slot(a, wave), wave, lane, mine);
   for (int key = threadIdx.x; key < keys; key += kSortThreads) {
     int32_t s = 0;
+#pragma unroll
     for (int w = 0; w < kSortWaves; ++w) s += cnt[w * keys + key];
     a.table[static_cast<int64_t>(blockIdx.x) * keys + key] = s;
   }
@@ -90,22 +101,26 @@ __global__ __launch_bounds__(kSortThreads) void adapter_sort_k(SortArgs a) {
   __shared__ int32_t sums[kSortWaves];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, keys = a.n + 1;
   const int64_t first = first_slot(a, wave);
-  count_keys(a, cnt, first, wave, lane);
+  int mine[kSortRounds];
+  count_keys(a, cnt, first, wave, lane, mine);
 
-  // an adapter a thread (n <= 1000): all its slots, and those of earlier workgroups
+  // a key a thread (n <= 1000, and the slots without an adapter): its slots in the
+  // waves, in all, and in earlier workgroups
   const int key = threadIdx.x;
-  int32_t total = 0, before = 0, none_before = 0;
-  if (a.chunks == 1) {
-    if (key < a.n)
-      for (int w = 0; w < kSortWaves; ++w) total += cnt[w * keys + key];
-  } else {
-    if (key < a.n)
+  int32_t of_wave[kSortWaves], total = 0, before = 0;
+  if (key < keys) {
+#pragma unroll
+    for (int w = 0; w < kSortWaves; ++w) of_wave[w] = cnt[w * keys + key];
+    if (a.chunks == 1) {
+#pragma unroll
+      for (int w = 0; w < kSortWaves; ++w) total += of_wave[w];
+    } else {
+#pragma unroll 8
       for (int c = 0; c < a.chunks; ++c) {
         if (c == static_cast<int>(blockIdx.x)) before = total;
         total += a.table[static_cast<int64_t>(c) * keys + key];
       }
-    if (key == 0)
-      for (int c = 0; c < static_cast<int>(blockIdx.x); ++c) none_before += a.table[static_cast<int64_t>(c) * keys + a.n];
+    }
   }
   // the first row of each: an exclusive sum over the threads
   int32_t upto = total;
@@ -116,36 +131,26 @@ __global__ __launch_bounds__(kSortThreads) void adapter_sort_k(SortArgs a) {
   }
   if (lane == 63) sums[wave] = upto;
   __syncthreads();
-  int32_t lower = 0, all = 0;
+  int32_t lower = 0;
 #pragma unroll
-  for (int w = 0; w < kSortWaves; ++w) {
-    if (w < wave) lower += sums[w];
-    all += sums[w];
-  }
+  for (int w = 0; w < kSortWaves; ++w) lower += w < wave ? sums[w] : 0;
   const int32_t start = lower + upto - total;
-  if (blockIdx.x == 0) {
-    if (key < a.n) a.bounds[key] = start;
-    if (key == 0) a.bounds[a.n] = all;
-  }
-  // counters of the waves: the next row of each key
-  auto rows_from = [&](int kk, int32_t row) {
+  if (key < keys) {
+    if (blockIdx.x == 0) a.bounds[key] = start;  // the last key's start is the end of the adapters' rows
+    // the counters become the next row of each key
+    int32_t row = start + before;
+#pragma unroll
     for (int w = 0; w < kSortWaves; ++w) {
-      const int32_t c = cnt[w * keys + kk];
-      cnt[w * keys + kk] = row;
-      row += c;
+      cnt[w * keys + key] = row;
+      row += of_wave[w];
     }
-  };
-  if (key < a.n) rows_from(key, start + before);
-  if (key == 0) rows_from(a.n, all + none_before);
+  }
   __syncthreads();
 
   const uint64_t below = (uint64_t(1) << lane) - 1;
-  for (int r = 0; r < a.rounds; ++r) {
-    const int64_t slot = first + r * 64 + lane;
-    const bool on = slot < a.N;
-    const int kk = on ? key_of(a, slot) : 0;
+  auto place64 = [&](int r, int kk) {
+    const bool on = kk >= 0;
     uint64_t same = __ballot(on);
-    if (same == 0) break;  // the same for the wave
     for (int b = 0; b < a.bits; ++b) {
       const uint64_t set = __ballot((kk >> b) & 1);
       same &= ((kk >> b) & 1) ? set : ~set;
@@ -156,15 +161,27 @@ __global__ __launch_bounds__(kSortThreads) void adapter_sort_k(SortArgs a) {
       if (lane == lead) row = atomicAdd(&cnt[wave * keys + kk], __popcll(same));
       row = __shfl(row, lead, 64) + __popcll(same & below);
       const bool has = kk < a.n;
+      const int64_t slot = first + r * 64 + lane;
       const int32_t s32 = static_cast<int32_t>(slot);
       a.order[row] = has ? s32 : ~s32;
       a.place[slot] = has ? row : ~row;
     }
+  };
+#pragma unroll
+  for (int r = 0; r < kSortRounds; ++r)
+    if (r < a.rounds) place64(r, mine[r]);
+  for (int r = kSortRounds; r < a.rounds; ++r) {
+    const int64_t slot = first + r * 64 + lane;
+    place64(r, slot < a.N ? key_of(a, slot) : -1);
   }
 }
 
+// Up to 4096 slots are one workgroup's, in one launch.  More are spread over up to 64
+// with one to four rounds each, and beyond over 256, whose table each of them reads.
 int sort_rounds(int64_t N) {
-  return static_cast<int>(std::max<int64_t>(kSortRounds, q4_ceil(N, kSortChunks * kSortThreads)));
+  if (N <= kSortThreads * kSortRounds) return static_cast<int>(std::max<int64_t>(1, q4_ceil(N, kSortThreads)));
+  if (N <= 64 * kSortThreads * kSortRounds) return static_cast<int>(q4_ceil(N, 64 * kSortThreads));
+  return static_cast<int>(std::max<int64_t>(kSortRounds, q4_ceil(N, 256 * kSortThreads)));
 }
 int64_t sort_chunks(int64_t N) { return std::max<int64_t>(1, q4_ceil(N, int64_t(kSortThreads) * sort_rounds(N))); }
 
@@ -248,21 +265,31 @@ __global__ __launch_bounds__(kRowThreads) void adapter_combine_k(RowsArgs a) {
       if (a.base && c0 + u * step < a.D) b = load_chunk<DT, VEC>(a.base, t, c0 + u * step, a.D);
       chunk_to_f32<DT>(b, s[u]);
     }
-    for (int j = 0; j < a.k; ++j) {
-      const int32_t p = a.place[t * a.k + j];
-      if (p < 0 || p >= a.R) continue;
-      const float w = a.w ? a.w[t * a.k + j] : 1.0f;
-      Chunk v[kU];
+    for (int j0 = 0; j0 < a.k; j0 += 2) {  // two slots' loads at a time, added in order
+      Chunk v[2][kU];
+      float w[2];
+      bool on[2];
 #pragma unroll
-      for (int u = 0; u < kU; ++u)
-        if (c0 + u * step < a.D) v[u] = load_chunk<DT, VEC>(a.rows, p, c0 + u * step, a.D);
+      for (int h = 0; h < 2; ++h) {
+        const int64_t slot = t * a.k + j0 + h;
+        const int32_t p = j0 + h < a.k ? a.place[slot] : -1;
+        on[h] = p >= 0 && p < a.R;
+        w[h] = on[h] && a.w ? a.w[slot] : 1.0f;
 #pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        if (c0 + u * step >= a.D) break;
-        float f[8];
-        chunk_to_f32<DT>(v[u], f);
+        for (int u = 0; u < kU; ++u)
+          if (on[h] && c0 + u * step < a.D) v[h][u] = load_chunk<DT, VEC>(a.rows, p, c0 + u * step, a.D);
+      }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) s[u][i] = __builtin_fmaf(w, f[i], s[u][i]);
+      for (int h = 0; h < 2; ++h) {
+        if (!on[h]) continue;
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+          if (c0 + u * step >= a.D) break;
+          float f[8];
+          chunk_to_f32<DT>(v[h][u], f);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) s[u][i] = __builtin_fmaf(w[h], f[i], s[u][i]);
+        }
       }
     }
 #pragma unroll

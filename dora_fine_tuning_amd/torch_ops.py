@@ -533,20 +533,9 @@ _BELOW_AUTOGRAD = torch._C._after_autograd_keyset
 
 
 def _refuse_tangents(name, args):
-    if fwad._current_level >= 0:
-        for a in args:
-            if isinstance(a, Tensor) and fwad.unpack_dual(a).tangent is not None:
-                raise RuntimeError(f"{name} has no forward-mode derivative")
-
-
-def _refuse_gradients(name, args):
-    grad, duals = torch.is_grad_enabled(), fwad._current_level >= 0
-    if grad or duals:
-        for a in args:
-            if isinstance(a, Tensor) and (grad and a.requires_grad
-                                          or duals and fwad.unpack_dual(a).tangent is not None):
-                hint = ", or use q8_layer" if name.startswith("q8_") else ""
-                raise RuntimeError(f"{name} has no gradient of its own: pass detached tensors{hint}")
+    for a in args:
+        if isinstance(a, Tensor) and fwad.unpack_dual(a).tangent is not None:
+            raise RuntimeError(f"{name} has no gradient of its own in forward mode: pass tensors without tangents")
 
 
 def _q8_kernel(name, gradient=None):
@@ -571,11 +560,15 @@ def _q8_kernel(name, gradient=None):
         direct = {}  # by a key set's bits: the device's kernel where nothing else is left of it, else None
 
         def autograd(keyset, *args):
-            if gradient is not None and torch.is_grad_enabled() and any(
-                    isinstance(a, Tensor) and a.requires_grad for a in args):
+            if fwad._current_level >= 0:
                 _refuse_tangents(name, args)
-                return gradient.apply(functools.partial(below, keyset), *args)
-            _refuse_gradients(name, args)
+            if torch.is_grad_enabled():
+                for a in args:
+                    if isinstance(a, Tensor) and a.requires_grad:
+                        if gradient is None:
+                            hint = ", or use q8_layer" if name.startswith("q8_") else ""
+                            raise RuntimeError(f"{name} has no gradient of its own: pass detached tensors{hint}")
+                        return gradient.apply(functools.partial(below, keyset), *args)
             return below(keyset, *args)
 
         def below(keyset, *args):
