@@ -16,7 +16,8 @@ constexpr int64_t kMaxCols = int64_t(1) << 22;
 int check_slots(const char* fn, int64_t T, int64_t k) {
   if (T < 0 || k < 0) return fail(DORA_INVALID_ARG, "%s: negative size (%lld, %lld)", fn, (long long)T, (long long)k);
   if (T > kMaxSlots || k > kMaxSlots || T * k > kMaxSlots)
-    return fail(DORA_UNSUPPORTED, "%s: %lld tokens of %lld slots are more than 2^31 - 1", fn, (long long)T, (long long)k);
+    return fail(DORA_UNSUPPORTED, "%s: %lld tokens of %lld slots are more than 2^31 - 1", fn, (long long)T,
+                (long long)k);
   return DORA_OK;
 }
 
@@ -48,7 +49,8 @@ bool wide(int64_t D, P... p) {
 extern "C" {
 
 size_t dora_adapter_sort_workspace_bytes(int64_t T, int64_t k, int64_t n) {
-  if (T <= 0 || k <= 0 || n < 0 || n > dora::kMaxAdapters || T > kMaxSlots || k > kMaxSlots || T * k > kMaxSlots) return 0;
+  if (T <= 0 || k <= 0 || n < 0 || n > dora::kMaxAdapters) return 0;
+  if (T > kMaxSlots || k > kMaxSlots || T * k > kMaxSlots) return 0;
   return dora::adapter_sort_workspace_bytes(T * k, n);
 }
 
@@ -59,7 +61,8 @@ int dora_adapter_sort(const void* ids, int id_bytes, int64_t T, int64_t k, int64
   if (int st = check_slots(fn, T, k)) return st;
   if (n < 0) return fail(DORA_INVALID_ARG, "%s: %lld adapters", fn, (long long)n);
   if (n > dora::kMaxAdapters)
-    return fail(DORA_UNSUPPORTED, "%s: %lld adapters are more than %lld", fn, (long long)n, (long long)dora::kMaxAdapters);
+    return fail(DORA_UNSUPPORTED, "%s: %lld adapters are more than %lld", fn, (long long)n,
+                (long long)dora::kMaxAdapters);
   const int64_t N = T * k;
   if (int st = need(fn, "bounds", bounds, 4)) return st;
   if (N > 0) {

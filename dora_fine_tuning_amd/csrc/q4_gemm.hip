@@ -348,10 +348,14 @@ __global__ __launch_bounds__(256) void q4_few_bwd_join(GemmArgs a) {
 //
 // Tile geometry: WM x WN waves (four), each TMW x TNW matrix tiles of 16 x 16 with their
 // accumulators in registers; a ring of NS slots of one stage, 64 contraction steps
-// of both operands.  x goes to LDS as rows of 128 bytes, logical 16-byte chunk c of
-// row p in place c ^ ((p/2) % 8), so that 16 consecutive rows at one chunk fall in 16
-// distinct bank groups; the weight's 4-bit tiles as they are, 64 bytes apart from
-// their neighbours (the backward's lanes read two tiles at once).
+// of both operands.  x goes to LDS as rows of 128 bytes, the 16-byte chunk that lane
+// group g of the reads takes in step s in place (4 s + g) ^ ((p/2) % 8) of row p: a
+// read's lanes go through the banks in parties of eight rows of one group and the other
+// eight of the next, and so meet 16 distinct bank groups.  (In the order 2 g + s of the
+// forward's columns they met two and two: 46 % of the LDS cycles, and 741 us instead of
+// 722, at 8192^2 x 8192.)  The weight's
+// 4-bit tiles go as they are, 64 bytes apart from their neighbours (the backward's lanes
+// read two tiles at once).
 template <int WM_, int WN_, int TMW_, int TNW_, int NS_, int OCC_, bool TRANS_>
 struct Q4Tile {
   static constexpr int WM = WM_, WN = WN_, TMW = TMW_, TNW = TNW_, NS = NS_, OCC = OCC_;
@@ -370,6 +374,11 @@ struct Q4Tile {
   static constexpr int WAIT = (NS - 2) * L;   // DMA instructions younger than the slot waited for
   static constexpr int LA = (L + 1) / 2;      // a slot's loads stand in the step after it is free and in the next one
   static constexpr int RELAX = NS - 2;        // stages whose slot was loaded before a tile's stores
+  // While a wave multiplies it goes before the other workgroups' waves on its SIMD, so
+  // that these convert and wait meanwhile instead of all doing the same at once: the
+  // widest tile backward 7 to 12 % faster (8192^2 x 8192: 805 and 728 us), the small ones
+  // 1 % on the mean; not forward in the widest, where it is 0.5 % slower.
+  static constexpr bool FIRST = TRANS || TMW < 8;
   static_assert(WM * WN == NW && WQ * NW == WT, "whole DMA instructions per wave");
   static_assert(WT * 16 <= NW * 64, "exponents of a stage in one DMA instruction a wave");
   static_assert(!TRANS || TNW == 8 || TNW == 4, "a backward lane's columns");
@@ -472,7 +481,8 @@ __global__ __launch_bounds__(TL::NT, TL::OCC) void q4_gemm_tile(GemmArgs a) {
   // past an operand reads zero; past the last unit everything does, so that every
   // step issues the same instructions and the waits count them exactly)
   const int xr = wave * 8 + (lane >> 3);  // x row of DMA instruction 0
-  const int xc = (lane & 7) ^ ((xr >> 1) & 7);  // its logical chunk
+  const int xp = (lane & 7) ^ ((xr >> 1) & 7);  // its logical chunk, in the order 4 s + g that the reads ask for
+  const int xc = TL::TRANS ? xp : ((xp & 3) << 1) | (xp >> 2);
   const uint32_t xo = static_cast<uint32_t>(xr * a.xp) * 2 + 16 * xc;
   const uint32_t xstep = static_cast<uint32_t>(TL::NW * 8 * a.xp) * 2;
   const int et = (wave * 64 + lane) >> 4;  // weight tile whose exponents this lane loads
@@ -494,7 +504,8 @@ __global__ __launch_bounds__(TL::NT, TL::OCC) void q4_gemm_tile(GemmArgs a) {
 #pragma unroll
       for (int q = 0; q < TL::WQ; ++q)
         wat[q] = static_cast<uint32_t>(q * TL::NW + wave) * rowq + static_cast<uint32_t>(ist) * kQ4TileQ + 16 * lane;
-      eat = et < TL::WT ? static_cast<uint32_t>(et) * rowe + static_cast<uint32_t>(ist) * kQ4TileE + 4 * (lane & 15) : kOob;
+      eat = et < TL::WT ? static_cast<uint32_t>(et) * rowe + static_cast<uint32_t>(ist) * kQ4TileE + 4 * (lane & 15)
+                        : kOob;
     }
   };
   auto issue_unit = [&](Unit u) {
@@ -511,9 +522,11 @@ __global__ __launch_bounds__(TL::NT, TL::OCC) void q4_gemm_tile(GemmArgs a) {
         wat[q] = c < a.ct ? (t / TL::CT) * rowq + static_cast<uint32_t>(c) * kQ4TileQ + 16 * lane : kOob;
       }
       const int c = in0 + et % TL::CT;
-      eat = et < TL::WT && c < a.ct ? (et / TL::CT) * rowe + static_cast<uint32_t>(c) * kQ4TileE + 4 * (lane & 15) : kOob;
+      eat = et < TL::WT && c < a.ct ? (et / TL::CT) * rowe + static_cast<uint32_t>(c) * kQ4TileE + 4 * (lane & 15)
+                                    : kOob;
     } else {
-      const int64_t r0 = static_cast<int64_t>(u.nt) * TL::WT, n = live ? min(a.rt - r0, static_cast<int64_t>(TL::WT)) : 0;
+      const int64_t r0 = static_cast<int64_t>(u.nt) * TL::WT;
+      const int64_t n = live ? min(a.rt - r0, static_cast<int64_t>(TL::WT)) : 0;
       rw = buffer_of(a.wq + r0 * rowq, n * rowq);
       re = buffer_of(a.we + r0 * rowe, n * rowe);
     }
@@ -549,10 +562,8 @@ __global__ __launch_bounds__(TL::NT, TL::OCC) void q4_gemm_tile(GemmArgs a) {
   const int l16 = lane & 15, g = lane >> 4;
   uint32_t xa[2];
 #pragma unroll
-  for (int s = 0; s < 2; ++s) {
-    const int c = TL::TRANS ? 4 * s + g : 2 * g + s;
-    xa[s] = lds0 + static_cast<uint32_t>((wm * TL::TMW * 16 + l16) * 128 + 16 * (c ^ ((l16 >> 1) & 7)));
-  }
+  for (int s = 0; s < 2; ++s)
+    xa[s] = lds0 + static_cast<uint32_t>((wm * TL::TMW * 16 + l16) * 128 + 16 * ((4 * s + g) ^ ((l16 >> 1) & 7)));
   const uint32_t w0 = lds0 + TL::X_BYTES, e0 = w0 + TL::W_BYTES;
   uint32_t wa[TL::TRANS ? 2 : 1], ea;
   if constexpr (TL::TRANS) {
@@ -697,6 +708,7 @@ __global__ __launch_bounds__(TL::NT, TL::OCC) void q4_gemm_tile(GemmArgs a) {
     using O = std::integral_constant<int, o>;
     constexpr int NR = NRX + ((TL::TRANS || o == 0) ? NRW : 0);
     constexpr int RA = (NR + MID - 1) / MID;
+    if constexpr (TL::FIRST) __builtin_amdgcn_s_setprio(1);
     constexpr int k0 = s == 1 ? 0 : TL::LA, k1 = s == 1 ? TL::LA : TL::L, DA = (k1 - k0 + NM - 1) / NM;
     unrolled<NM>([&](auto mm) {
       constexpr int m = decltype(mm)::value;
@@ -722,6 +734,7 @@ __global__ __launch_bounds__(TL::NT, TL::OCC) void q4_gemm_tile(GemmArgs a) {
       }
       __builtin_amdgcn_sched_barrier(0);
     });
+    if constexpr (TL::FIRST) __builtin_amdgcn_s_setprio(0);
     pin_acc();
   };
 
@@ -754,8 +767,8 @@ __global__ __launch_bounds__(TL::NT, TL::OCC) void q4_gemm_tile(GemmArgs a) {
     const uint32_t er = static_cast<uint32_t>(el & 15);
     const bool part = cu.tail >= 0 && a.nSplit > 1;
     // a split's fp32 tile: 16 bytes a lane, in the order the join reads it
-    f32x4* p = reinterpret_cast<f32x4*>(a.part) +
-               ((static_cast<int64_t>(cu.split) * (a.nRB * a.nTiles - a.whole) + cu.tail) * TL::NW + wave) * (NM * 64) + el;
+    const int64_t tile = static_cast<int64_t>(cu.split) * (a.nRB * a.nTiles - a.whole) + cu.tail;
+    f32x4* p = reinterpret_cast<f32x4*>(a.part) + (tile * TL::NW + wave) * (NM * 64) + el;
     const int64_t m0 = static_cast<int64_t>(cu.rb) * TL::BM + wm * TL::TMW * 16;
     const __amdgpu_buffer_rsrc_t ry = rows_of_y(a, m0, TL::TMW * 16);
     const int64_t c0 = static_cast<int64_t>(cu.nt) * TL::BN + wn * TL::TNW * 16;
@@ -844,8 +857,9 @@ __global__ __launch_bounds__(256) void q4_pad_rows(const uint16_t* x, int64_t T,
 }
 
 // Two or three workgroups a CU, with a wave an SIMD each, whose waits the others' work
-// covers.  (One of 256 x 256 a CU: 734 and 741 us forward at 8192^2 x 8192, 854 and 806
-// backward; one of 64 x 256, with a ring of twice the slots, 8 to 12 % slower.)
+// covers.  (A workgroup of 256 x 256 a CU, in us at 8192^2 x 8192: 734 forward and 854
+// backward, against 741 and 806 of 128 x 256, both before the steps above; a workgroup of
+// 64 x 256 a CU, with a ring of twice the slots, took 8 to 12 % longer than two.)
 template <bool TRANS>
 using WideTile = Q4Tile<1, 4, 8, 4, 3, 2, TRANS>;  // 128 x 256
 template <bool TRANS>
@@ -893,7 +907,8 @@ double few_us(const GemmPlan& p, int64_t T, int64_t out, int64_t in, bool trans)
            (p.nSplit > 1 ? 1.13 + 0.43 * p.nSplit + 0.42 * part_mb : 0.0);
   }
   const int64_t rnt = p.R * nt, steps = q4_ceil(q4_ceil(q4_ceil(in, 128), p.nSplit), rnt == 1 ? 16 : 8);
-  return 2.95 + 0.069 * (w_mb + 0.77 * x_mb) + q4_ceil(p.grid, (rnt == 2 ? 2 : 1) * kCUs) * steps * (0.788 + 0.237 * rnt) +
+  const int64_t rounds = q4_ceil(p.grid, (rnt == 2 ? 2 : 1) * kCUs);
+  return 2.95 + 0.069 * (w_mb + 0.77 * x_mb) + rounds * steps * (0.788 + 0.237 * rnt) +
          (p.nSplit > 1 ? 1.27 + 0.25 * p.nSplit + 0.58 * part_mb : 0.0);
 }
 
@@ -903,11 +918,11 @@ struct TileKind {
   double us[2][3];  // a stage forward and backward, with one to three workgroups on a CU
 };
 constexpr TileKind kTiles[] = {
-    {GemmPlan::kLow, 64, 128, 3, {{0.368, 0.522, 0.685}, {0.576, 0.813, 0.954}}},
-    {GemmPlan::kThin, 48, 256, 2, {{0.443, 0.627, 0.0}, {0.639, 0.843, 0.0}}},
-    {GemmPlan::kFlat, 64, 256, 2, {{0.509, 0.748, 0.0}, {0.682, 0.940, 0.0}}},
-    {GemmPlan::kBroad, 96, 256, 2, {{0.669, 1.035, 0.0}, {0.841, 1.163, 0.0}}},
-    {GemmPlan::kWide, 128, 256, 2, {{0.804, 1.386, 0.0}, {0.981, 1.501, 0.0}}},
+    {GemmPlan::kLow, 64, 128, 3, {{0.372, 0.490, 0.691}, {0.591, 0.805, 0.959}}},
+    {GemmPlan::kThin, 48, 256, 2, {{0.445, 0.602, 0.0}, {0.663, 0.813, 0.0}}},
+    {GemmPlan::kFlat, 64, 256, 2, {{0.508, 0.721, 0.0}, {0.703, 0.905, 0.0}}},
+    {GemmPlan::kBroad, 96, 256, 2, {{0.650, 1.024, 0.0}, {0.863, 1.108, 0.0}}},
+    {GemmPlan::kWide, 128, 256, 2, {{0.756, 1.350, 0.0}, {0.993, 1.368, 0.0}}},
 };
 
 // Tiles of one kind: as many rounds of one whole tile a workgroup as there are, and the
@@ -926,21 +941,21 @@ double tile_us(GemmPlan& p, int64_t T, const TileKind& t, bool trans) {
   // a tile's rows that exist are written, on the mean of the tiles
   const double mb = static_cast<double>(rest) * t.bn * 4e-6 * static_cast<double>(T) / static_cast<double>(p.nRB);
   for (int s = 1; rest > 0 && s <= 16 && (s == 1 || p.S / s >= 4); ++s) {
-    double c = s > 1 ? 2.65 + 0.29 * s + 0.235 * mb * s : 0.0;
+    double c = s > 1 ? 2.53 + 0.29 * s + 0.25 * mb * s : 0.0;
     for (int64_t left = rest * s; left > 0; left -= slots)
       c += static_cast<double>(q4_ceil(p.S, s)) * us[q4_ceil(std::min(left, slots), kCUs) - 1];
     if (s == 1 || c < least) least = c, p.nSplit = s;
   }
   p.grid = std::min<int64_t>(slots, q4_ceil(p.whole + rest * p.nSplit, 8) * 8);
   p.bytes = p.nSplit > 1 ? static_cast<size_t>(rest) * p.nSplit * t.bm * t.bn * 4 : 0;
-  return 5.0 + static_cast<double>(rounds) * p.S * us[t.occ - 1] + least;
+  return 4.9 + static_cast<double>(rounds) * p.S * us[t.occ - 1] + least;
 }
 
 // The kernel, its tile and its ranges are those expected to be fastest.  The times are
 // fitted to 5600 calls (nine weights from 512 x 512 to 27648 x 5120, both directions, 1
 // to 8192 rows, every kind with 1 to 16 ranges, weights out of the caches); over them
 // the plan's call takes 1.1 % more than the fastest measured one on the mean with the
-// tiles (12 % at most) and 2.8 % forward, 1.2 % backward with the kernels for few rows
+// tiles (12 % at most) and 3.0 % forward, 1.2 % backward with the kernels for few rows
 // (21 % at most).
 GemmPlan gemm_plan(int64_t T, int64_t out, int64_t in, bool trans) {
   GemmPlan p;
@@ -984,8 +999,8 @@ template <int DT, class FW>
 void launch_few_as(const GemmArgs& g, const GemmPlan& p, hipStream_t stream) {
   hipLaunchKernelGGL((q4_few<DT, FW>), dim3(static_cast<unsigned>(p.grid)), dim3(64 * FW::NW), 0, stream, g);
   if (p.nSplit > 1) {
-    const int64_t entries = p.grid / p.nSplit * FW::ENTRIES;
-    hipLaunchKernelGGL((q4_few_join<DT, FW>), dim3(static_cast<unsigned>(q4_ceil(entries, 256))), dim3(256), 0, stream, g);
+    const dim3 grid(static_cast<unsigned>(q4_ceil(p.grid / p.nSplit * FW::ENTRIES, 256)));
+    hipLaunchKernelGGL((q4_few_join<DT, FW>), grid, dim3(256), 0, stream, g);
   }
 }
 template <int DT, int NT>

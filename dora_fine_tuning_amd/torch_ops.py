@@ -888,7 +888,8 @@ def _q4_where(device) -> tuple[Tensor, Tensor]:
     r, b = torch.arange(32, device=device)[:, None], torch.arange(2, device=device)[None, :]
     g, i = r // 8, r % 8
     at = 128 * i + 32 * g + 16 * (b ^ (i // 2 % 2))
-    return (at[:, :, None] + torch.arange(16, device=device)).flatten(), (32 * b + 8 * g + 2 * (i % 4) + i // 4).flatten()
+    exponents = 32 * b + 8 * g + 2 * (i % 4) + i // 4
+    return (at[:, :, None] + torch.arange(16, device=device)).flatten(), exponents.flatten()
 
 
 def _q4_values(q, e, rows, cols) -> Tensor:
