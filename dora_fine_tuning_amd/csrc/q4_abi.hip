@@ -43,7 +43,7 @@ int weight_ptrs(const char* fn, const void* q, const void* e) {
 
 size_t workspace(int64_t T, int64_t out, int64_t in, bool trans) {
   if (T <= 0 || out <= 0 || in <= 0 || T >= kMaxRows || out > kMaxCols || in > kMaxCols) return 0;
-  return dora::q4_gemm_workspace_bytes(T, out, in, trans);
+  return dora::q4_plan(T, out, in, trans).workspace();
 }
 
 int gemm_call(const char* fn, const void* x, const void* q, const void* e, int64_t T, int64_t out, int64_t in,
@@ -57,18 +57,19 @@ int gemm_call(const char* fn, const void* x, const void* q, const void* e, int64
     if (!x || !aligned16(x)) return fail(DORA_INVALID_ARG, "%s: the rows are NULL or not 16-byte aligned", fn);
     if (int st = weight_ptrs(fn, q, e)) return st;
   }
-  const size_t need = workspace(T, out, in, trans);
+  const dora::Q4Plan plan = dora::q4_plan(T, out, in, trans);
+  const size_t need = K > 0 ? plan.workspace() : 0;
   if (ws_bytes < need) return fail(DORA_INVALID_ARG, "%s: workspace of %zu bytes, %zu needed", fn, ws_bytes, need);
   if (need > 0 && (!ws || !aligned16(ws)))
     return fail(DORA_INVALID_ARG, "%s: workspace is NULL or not 16-byte aligned", fn);
   const Range outs[2] = {{y, mat16(T, N)}, {ws, need}};
   const Range ins[3] = {{x, mat16(T, K)}, {q, weight_q(out, in)}, {e, weight_e(out, in)}};
   if (outputs_overlap(outs, ins)) return fail(DORA_INVALID_ARG, "%s: an output overlaps another argument", fn);
-  if (dora::q4_gemm_max_grid(T, out, in, trans) > INT32_MAX)
+  if (plan.units() > INT32_MAX)
     return fail(DORA_UNSUPPORTED, "%s: T=%lld out=%lld in=%lld needs more workgroups than one launch holds", fn,
                 (long long)T, (long long)out, (long long)in);
   const dora::Q4GemmArgs a{x, q, e, T, out, in, dtype, trans, y, ws, stream};
-  return hip_status(dora::launch_q4_gemm(a), fn);
+  return hip_status(dora::launch_q4_gemm(a, plan), fn);
 }
 
 }  // namespace

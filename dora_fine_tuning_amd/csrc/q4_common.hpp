@@ -98,8 +98,19 @@ struct Q4GemmArgs {
   void* ws;
   hipStream_t stream;
 };
-size_t q4_gemm_workspace_bytes(int64_t T, int64_t out, int64_t in, bool trans);
-int64_t q4_gemm_max_grid(int64_t T, int64_t out, int64_t in, bool trans);
-hipError_t launch_q4_gemm(const Q4GemmArgs& a);
+// The kernel a call takes and how it shares out its work.
+struct Q4Plan {
+  enum Path { kLow, kThin, kFlat, kBroad, kWide, kFew } path = kWide;
+  int64_t N = 0, K = 0, xp = 0;  // output columns, contraction, elements of a row of x in the workspace or as given
+  int R = 1;                     // row tiles of a group of few rows
+  int S = 0, nSplit = 1;         // stages of 64; ranges of them
+  int64_t nRB = 0, nTiles = 0, whole = 0, grid = 0;
+  size_t pad = 0, bytes = 0;  // of padded rows; of a split's fp32 sums
+  size_t workspace() const { return pad + bytes; }
+  // units of work (tiles in up to 16 ranges) are numbered in 32 bits
+  int64_t units() const { return nRB * nTiles * 16 > grid ? nRB * nTiles * 16 : grid; }
+};
+Q4Plan q4_plan(int64_t T, int64_t out, int64_t in, bool trans);
+hipError_t launch_q4_gemm(const Q4GemmArgs& a, const Q4Plan& plan);
 
 }  // namespace dora

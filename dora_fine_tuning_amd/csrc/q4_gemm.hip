@@ -8,6 +8,7 @@
 // power of two, applied by the conversion), so the products are those of the
 // 16-bit matrix instruction: exact in fp32, added in fp32, rounded once.
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "dma_common.hpp"
@@ -871,21 +872,11 @@ using ThinTile = Q4Tile<1, 4, 3, 4, 4, 2, TRANS>;  // 48 x 256
 template <bool TRANS>
 using LowTile = Q4Tile<2, 2, 2, 4, 3, 3, TRANS>;  // 64 x 128
 
-struct GemmPlan {
-  enum Path { kLow, kThin, kFlat, kBroad, kWide, kFew } path = kWide;
-  int R = 1;  // row tiles of a group of few rows
-  int64_t N = 0, K = 0, xp = 0;
-  int S = 0, nSplit = 1;
-  int64_t nRB = 0, nTiles = 0, whole = 0;
-  int64_t grid = 0;
-  size_t pad = 0, bytes = 0;  // of padded rows; of a split's fp32 tiles
-};
-
 // Few rows: groups of R row tiles (forward) or 128 columns (backward), each in so many
 // ranges of the contraction.
-void few_plan(GemmPlan& p, int64_t T, int64_t out, int64_t in, bool trans, int R, int splits) {
+void few_plan(Q4Plan& p, int64_t T, int64_t out, int64_t in, bool trans, int R, int splits) {
   const int64_t groups = trans ? q4_ceil(in, 128) : q4_ceil(q4_ceil(out, kQ4Rows), R);
-  p.path = GemmPlan::kFew;
+  p.path = Q4Plan::kFew;
   p.R = R;
   p.nSplit = splits;
   p.grid = groups * splits;
@@ -893,11 +884,12 @@ void few_plan(GemmPlan& p, int64_t T, int64_t out, int64_t in, bool trans, int R
   p.bytes = splits > 1 ? static_cast<size_t>(p.grid * entries) * 16 : 0;
 }
 
-// Expected microseconds of few rows.  A workgroup's waves take `steps` steps each, a
-// step as long as its matrix tiles ask for, on every CU as many workgroups at once as
-// its registers allow; the weight's and the rows' bytes into the CUs come on top, and
-// for ranges the join's launch, its sums and the partial sums written and read.
-double few_us(const GemmPlan& p, int64_t T, int64_t out, int64_t in, bool trans) {
+// Expected microseconds of few rows: the weight's and the rows' bytes into the CUs, and
+// the steps that a workgroup's waves take one after the other (as long as its matrix
+// tiles and rows ask for, with as many workgroups on a CU as its registers allow), of
+// which the longer hides most of the other; for ranges also the join's launch, its sums
+// and the partial sums written and read.
+double few_us(const Q4Plan& p, int64_t T, int64_t out, int64_t in, bool trans) {
   const int64_t nt = q4_ceil(T, 16), groups = p.grid / p.nSplit;
   const double w_mb = static_cast<double>(out) * in * 17e-6 / 32, x_mb = 2e-6 * groups * T * p.K;
   const double part_mb = static_cast<double>(p.bytes) * 1e-6;
@@ -908,27 +900,29 @@ double few_us(const GemmPlan& p, int64_t T, int64_t out, int64_t in, bool trans)
   }
   const int64_t rnt = p.R * nt, steps = q4_ceil(q4_ceil(q4_ceil(in, 128), p.nSplit), rnt == 1 ? 16 : 8);
   const int64_t rounds = q4_ceil(p.grid, (rnt == 2 ? 2 : 1) * kCUs);
-  return 2.95 + 0.069 * (w_mb + 0.77 * x_mb) + rounds * steps * (0.788 + 0.237 * rnt) +
-         (p.nSplit > 1 ? 1.27 + 0.25 * p.nSplit + 0.58 * part_mb : 0.0);
+  const double load = 0.163 * w_mb + 0.074 * x_mb;
+  const double work = static_cast<double>(rounds * steps) * (0.570 + 0.229 * rnt + 0.315 * nt);
+  return 2.78 + std::cbrt(load * load * load + work * work * work) +
+         (p.nSplit > 1 ? 1.50 + 0.156 * p.nSplit + 0.687 * part_mb : 0.0);
 }
 
 struct TileKind {
-  GemmPlan::Path path;
+  Q4Plan::Path path;
   int64_t bm, bn, occ;
   double us[2][3];  // a stage forward and backward, with one to three workgroups on a CU
 };
 constexpr TileKind kTiles[] = {
-    {GemmPlan::kLow, 64, 128, 3, {{0.372, 0.490, 0.691}, {0.591, 0.805, 0.959}}},
-    {GemmPlan::kThin, 48, 256, 2, {{0.445, 0.602, 0.0}, {0.663, 0.813, 0.0}}},
-    {GemmPlan::kFlat, 64, 256, 2, {{0.508, 0.721, 0.0}, {0.703, 0.905, 0.0}}},
-    {GemmPlan::kBroad, 96, 256, 2, {{0.650, 1.024, 0.0}, {0.863, 1.108, 0.0}}},
-    {GemmPlan::kWide, 128, 256, 2, {{0.756, 1.350, 0.0}, {0.993, 1.368, 0.0}}},
+    {Q4Plan::kLow, 64, 128, 3, {{0.372, 0.490, 0.691}, {0.591, 0.805, 0.959}}},
+    {Q4Plan::kThin, 48, 256, 2, {{0.445, 0.602, 0.0}, {0.663, 0.813, 0.0}}},
+    {Q4Plan::kFlat, 64, 256, 2, {{0.508, 0.721, 0.0}, {0.703, 0.905, 0.0}}},
+    {Q4Plan::kBroad, 96, 256, 2, {{0.650, 1.024, 0.0}, {0.863, 1.108, 0.0}}},
+    {Q4Plan::kWide, 128, 256, 2, {{0.756, 1.350, 0.0}, {0.993, 1.368, 0.0}}},
 };
 
 // Tiles of one kind: as many rounds of one whole tile a workgroup as there are, and the
 // rest in up to 16 ranges of stages each (at least four stages), whichever number is
 // expected to be fastest.  Returns the expected microseconds.
-double tile_us(GemmPlan& p, int64_t T, const TileKind& t, bool trans) {
+double tile_us(Q4Plan& p, int64_t T, const TileKind& t, bool trans) {
   const double* us = t.us[trans ? 1 : 0];
   const int64_t slots = kCUs * t.occ;
   p.path = t.path;
@@ -951,43 +945,8 @@ double tile_us(GemmPlan& p, int64_t T, const TileKind& t, bool trans) {
   return 4.9 + static_cast<double>(rounds) * p.S * us[t.occ - 1] + least;
 }
 
-// The kernel, its tile and its ranges are those expected to be fastest.  The times are
-// fitted to 5600 calls (nine weights from 512 x 512 to 27648 x 5120, both directions, 1
-// to 8192 rows, every kind with 1 to 16 ranges, weights out of the caches); over them
-// the plan's call takes 1.1 % more than the fastest measured one on the mean with the
-// tiles (12 % at most) and 3.0 % forward, 1.2 % backward with the kernels for few rows
-// (21 % at most).
-GemmPlan gemm_plan(int64_t T, int64_t out, int64_t in, bool trans) {
-  GemmPlan p;
-  p.N = trans ? in : out;
-  p.K = trans ? out : in;
-  p.xp = q4_ceil(p.K, 8) * 8;
-  p.pad = p.xp != p.K ? (static_cast<size_t>(T) * p.xp * 2 + 255) / 256 * 256 : 0;
-  p.S = static_cast<int>(q4_ceil(p.K, kQ4Cols));
-  GemmPlan best;
-  double least = -1.0;
-  auto take = [&](const GemmPlan& q, double us) {
-    if (least < 0.0 || us < least) least = us, best = q;
-  };
-  if (T <= (trans ? 32 : 48)) {
-    for (int R = 1; R <= (trans ? 1 : 4); R *= 2)
-      for (int splits : {1, 2, 3, 4, 6, 8, 12, 16}) {
-        if (splits > 1 && p.S / splits < 8) break;
-        GemmPlan q = p;
-        few_plan(q, T, out, in, trans, R, splits);
-        take(q, few_us(q, T, out, in, trans));
-      }
-  }
-  for (const TileKind& t : kTiles) {
-    GemmPlan q = p;
-    const double us = tile_us(q, T, t, trans);
-    take(q, us);
-  }
-  return best;
-}
-
 template <int DT, class TL>
-void launch_tile(const GemmArgs& g, const GemmPlan& p, hipStream_t stream) {
+void launch_tile(const GemmArgs& g, const Q4Plan& p, hipStream_t stream) {
   hipLaunchKernelGGL((q4_gemm_tile<DT, TL>), dim3(static_cast<unsigned>(p.grid)), dim3(TL::NT), 0, stream, g);
   if (p.nSplit > 1) {
     const int64_t waves = (p.nRB * p.nTiles - p.whole) * TL::NW * TL::NM / (TL::TRANS ? TL::TNW : 2);
@@ -996,7 +955,7 @@ void launch_tile(const GemmArgs& g, const GemmPlan& p, hipStream_t stream) {
 }
 
 template <int DT, class FW>
-void launch_few_as(const GemmArgs& g, const GemmPlan& p, hipStream_t stream) {
+void launch_few_as(const GemmArgs& g, const Q4Plan& p, hipStream_t stream) {
   hipLaunchKernelGGL((q4_few<DT, FW>), dim3(static_cast<unsigned>(p.grid)), dim3(64 * FW::NW), 0, stream, g);
   if (p.nSplit > 1) {
     const dim3 grid(static_cast<unsigned>(q4_ceil(p.grid / p.nSplit * FW::ENTRIES, 256)));
@@ -1004,18 +963,18 @@ void launch_few_as(const GemmArgs& g, const GemmPlan& p, hipStream_t stream) {
   }
 }
 template <int DT, int NT>
-void launch_few_nt(const GemmArgs& g, const GemmPlan& p, hipStream_t stream) {
+void launch_few_nt(const GemmArgs& g, const Q4Plan& p, hipStream_t stream) {
   switch (p.R) {
     case 1:
       return launch_few_as<DT, FewFwd<NT, 1, NT == 1 ? 16 : 8, 2>>(g, p, stream);
     case 2:
       return launch_few_as<DT, FewFwd<NT, 2, 8, 2>>(g, p, stream);
     default:
-      return launch_few_as<DT, FewFwd<NT, 4, 8, NT <= 2 ? 2 : 1>>(g, p, stream);
+      if constexpr (NT <= 2) return launch_few_as<DT, FewFwd<NT, 4, 8, 2>>(g, p, stream);
   }
 }
 template <int DT, int NT>
-void launch_few_bwd(const GemmArgs& g, const GemmPlan& p, hipStream_t stream) {
+void launch_few_bwd(const GemmArgs& g, const Q4Plan& p, hipStream_t stream) {
   using FW = FewBwd<NT, 8>;
   hipLaunchKernelGGL((q4_few_bwd<DT, FW>), dim3(static_cast<unsigned>(p.grid)), dim3(64 * FW::NW), 0, stream, g);
   if (p.nSplit > 1)
@@ -1023,7 +982,7 @@ void launch_few_bwd(const GemmArgs& g, const GemmPlan& p, hipStream_t stream) {
                        stream, g);
 }
 template <int DT, bool TRANS>
-void launch_few(const GemmArgs& g, const GemmPlan& p, hipStream_t stream) {
+void launch_few(const GemmArgs& g, const Q4Plan& p, hipStream_t stream) {
   const int nt = static_cast<int>((g.T + 15) / 16);
   if constexpr (TRANS)
     return nt == 1 ? launch_few_bwd<DT, 1>(g, p, stream) : launch_few_bwd<DT, 2>(g, p, stream);
@@ -1034,36 +993,61 @@ void launch_few(const GemmArgs& g, const GemmPlan& p, hipStream_t stream) {
 }
 
 template <int DT, bool TRANS>
-void launch_typed(const GemmArgs& g, const GemmPlan& p, hipStream_t stream) {
+void launch_typed(const GemmArgs& g, const Q4Plan& p, hipStream_t stream) {
   switch (p.path) {
-    case GemmPlan::kFew:
+    case Q4Plan::kFew:
       return launch_few<DT, TRANS>(g, p, stream);
-    case GemmPlan::kLow:
+    case Q4Plan::kLow:
       return launch_tile<DT, LowTile<TRANS>>(g, p, stream);
-    case GemmPlan::kThin:
+    case Q4Plan::kThin:
       return launch_tile<DT, ThinTile<TRANS>>(g, p, stream);
-    case GemmPlan::kFlat:
+    case Q4Plan::kFlat:
       return launch_tile<DT, FlatTile<TRANS>>(g, p, stream);
-    case GemmPlan::kBroad:
+    case Q4Plan::kBroad:
       return launch_tile<DT, BroadTile<TRANS>>(g, p, stream);
-    case GemmPlan::kWide:
+    case Q4Plan::kWide:
       return launch_tile<DT, WideTile<TRANS>>(g, p, stream);
   }
 }
 
 }  // namespace
 
-size_t q4_gemm_workspace_bytes(int64_t T, int64_t out, int64_t in, bool trans) {
-  const GemmPlan p = gemm_plan(T, out, in, trans);
-  return p.pad + p.bytes;
-}
-int64_t q4_gemm_max_grid(int64_t T, int64_t out, int64_t in, bool trans) {
-  const GemmPlan p = gemm_plan(T, out, in, trans);
-  return std::max(p.grid, p.nRB * p.nTiles * 16);  // units of work (tiles in up to 16 ranges) are numbered in 32 bits
+// The kernel, its tile and its ranges are those expected to be fastest.  The times are
+// fitted to 5600 calls (nine weights from 512 x 512 to 27648 x 5120, both directions, 1
+// to 8192 rows, every kind with 1 to 16 ranges, weights out of the caches); over them
+// the plan's call takes 1.1 % more than the fastest measured one on the mean with the
+// tiles (12 % at most) and 3.0 % forward, 1.2 % backward with the kernels for few rows
+// (21 % at most).
+Q4Plan q4_plan(int64_t T, int64_t out, int64_t in, bool trans) {
+  Q4Plan p;
+  p.N = trans ? in : out;
+  p.K = trans ? out : in;
+  p.xp = q4_ceil(p.K, 8) * 8;
+  p.pad = p.xp != p.K ? (static_cast<size_t>(T) * p.xp * 2 + 255) / 256 * 256 : 0;
+  p.S = static_cast<int>(q4_ceil(p.K, kQ4Cols));
+  Q4Plan best;
+  double least = -1.0;
+  auto take = [&](const Q4Plan& q, double us) {
+    if (least < 0.0 || us < least) least = us, best = q;
+  };
+  if (T <= (trans ? 32 : 48)) {
+    for (int R = 1; R <= (trans ? 1 : T <= 32 ? 4 : 2); R *= 2)
+      for (int splits : {1, 2, 3, 4, 6, 8, 12, 16}) {
+        if (splits > 1 && p.S / splits < 8) break;
+        Q4Plan q = p;
+        few_plan(q, T, out, in, trans, R, splits);
+        take(q, few_us(q, T, out, in, trans));
+      }
+  }
+  for (const TileKind& t : kTiles) {
+    Q4Plan q = p;
+    const double us = tile_us(q, T, t, trans);
+    take(q, us);
+  }
+  return best;
 }
 
-hipError_t launch_q4_gemm(const Q4GemmArgs& p) {
-  const GemmPlan plan = gemm_plan(p.T, p.out, p.in, p.trans);
+hipError_t launch_q4_gemm(const Q4GemmArgs& p, const Q4Plan& plan) {
   if (plan.K == 0) {
     const int64_t n = p.T * plan.N;
     hipLaunchKernelGGL(q4_zero, dim3(static_cast<unsigned>(std::min<int64_t>(q4_ceil(n, 256), 4096))), dim3(256), 0,

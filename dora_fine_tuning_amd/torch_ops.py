@@ -1098,10 +1098,15 @@ q4_weight_norm.register_autograd(_q4_norm_grad, setup_context=_q8_norm_setup)
 # adapter_gather and adapter_combine go to the rows and back.
 
 
+def _whole_ids(ids, adapters):
+    if adapters < 0 or ids.dim() != 2 or ids.is_floating_point() or ids.is_complex():
+        raise ValueError(f"{adapters} adapters, ids {tuple(ids.shape)} in {ids.dtype}: expected whole numbers [T x k]")
+    return ids if ids.dtype in (torch.int64, torch.int32) else ids.to(torch.int64)
+
+
 @_q8_eager
 def _eager_adapter_sort(ids, adapters):
-    if adapters < 0 or ids.dim() != 2:
-        raise ValueError(f"{adapters} adapters, ids of {ids.dim()} dimensions: expected ids [T x k]")
+    ids = _whole_ids(ids, adapters)
     flat = ids.flatten().to(torch.int64)
     has = (flat >= 0) & (flat < adapters)
     key = torch.where(has, flat, torch.full_like(flat, adapters))
@@ -1227,9 +1232,7 @@ def adapter_sort(ids: Tensor, adapters: int) -> tuple[Tensor, Tensor, Tensor]:
     behind them all.  order holds the slot t * k + j of each row, place the row of
     each slot, both as complements for slots without an adapter; adapter a has rows
     bounds[a] to bounds[a + 1]."""
-    if ids.dtype not in (torch.int64, torch.int32):
-        ids = ids.to(torch.int64)
-    return binding.dora_adapter_sort(ids.contiguous(), adapters)
+    return binding.dora_adapter_sort(_whole_ids(ids, adapters).contiguous(), adapters)
 
 
 @torch.library.register_fake("dora_amd::adapter_sort")

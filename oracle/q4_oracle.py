@@ -14,8 +14,15 @@ from __future__ import annotations
 
 import numpy as np
 
-E2M1 = np.array([(-1.0) ** (c >> 3) * (0.5 * (c & 1) if (c >> 1) & 3 == 0 else (1 + 0.5 * (c & 1)) * 2.0 ** (((c >> 1) & 3) - 1))
-                 for c in range(16)])
+
+
+def _value(c: int) -> float:
+    """The value of a code, from the format's definition."""
+    sign, ex, half = -1.0 if c & 8 else 1.0, (c >> 1) & 3, 0.5 * (c & 1)
+    return sign * (half if ex == 0 else (1 + half) * 2.0 ** (ex - 1))
+
+
+E2M1 = np.array([_value(c) for c in range(16)])
 NAN_BYTE = 255
 
 

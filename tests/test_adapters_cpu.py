@@ -48,10 +48,14 @@ def test_eager_sort_types_and_no_adapters():
     check_sort("cpu", ids, 9, torch.int32)
     check_sort("cpu", ids, 9, torch.int16)
     check_sort("cpu", ids, 0)
-    with pytest.raises(ValueError):
-        F.adapter_sort(ids, -1)
-    with pytest.raises(ValueError):
-        F.adapter_sort(ids[0], 3)
+    check_sort_refusals("cpu")
+
+
+def check_sort_refusals(device):
+    ids = make_ids("some", 20, 2, 9).to(device)
+    for bad in ((ids, -1), (ids[0], 3), (ids.float(), 3), (ids[None], 3)):
+        with pytest.raises(ValueError, match="whole numbers"):
+            F.adapter_sort(*bad)
 
 
 def data(T, k, D, dtype, device, seed=0, weights=True, base=True):
@@ -141,7 +145,8 @@ def check_foreign_places(device, dtype):
     rows = torch.ones((6, 16), device=device, dtype=dtype)
     y = F.adapter_combine(rows, None, place, None)
     assert y[:, 0].tolist() == [1.0, 0.0, 1.0]
-    d_rows, d_w = F.adapter_combine_backward(torch.ones((3, 16), device=device, dtype=dtype), rows, None, place, True, True)
+    dy = torch.ones((3, 16), device=device, dtype=dtype)
+    d_rows, d_w = F.adapter_combine_backward(dy, rows, None, place, True, True)
     assert d_w.tolist() == [[16.0, 0.0], [0.0, 0.0], [0.0, 16.0]] and d_rows[:2].float().min() == 1
     assert F.adapter_gather(torch.ones((3, 16), device=device, dtype=dtype), place)[:2].float().min() == 1
 
@@ -263,7 +268,8 @@ def check_traced_outputs(device, dtype):
     place = F.adapter_sort(ids, 4)[1]
     d = data(9, 2, 24, dtype, device)
     calls = [(F.adapter_sort, (ids, 4)), (F.adapter_gather, (d["x"], place)),
-             (F.adapter_combine, (d["rows"], d["w"], place, d["base"])), (F.adapter_combine, (d["rows"], None, place, None)),
+             (F.adapter_combine, (d["rows"], d["w"], place, d["base"])),
+             (F.adapter_combine, (d["rows"], None, place, None)),
              (F.adapter_combine_backward, (d["dy"], d["rows"], d["w"], place, True, True)),
              (F.adapter_combine_backward, (d["dy"], d["rows"], d["w"], place, False, True)),
              (F.adapter_combine_backward, (d["dy"], d["rows"], None, place, True, False))]
@@ -292,7 +298,8 @@ def check_wrong_arguments(device, dtype):
     m = lambda *s, t=dtype: torch.zeros(s, device=device, dtype=t)
     bad = [lambda: F.adapter_gather(m(5, 8), place), lambda: F.adapter_gather(m(4, 8), place.long()),
            lambda: F.adapter_gather(m(4, 8), place.reshape(-1)),
-           lambda: F.adapter_combine(m(7, 8), None, place, None), lambda: F.adapter_combine(m(8, 8), m(4, 1), place, None),
+           lambda: F.adapter_combine(m(7, 8), None, place, None),
+           lambda: F.adapter_combine(m(8, 8), m(4, 1), place, None),
            lambda: F.adapter_combine(m(8, 8), None, place, m(4, 9)),
            lambda: F.adapter_combine(m(8, 8), None, place, m(4, 8, t=torch.float64)),
            lambda: F.adapter_combine(m(8, 8), None, place.reshape(-1), None),
@@ -376,7 +383,8 @@ def test_rows_refusals():
 def test_binding_refuses_host_tensors():
     ids = torch.zeros((4, 2), dtype=torch.int64)
     place = F.adapter_sort(ids, 1)[1]
-    for f in (lambda: binding.dora_adapter_sort(ids, 1), lambda: binding.dora_adapter_gather(torch.zeros(4, 8).half(), place),
+    for f in (lambda: binding.dora_adapter_sort(ids, 1),
+              lambda: binding.dora_adapter_gather(torch.zeros(4, 8).half(), place),
               lambda: binding.dora_adapter_combine(torch.zeros(8, 8).half(), None, place)):
         with pytest.raises(ValueError, match="HIP device"):
             f()

@@ -5,7 +5,7 @@ import torch
 
 from oracle import q4_oracle as Q
 from test_adapters_cpu import (SHAPES, check_by_differences, check_foreign_places, check_layer, check_layer_edges,
-                               check_rows, check_sort, check_traced_outputs, check_unused_values, check_wrong_arguments,
+                               check_rows, check_sort, check_sort_refusals, check_traced_outputs, check_unused_values, check_wrong_arguments,
                                make_ids)
 
 pytestmark = pytest.mark.gpu
@@ -20,8 +20,8 @@ def F():
 
 
 @pytest.mark.parametrize("kind", ["some", "skewed", "none", "one", "wild"])
-@pytest.mark.parametrize("T,k,n", [(1, 1, 1), (7, 1, 3), (63, 1, 2), (64, 1, 64), (65, 3, 5), (1024, 1, 8), (1000, 4, 1000),
-                                   (4096, 1, 7), (4097, 1, 7), (2049, 2, 255), (5000, 3, 256), (0, 2, 5), (5, 0, 5)])
+@pytest.mark.parametrize("T,k,n", [(1, 1, 1), (7, 1, 3), (63, 1, 2), (64, 1, 64), (65, 3, 5), (1024, 1, 8),
+                                   (1025, 1, 9), (1000, 4, 1000), (4096, 1, 7), (4097, 1, 7), (2049, 2, 255), (5000, 3, 256), (0, 2, 5), (5, 0, 5)])
 def test_sort(kind, T, k, n):
     for dt in (torch.int64, torch.int32):
         check_sort(DEV, make_ids(kind, T, k, n), n, dt)
@@ -46,11 +46,13 @@ def test_more_adapters_than_the_kernel_takes(F):
     check_sort(DEV, make_ids("some", 300, 2, 1500), 1500)
     check_sort(DEV, make_ids("some", 30, 2, 9), 0)
     check_sort(DEV, make_ids("some", 30, 2, 9), 9, torch.int16)
+    check_sort_refusals(DEV)
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
 @pytest.mark.parametrize("kind", ["some", "none"])
-@pytest.mark.parametrize("T,k,n,D", SHAPES + [(33, 2, 4, 40), (20, 4, 3, 1000), (5, 2, 2, 2056), (6, 1, 2, 8192), (3, 3, 2, 10001),
+@pytest.mark.parametrize("T,k,n,D", SHAPES + [(33, 2, 4, 40), (20, 4, 3, 1000), (5, 2, 2, 2056), (6, 1, 2, 8192),
+                                              (3, 3, 2, 10001),
                                               (130, 2, 16, 129), (2, 9, 5, 27648)])
 def test_rows(T, k, n, D, dtype, kind):
     for weights, base in ((True, True), (False, False), (True, False), (False, True)):
@@ -110,7 +112,9 @@ def test_combine_in_place_of_its_base(F):
     for D in (40, 33):
         rows, base = torch.randn((100, D), device=DEV).half(), torch.randn((50, D), device=DEV).half()
         want = F.adapter_combine(rows, None, place, base)
-        assert LIB.dora_adapter_combine(_ptr(rows), None, _ptr(place), _ptr(base), 50, 2, D, 1, _ptr(base), _raw_stream(DEV)) == 0
+        st = LIB.dora_adapter_combine(_ptr(rows), None, _ptr(place), _ptr(base), 50, 2, D, 1, _ptr(base),
+                                      _raw_stream(DEV))
+        assert st == 0
         assert torch.equal(base, want)
 
 

@@ -112,11 +112,12 @@ def test_eager_products(T, out, in_, dtype):
                      (rnd(3, (T, out), dtype), held, lambda v: F.q4_linear_backward(v, q, e, in_))):
         want, mass, y = O.as_f64(x) @ M, np.abs(O.as_f64(x)) @ np.abs(M), op(x)
         assert y.dtype == dtype and tuple(y.shape) == want.shape
-        assert np.all(np.abs(y.double().numpy() - want) <= half * np.abs(want) + M.shape[0] * 2.0**-23 * mass + 2.0**-25)
+        tol = half * np.abs(want) + M.shape[0] * 2.0**-23 * mass + 2.0**-25
+        assert np.all(np.abs(y.double().numpy() - want) <= tol)
 
 
 def test_gradients_are_the_formulas_and_the_differences():
-    """y is linear in x: its gradient is W^T dy, equal to exact differences of the loss; a second one is zero's product back."""
+    """y is linear in x: its gradient is dy W, equal to the differences of the loss; and so is the gradient's own."""
     W = rnd(5, (24, 40), torch.float32, 0.1)
     q, e = F.q4_pack_weight(W)
     held = torch.from_numpy(Q.held(O.as_f64(W)))
@@ -301,9 +302,11 @@ def _status(status, want, text):
 @pytest.mark.parametrize("name", ["pack", "unpack"])
 def test_pack_refusals(name):
     if name == "pack":
-        fn = lambda W=FAR[0], out=64, in_=128, dt=0, q=FAR[1], e=FAR[2]: LIB.dora_q4_pack_weight(W, out, in_, dt, q, e, None)
+        def fn(W=FAR[0], out=64, in_=128, dt=0, q=FAR[1], e=FAR[2]):
+            return LIB.dora_q4_pack_weight(W, out, in_, dt, q, e, None)
     else:
-        fn = lambda W=FAR[0], out=64, in_=128, dt=0, q=FAR[1], e=FAR[2]: LIB.dora_q4_unpack_weight(q, e, out, in_, dt, W, None)
+        def fn(W=FAR[0], out=64, in_=128, dt=0, q=FAR[1], e=FAR[2]):
+            return LIB.dora_q4_unpack_weight(q, e, out, in_, dt, W, None)
     _status(fn(dt=2), UNSUPPORTED, "dtype")
     _status(fn(out=-1), INVALID, "negative")
     _status(fn(in_=1 << 22), UNSUPPORTED, "beyond")

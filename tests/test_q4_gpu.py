@@ -101,7 +101,8 @@ def test_eager_tier_packs_the_same_bytes(F):
 
 
 TOKENS = [1, 2, 7, 15, 16, 17, 31, 33, 48, 63, 64, 65, 100, 128, 129, 200, 257, 300, 513, 1000]
-WEIGHTS = [(1, 1), (5, 7), (40, 72), (33, 100), (65, 129), (152, 200), (264, 1000), (1030, 520), (512, 4096), (300, 8192)]
+WEIGHTS = [(1, 1), (5, 7), (40, 72), (33, 100), (65, 129), (152, 200), (264, 1000), (1030, 520), (512, 4096),
+           (300, 8192)]
 
 
 @pytest.mark.parametrize("out,in_", WEIGHTS)
@@ -138,7 +139,7 @@ def test_batches(b, T, out, in_, dtype):
 @pytest.mark.parametrize("T", [1, 20, 300])
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 def test_whole_range_of_scales(b, T, dtype):
-    """Weights from fp16's smallest subnormal to 6 * 2^13 in neighbouring blocks: the operands are exact in both types."""
+    """Weights from fp16's smallest subnormal to 6 * 2^13 in neighbouring blocks: operands exact in both types."""
     out, in_ = 96, 320
     rng = np.random.default_rng(4)
     W = rng.standard_normal((out, in_)) * np.repeat(np.exp2(rng.integers(-26, 14, (out, in_ // 32))), 32, axis=1)
@@ -155,7 +156,7 @@ def test_whole_range_of_scales(b, T, dtype):
 
 @pytest.mark.parametrize("T", [1, 5, 40, 300])
 def test_not_finite(b, T):
-    """A NaN or infinity in a row stays in that row's result, a NaN block in its column (forward) or its 32 (backward)."""
+    """A NaN or infinity in a row stays in that row's result, a NaN block in its column (its 32 backward)."""
     out, in_ = 72, 136
     W = rnd(1, (out, in_), torch.bfloat16, 0.02)
     q, e = b.dora_q4_pack_weight(W.to(DEV))
@@ -211,8 +212,8 @@ def test_outputs_write_nothing_else(b):
             for off in (8, 9):
                 buf = torch.full((T * N + 32,), 7.0, dtype=torch.bfloat16, device=DEV)
                 y = buf[off : off + T * N]
-                st = getattr(LIB, f"dora_q4_linear_{name}")(_ptr(x), _ptr(q), _ptr(e), T, out, in_, 0, _ptr(y), _ptr(ws),
-                                                            need, _raw_stream(DEV))
+                fn = getattr(LIB, f"dora_q4_linear_{name}")
+                st = fn(_ptr(x), _ptr(q), _ptr(e), T, out, in_, 0, _ptr(y), _ptr(ws), need, _raw_stream(DEV))
                 assert st == 0, b.dora_last_error()
                 assert torch.equal(y.view(T, N), want), (name, T, out, in_, off)
                 assert bool((buf[:off] == 7).all()) and bool((buf[off + T * N :] == 7).all())
@@ -261,8 +262,8 @@ def test_strides_slices_and_streams(F, b):
     q, e, _ = weight(b, out, in_, torch.bfloat16)
     W = values(b, q, e, out, in_)
     wide = torch.randn((30, 2 * in_ + 1), device=DEV).bfloat16()
-    for x in (wide[:, 1 : 1 + in_], wide.t()[:in_, :].t(), wide[::3, :in_], wide.reshape(-1)[1 : 1 + 20 * in_].view(20, in_),
-              wide[:1, :in_].expand(6, in_)):
+    for x in (wide[:, 1 : 1 + in_], wide.t()[:in_, :].t(), wide[::3, :in_],
+              wide.reshape(-1)[1 : 1 + 20 * in_].view(20, in_), wide[:1, :in_].expand(6, in_)):
         assert_product(F.q4_linear(x, q, e, out), x, W.t())
     s = torch.cuda.Stream()
     x = wide[:, :in_].contiguous()
