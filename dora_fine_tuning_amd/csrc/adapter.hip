@@ -189,7 +189,7 @@ int64_t sort_chunks(int64_t N) { return std::max<int64_t>(1, q4_ceil(N, int64_t(
 //
 // A token's row is shared by `span` threads (a power of two up to 256), each
 // taking chunks of 8 elements, kU of them at a time.
-constexpr int kRowThreads = 256, kU = 4;
+constexpr int kRowThreads = kAdapterRowThreads, kU = 4;
 
 struct RowsArgs {
   const void *x, *rows, *base;

@@ -26,6 +26,9 @@ int check_rows(const char* fn, int64_t T, int64_t k, int64_t D, int dtype) {
   if (int st = check_slots(fn, T, k)) return st;
   if (D < 0) return fail(DORA_INVALID_ARG, "%s: negative size %lld", fn, (long long)D);
   if (D > kMaxCols) return fail(DORA_UNSUPPORTED, "%s: D=%lld beyond 2^22", fn, (long long)D);
+  if (dora::adapter_rows_grid(T, D) * dora::kAdapterRowThreads > UINT32_MAX)
+    return fail(DORA_UNSUPPORTED, "%s: T=%lld D=%lld needs more threads than one launch holds (2^32 - 1)", fn,
+                (long long)T, (long long)D);
   return DORA_OK;
 }
 

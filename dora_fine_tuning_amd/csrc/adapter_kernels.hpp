@@ -35,7 +35,8 @@ struct AdapterRowsArgs {
   float* d_weights;
   hipStream_t stream;
 };
-int64_t adapter_rows_grid(int64_t T, int64_t D);
+constexpr int kAdapterRowThreads = 256;
+int64_t adapter_rows_grid(int64_t T, int64_t D);  // workgroups
 hipError_t launch_adapter_gather(const AdapterRowsArgs& a);       // x, place -> y [T k x D]
 hipError_t launch_adapter_combine(const AdapterRowsArgs& a);      // rows, weights, place, base -> y [T x D]
 hipError_t launch_adapter_combine_bwd(const AdapterRowsArgs& a);  // x = dy, rows, weights, place -> d_rows, d_weights

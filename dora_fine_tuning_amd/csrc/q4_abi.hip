@@ -27,6 +27,15 @@ int check_sizes(const char* fn, int dtype, int64_t T, int64_t out, int64_t in) {
   return DORA_OK;
 }
 
+// Packing and unpacking: a launch holds fewer than 2^32 threads.
+int check_pack(const char* fn, int dtype, int64_t out, int64_t in) {
+  if (int st = check_sizes(fn, dtype, 0, out, in)) return st;
+  if (dora::q4_pack_grid(out, in) * 256 > UINT32_MAX)
+    return fail(DORA_UNSUPPORTED, "%s: a weight of %lld x %lld needs more threads than one launch holds", fn,
+                (long long)out, (long long)in);
+  return DORA_OK;
+}
+
 size_t mat16(int64_t rows, int64_t cols) { return static_cast<size_t>(rows) * cols * 2; }
 size_t tiles(int64_t out, int64_t in) {
   return static_cast<size_t>(dora::q4_ceil(out, dora::kQ4Rows)) * dora::q4_ceil(in, dora::kQ4Cols);
@@ -41,9 +50,27 @@ int weight_ptrs(const char* fn, const void* q, const void* e) {
   return DORA_OK;
 }
 
+// The plan of a call, which depends on its sizes alone.  Weighing the kernels takes
+// 1.6 us, twice a call (workspace, product), next to 5 us of a single token's kernel:
+// each thread keeps the plans of the sizes it met last.
+const dora::Q4Plan& plan_of(int64_t T, int64_t out, int64_t in, bool trans) {
+  struct Entry {
+    int64_t T = 0, out = 0, in = 0;
+    bool trans = false;
+    dora::Q4Plan plan;
+  };
+  static thread_local Entry table[64];
+  const uint64_t mix = (static_cast<uint64_t>(T) * 0x9e3779b97f4a7c15u ^ static_cast<uint64_t>(out)) * 0x9e3779b97f4a7c15u ^
+                       static_cast<uint64_t>(in) * 2 ^ (trans ? 1u : 0u);
+  Entry& e = table[mix * 0x9e3779b97f4a7c15u >> 58];
+  if (e.T != T || e.out != out || e.in != in || e.trans != trans)  // (T >= 1)
+    e = Entry{T, out, in, trans, dora::q4_plan(T, out, in, trans)};
+  return e.plan;
+}
+
 size_t workspace(int64_t T, int64_t out, int64_t in, bool trans) {
   if (T <= 0 || out <= 0 || in <= 0 || T >= kMaxRows || out > kMaxCols || in > kMaxCols) return 0;
-  return dora::q4_plan(T, out, in, trans).workspace();
+  return plan_of(T, out, in, trans).workspace();
 }
 
 int gemm_call(const char* fn, const void* x, const void* q, const void* e, int64_t T, int64_t out, int64_t in,
@@ -57,7 +84,7 @@ int gemm_call(const char* fn, const void* x, const void* q, const void* e, int64
     if (!x || !aligned16(x)) return fail(DORA_INVALID_ARG, "%s: the rows are NULL or not 16-byte aligned", fn);
     if (int st = weight_ptrs(fn, q, e)) return st;
   }
-  const dora::Q4Plan plan = dora::q4_plan(T, out, in, trans);
+  const dora::Q4Plan& plan = plan_of(T, out, in, trans);
   const size_t need = K > 0 ? plan.workspace() : 0;
   if (ws_bytes < need) return fail(DORA_INVALID_ARG, "%s: workspace of %zu bytes, %zu needed", fn, ws_bytes, need);
   if (need > 0 && (!ws || !aligned16(ws)))
@@ -78,7 +105,7 @@ extern "C" {
 
 int dora_q4_pack_weight(const void* W, int64_t out, int64_t in, int dtype, void* q, void* e, hipStream_t stream) {
   const char* fn = "dora_q4_pack_weight";
-  if (int st = check_sizes(fn, dtype, 0, out, in)) return st;
+  if (int st = check_pack(fn, dtype, out, in)) return st;
   if (out == 0 || in == 0) return ok();
   if (!W || !aligned(W, 2)) return fail(DORA_INVALID_ARG, "%s: the weight is NULL or not 2-byte aligned", fn);
   if (int st = weight_ptrs(fn, q, e)) return st;
@@ -91,7 +118,7 @@ int dora_q4_pack_weight(const void* W, int64_t out, int64_t in, int dtype, void*
 int dora_q4_unpack_weight(const void* q, const void* e, int64_t rows, int64_t cols, int dtype, void* W,
                           hipStream_t stream) {
   const char* fn = "dora_q4_unpack_weight";
-  if (int st = check_sizes(fn, dtype, 0, rows, cols)) return st;
+  if (int st = check_pack(fn, dtype, rows, cols)) return st;
   if (rows == 0 || cols == 0) return ok();
   if (!W || !aligned(W, 2)) return fail(DORA_INVALID_ARG, "%s: the output is NULL or not 2-byte aligned", fn);
   if (int st = weight_ptrs(fn, q, e)) return st;

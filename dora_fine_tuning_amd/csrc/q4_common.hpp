@@ -82,6 +82,7 @@ __device__ inline Chunk q4_decode8(uint32_t w, float scale) {
 
 // ---- host-side launch interface
 
+int64_t q4_pack_grid(int64_t out, int64_t in);  // workgroups of 256, of either
 hipError_t launch_q4_pack(const void* W, int64_t out, int64_t in, int dtype, bool vec, void* q, void* e,
                           hipStream_t stream);
 hipError_t launch_q4_unpack(const void* q, const void* e, int64_t rows, int64_t cols, int dtype, bool vec, void* x,

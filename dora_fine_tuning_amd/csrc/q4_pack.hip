@@ -94,10 +94,14 @@ __global__ __launch_bounds__(256) void q4_unpack_k(const uint8_t* q, const uint8
 
 }  // namespace
 
+int64_t q4_pack_grid(int64_t out, int64_t in) {
+  return q4_ceil(out, kQ4Rows) * q4_ceil(q4_ceil(in, kQ4Cols), kU);
+}
+
 hipError_t launch_q4_pack(const void* W, int64_t out, int64_t in, int dtype, bool vec, void* q, void* e,
                           hipStream_t stream) {
   const uint32_t ib = static_cast<uint32_t>(q4_ceil(in, kQ4Cols)), groups = (ib + kU - 1) / kU;
-  const dim3 grid(static_cast<uint32_t>(q4_ceil(out, kQ4Rows)) * groups);
+  const dim3 grid(static_cast<uint32_t>(q4_pack_grid(out, in)));
   auto go = [&](auto k) {
     hipLaunchKernelGGL(k, grid, dim3(256), 0, stream, W, out, in, ib, groups, static_cast<uint8_t*>(q),
                        static_cast<uint8_t*>(e));
@@ -112,7 +116,7 @@ hipError_t launch_q4_pack(const void* W, int64_t out, int64_t in, int dtype, boo
 hipError_t launch_q4_unpack(const void* q, const void* e, int64_t rows, int64_t cols, int dtype, bool vec, void* x,
                             hipStream_t stream) {
   const uint32_t ib = static_cast<uint32_t>(q4_ceil(cols, kQ4Cols)), groups = (ib + kU - 1) / kU;
-  const dim3 grid(static_cast<uint32_t>(q4_ceil(rows, kQ4Rows)) * groups);
+  const dim3 grid(static_cast<uint32_t>(q4_pack_grid(rows, cols)));
   auto go = [&](auto k) {
     hipLaunchKernelGGL(k, grid, dim3(256), 0, stream, static_cast<const uint8_t*>(q), static_cast<const uint8_t*>(e),
                        rows, cols, ib, groups, x);

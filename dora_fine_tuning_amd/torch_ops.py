@@ -33,12 +33,21 @@ This module registers:
   ``_packed``: the compose's backward from the base kept in 8 bits) and
   ``q8_grad_a`` (the gradient of A from x kept in 8 bits).  ``q8_layer`` runs
   them together under autograd.
+* the 4-bit weight: ``q4_pack_weight`` / ``q4_unpack_weight`` (e2m1 blocks of 32
+  with a power-of-two scale each), ``q4_linear`` (x W0^T from 16-bit x) and
+  ``q4_linear_backward`` (g W0), each the other's autograd formula, and
+  ``q4_weight_norm``, the norm of a W0 held so.
+* tokens sorted by adapter: ``adapter_sort`` (a batch's slots by adapter),
+  ``adapter_gather`` (tokens' rows in that order) and ``adapter_combine`` (rows
+  added up per token, with weights; ``adapter_combine_backward`` is its formula).
 * ``DoRALinear`` -- a linear layer with frozen W0 and trainable A, B and m:
   y = x W0^T + compose(x W0^T, x A^T B^T, m, n, s), with n = ||W0 + s*B*A||
   detached by default.  With ``detach_norm=False`` the gradient also flows
   through n: the compose's formula gives dL/dn = -(m / n) * d_mag (L depends on
   n only through g = m / n; this [out]-sized product is the one step of the
   chain done by torch), and the norm's formula turns it into d_A and d_B.
+  ``q8_weight`` and ``q4_weight`` hold W0 in 8 or 4 bits.
+* ``DoRAAdapters`` -- several adapters over one W0, each token with its own.
 
 Tiers (paragraph on the dispatch tiers): autograd records the compose only
 when a gradient is needed (training: the fused forward, then the fused
@@ -523,11 +532,12 @@ def _eager_q8_grad_a(dh, xq, xe, in_features):
 
 
 # These operators are registered without the wrapper of a custom operator: they
-# have no autograd formula of their own (``q8_layer`` has) and run in serving
-# loops, where its layers cost as much as a launch.  Arguments that require a
-# gradient, or carry a tangent, are refused: none would come back through them.
-# The refusal is the operators' Autograd kernel, which tracing and functorch run
-# as well as an eager call.
+# run in serving loops, where its layers cost as much as a launch.  Those without
+# an autograd formula of their own (the 8-bit ones, for which ``q8_layer`` has it)
+# refuse arguments that require a gradient: none would come back through them.
+# None takes arguments that carry a tangent.  Gradients and refusals are the
+# operators' Autograd kernel, which tracing and functorch run as well as an eager
+# call.
 _Q8_LIB = torch.library.Library("dora_amd", "FRAGMENT")
 _BELOW_AUTOGRAD = torch._C._after_autograd_keyset
 
@@ -1464,9 +1474,11 @@ class DoRAAdapters(torch.nn.Module):
 
     def weight_norm(self, adapter: int) -> Tensor:
         """n_a = ||W0 + s*B_a*A_a|| per output row."""
-        if self.weight_sqnorm is None or self.weight_sqnorm.device != self.lora_A.device:
+        return self._norm_of(self.lora_A[adapter], self.lora_B[adapter])
+
+    def _norm_of(self, A: Tensor, B: Tensor) -> Tensor:
+        if self.weight_sqnorm is None or self.weight_sqnorm.device != A.device:
             self.refresh_weight_cache()
-        A, B = self.lora_A[adapter], self.lora_B[adapter]
         if self.detach_norm:
             A, B = A.detach(), B.detach()
         if self.q4_weight:
@@ -1488,17 +1500,18 @@ class DoRAAdapters(torch.nn.Module):
         else:
             base = F.linear(x2, self.weight)
         order, place, bounds = adapter_sort(ids.reshape(T, k), self.adapters)
-        xs, bs = adapter_gather(x2, place), adapter_gather(base, place)
         ends = bounds.tolist()
+        sizes = [b - a for a, b in zip(ends, ends[1:] + [T * k])]  # the rows of slots without an adapter last
+        # taken apart once: the gradient of each slice by itself would be the whole's, in zeros
+        xs, bs = adapter_gather(x2, place).split(sizes), adapter_gather(base, place).split(sizes)
         parts = []
-        for a in range(self.adapters):
-            rows = slice(ends[a], ends[a + 1])
-            if rows.start < rows.stop:
-                h = F.linear(xs[rows], self.lora_A[a])
-                (B,) = _autocast(self.lora_B[a])
-                parts.append(lora_compose(bs[rows], h, B, self.magnitude[a], self.weight_norm(a), self.s, False))
-        if ends[-1] < T * k:  # the rows of slots without an adapter: not used
-            parts.append(base.new_zeros((T * k - ends[-1], self.out_features)))
+        for xa, ba, A, B, m in zip(xs, bs, self.lora_A.unbind(), self.lora_B.unbind(), self.magnitude.unbind()):
+            if xa.shape[0] > 0:
+                h, n = F.linear(xa, A), self._norm_of(A, B)
+                (B,) = _autocast(B)
+                parts.append(lora_compose(ba, h, B, m, n, self.s, False))
+        if sizes[-1] > 0:  # not used
+            parts.append(base.new_zeros((sizes[-1], self.out_features)))
         rows = torch.cat(parts) if parts else base.new_zeros((0, self.out_features))
         y = adapter_combine(rows, None if weights is None else weights.reshape(T, k), place, base)
         return y.reshape(*lead, self.out_features)

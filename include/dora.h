@@ -116,7 +116,9 @@ extern "C" {
  *  - in the 8-bit and 4-bit operators (dora_q8_*, dora_q4_*), 2^31 rows or more,
  *    more than 2^22 - 128 columns, or a rank above 2^20;
  *  - in the operators on sorted tokens (dora_adapter_*), more than 2^31 - 1 slots,
- *    1000 adapters or 2^22 columns, or ids of neither 4 nor 8 bytes.
+ *    1000 adapters or 2^22 columns, or ids of neither 4 nor 8 bytes;
+ *  - in both, matrices of so many elements (2^36 and more) that a launch would need
+ *    2^32 threads.
  */
 enum dora_status {
   DORA_OK = 0,

@@ -380,6 +380,28 @@ def test_rows_refusals():
     assert gather(D=0, x=None) == OK and gather(k=0, x=None) == OK
 
 
+def test_rows_refuse_more_threads_than_a_launch_holds():
+    """2^31 - 8 tokens of 128 elements take four threads each; of 32, one, and they go on to the next check."""
+    T = (1 << 31) - 8
+    _status(LIB.dora_adapter_gather(FAR[0], FAR[1], T, 1, 128, 0, FAR[2], None), UNSUPPORTED, "threads")
+    _status(LIB.dora_adapter_combine(FAR[0], None, FAR[2], None, T, 1, 128, 0, FAR[4], None), UNSUPPORTED, "threads")
+    _status(LIB.dora_adapter_combine_bwd(FAR[0], FAR[1], None, FAR[3], T, 1, 128, 0, FAR[4], None, None), UNSUPPORTED,
+            "threads")
+    _status(LIB.dora_adapter_gather(FAR[0], FAR[1], T, 1, 32, 0, None, None), INVALID, "NULL")
+
+
+def test_layer_gradients_of_adapters_that_no_token_uses():
+    """Zeros, and those of the others as if they were alone."""
+    torch.manual_seed(3)
+    layer = F.DoRAAdapters(24, 40, 4, 5, dtype=torch.float32)
+    with torch.no_grad():
+        layer.lora_B.normal_()
+    x, ids = torch.randn(6, 24), torch.tensor([1, 3, 3, -1, 1, 7])
+    layer(x, ids).square().sum().backward()
+    for p in (layer.lora_A, layer.lora_B, layer.magnitude):
+        assert [bool(g.any()) for g in p.grad] == [False, True, False, True, False]
+
+
 def test_binding_refuses_host_tensors():
     ids = torch.zeros((4, 2), dtype=torch.int64)
     place = F.adapter_sort(ids, 1)[1]

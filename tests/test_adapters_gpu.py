@@ -5,8 +5,8 @@ import torch
 
 from oracle import q4_oracle as Q
 from test_adapters_cpu import (SHAPES, check_by_differences, check_foreign_places, check_layer, check_layer_edges,
-                               check_rows, check_sort, check_sort_refusals, check_traced_outputs, check_unused_values, check_wrong_arguments,
-                               make_ids)
+                               check_rows, check_sort, check_sort_refusals, check_traced_outputs, check_unused_values,
+                               check_wrong_arguments, make_ids)
 
 pytestmark = pytest.mark.gpu
 DEV = torch.device("cuda:0")
@@ -21,7 +21,8 @@ def F():
 
 @pytest.mark.parametrize("kind", ["some", "skewed", "none", "one", "wild"])
 @pytest.mark.parametrize("T,k,n", [(1, 1, 1), (7, 1, 3), (63, 1, 2), (64, 1, 64), (65, 3, 5), (1024, 1, 8),
-                                   (1025, 1, 9), (1000, 4, 1000), (4096, 1, 7), (4097, 1, 7), (2049, 2, 255), (5000, 3, 256), (0, 2, 5), (5, 0, 5)])
+                                   (1025, 1, 9), (1000, 4, 1000), (4096, 1, 7), (4097, 1, 7), (2049, 2, 255),
+                                   (5000, 3, 256), (0, 2, 5), (5, 0, 5)])
 def test_sort(kind, T, k, n):
     for dt in (torch.int64, torch.int32):
         check_sort(DEV, make_ids(kind, T, k, n), n, dt)
@@ -71,7 +72,8 @@ def test_rows_at_any_alignment(F):
         y = F.adapter_combine(F.adapter_gather(x, place), None, place, x)
         count = (ids >= 0).sum(dim=1, keepdim=True)
         assert torch.equal(y, (x.float() * (1 + count)).to(x.dtype))
-        assert torch.equal(F.adapter_combine(F.adapter_gather(x, place), torch.ones(2, 12, device=DEV).t(), place, x), y)
+        ones = torch.ones(2, 12, device=DEV).t()
+        assert torch.equal(F.adapter_combine(F.adapter_gather(x, place), ones, place, x), y)
 
 
 def test_unused_values():

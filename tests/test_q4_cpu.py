@@ -1,5 +1,6 @@
 """The 4-bit weight without a GPU: pins of its oracle, the eager tier against it,
 the layer's gradients, and the entry points' refusals."""
+import concurrent.futures
 from fractions import Fraction
 
 import numpy as np
@@ -318,6 +319,25 @@ def test_pack_refusals(name):
     _status(fn(e=FAR[2] + 4), INVALID, "alignment")
     _status(fn(W=FAR[1] + 16), INVALID, "overlaps")
     assert fn(out=0, W=None, q=None) == OK and fn(in_=0, W=None, q=None) == OK
+
+
+def test_pack_refuses_more_threads_than_a_launch_holds():
+    n = 1 << 20  # 2^40 elements, 32 a thread
+    _status(LIB.dora_q4_pack_weight(1 << 60, n, n, 0, 1 << 58, 1 << 56, None), UNSUPPORTED, "threads")
+    _status(LIB.dora_q4_unpack_weight(1 << 58, 1 << 56, n, n, 0, 1 << 60, None), UNSUPPORTED, "threads")
+
+
+def test_workspace_is_that_of_the_sizes_whatever_came_before():
+    """The plans are kept by their sizes: asked in another order, and in another thread, the answers are the same."""
+    sizes = [(T, o, i) for T in (1, 2, 17, 48, 49, 300, 4096) for o in (96, 4096, 5121) for i in (64, 1000, 8192)]
+
+    def ask(order):
+        return {(k, s): getattr(LIB, f"dora_q4_linear_{k}workspace_bytes")(*s) for s in order for k in ("", "bwd_")}
+
+    first = ask(sizes)
+    assert len(set(first.values())) > 10 and ask(sizes[::-1]) == first
+    with concurrent.futures.ThreadPoolExecutor(4) as pool:
+        assert all(a == first for a in pool.map(ask, [sizes, sizes[::-1], sizes[::2] + sizes[1::2], sizes]))
 
 
 @pytest.mark.parametrize("name", ["fwd", "bwd"])
