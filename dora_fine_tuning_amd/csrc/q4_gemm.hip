@@ -7,6 +7,18 @@
 // A weight value leaves its 4 bits as an exact bf16 or fp16 value (the scale is a
 // power of two, applied by the conversion), so the products are those of the
 // 16-bit matrix instruction: exact in fp32, added in fp32, rounded once.
+//
+// What bounds them, with whole calls in us (weights from memory for few rows):
+//   1 row, 4096^2 and 27648 x 5120 (8.9 and 75 MB of weight): 5.4 and 15.4 in the
+//     kernel, 4.9 TB/s of the second's bytes; the first is a launch and one latency;
+//   37 rows, 27648 columns into 5120: 27.8, a ring of stages on 240 of the CUs that
+//     waits for memory, and the join of 12 ranges (5.4 of it);
+//   300 rows, backward of 8192^2: 50.5 (0.80 PFLOP/s), 57 % of the cycles in matrix
+//     instructions; 384 rows are multiplied, and the join of 2 ranges takes 8.5;
+//   8192 rows of 8192^2: 715 to 737 forward (1.5 PFLOP/s); 10240 rows, backward of
+//     27648 x 5120: 1940 to 2000 (1.45 to 1.49).  Matrix instructions are busy for 77 and
+//     80 % of the cycles at 1.69 and 1.75 GHz: the card's power is the limit, so that
+//     what takes fewer cycles alone gives part of them back as clock.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -460,7 +472,7 @@ __device__ inline void store_group(__amdgpu_buffer_rsrc_t ry, int vec, uint32_t 
   }
 }
 
-// One workgroup a CU, each taking its units in turn (tile_units.hpp).  The ring runs
+// Two or three workgroups a CU, each taking its units in turn (tile_units.hpp).  The ring runs
 // on from one unit to the next: while a unit's last slots are worked on, the next
 // one's first ones load, and its stores are under way while the next one's products
 // run.  A step of 32 works on fragments that were read and converted during the step
@@ -1016,8 +1028,8 @@ void launch_typed(const GemmArgs& g, const Q4Plan& p, hipStream_t stream) {
 // fitted to 5600 calls (nine weights from 512 x 512 to 27648 x 5120, both directions, 1
 // to 8192 rows, every kind with 1 to 16 ranges, weights out of the caches); over them
 // the plan's call takes 1.1 % more than the fastest measured one on the mean with the
-// tiles (12 % at most) and 3.0 % forward, 1.2 % backward with the kernels for few rows
-// (21 % at most).
+// tiles (12 % at most) and 2.8 % forward, 1.2 % backward with the kernels for few rows
+// (29 and 20 % at most, both with 32 rows).
 Q4Plan q4_plan(int64_t T, int64_t out, int64_t in, bool trans) {
   Q4Plan p;
   p.N = trans ? in : out;

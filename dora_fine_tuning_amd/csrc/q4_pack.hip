@@ -4,6 +4,9 @@
 // unpacking the reverse.  A block of 32 is 4 lanes of 8 values (one 16-byte load
 // each); a workgroup's 256 lanes are one tile of 32 x 64, and take kU tiles of a
 // row of tiles, all loads in flight before the first maximum.
+//
+// 27648 x 5120 in bf16 (358 MB): packing 66 us (5.4 TB/s), unpacking 53 to 68; 8192^2
+// (170 MB): 26.6 and 27.2 (6.3 TB/s), where a copy of 2 GiB reaches 4.9.
 #include "q4_common.hpp"
 
 namespace dora {

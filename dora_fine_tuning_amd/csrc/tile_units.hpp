@@ -1,5 +1,6 @@
 // How the tile kernels of the packed products share out their work: tiles of the
-// output over one workgroup a CU, the last ones split over the contraction.
+// output over as many workgroups as the card holds at once, the last ones split over
+// the contraction.
 #pragma once
 
 #include <hip/hip_runtime.h>
