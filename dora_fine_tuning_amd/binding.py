@@ -54,6 +54,8 @@ EXPORTS = (
     "dora_q4_linear_fwd",
     "dora_q4_linear_bwd_workspace_bytes",
     "dora_q4_linear_bwd",
+    "dora_q4_norm_workspace_bytes",
+    "dora_q4_norm_cached",
     "dora_adapter_sort_workspace_bytes",
     "dora_adapter_sort",
     "dora_adapter_gather",
@@ -129,6 +131,10 @@ def _load() -> ctypes.CDLL:
     for name in ("dora_q4_linear_fwd", "dora_q4_linear_bwd"):
         getattr(lib, name).argtypes = [vp, vp, vp, i64, i64, i64, i32, vp, vp, sz, vp]
         getattr(lib, name).restype = i32
+    lib.dora_q4_norm_workspace_bytes.argtypes = [i64, i64, i64, i32]
+    lib.dora_q4_norm_workspace_bytes.restype = sz
+    lib.dora_q4_norm_cached.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, f32, i32, vp, vp, sz, vp]
+    lib.dora_q4_norm_cached.restype = i32
     lib.dora_adapter_sort.argtypes = [vp, i32, i64, i64, i64, vp, vp, vp, vp, sz, vp]
     lib.dora_adapter_sort.restype = i32
     lib.dora_adapter_gather.argtypes = [vp, vp, i64, i64, i64, i32, vp, vp]
@@ -702,6 +708,24 @@ def dora_q4_linear_bwd(g, q, e, in_: int):
         _check(LIB.dora_q4_linear_bwd(_ptr(g), _ptr(q), _ptr(e), T, out, in_, code, _ptr(dx), _ptr(ws), need,
                                       _raw_stream(dev)))
     return dx
+
+
+def dora_q4_norm_cached(q, e, A, B, base_sq, s: float):
+    """||W + s*B*A|| per row (fp32 [out]) of a packed weight, with ||W_i||^2 from base_sq (fp32 [out])."""
+    code = _code(A)
+    (r, in_), out, dev = _shape2(A, "A"), _shape2(B, "B")[0], A.device
+    _matrix(A, "A", (r, in_))
+    _matrix(B, "B", (out, r), A.dtype, dev)
+    _matrix(base_sq, "base_sq", (out,), torch.float32, dev)
+    _q4_packed(q, e, q4_weight_shapes(out, in_), dev)
+    A, B = _aligned(A), _aligned(B)
+    with _on_device(dev):
+        n = torch.empty(out, dtype=torch.float32, device=dev)
+        need = int(LIB.dora_q4_norm_workspace_bytes(out, in_, r, code))
+        ws = _workspace(need, dev)
+        _check(LIB.dora_q4_norm_cached(_ptr(q), _ptr(e), _ptr(A), _ptr(B), _ptr(base_sq), out, in_, r, float(s), code,
+                                       _ptr(n), _ptr(ws), need, _raw_stream(dev)))
+    return n
 
 
 # ------------------------------------------------------------ tokens sorted by adapter

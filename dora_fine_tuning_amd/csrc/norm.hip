@@ -1425,6 +1425,11 @@ hipError_t launch_norm_bwd_db_t(const NormPlan& p, const void* W0, const void* A
 
 }  // namespace
 
+hipError_t launch_norm_gram(const NormPlan& p, const void* A, float scale, void* ws, hipStream_t stream) {
+  char* w = static_cast<char*>(ws);
+  return p.dtype == 0 ? launch_gram_t<0>(p, A, scale, w, true, stream) : launch_gram_t<1>(p, A, scale, w, true, stream);
+}
+
 size_t norm_bwd_acc_bytes(const NormPlan& p) { return static_cast<size_t>(p.nSplit) * p.out * p.r * 4; }
 
 hipError_t launch_norm_bwd_db(const NormPlan& p, const void* W0, const void* A, const void* B, float s,

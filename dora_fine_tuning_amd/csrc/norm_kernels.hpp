@@ -68,6 +68,8 @@ struct NormArgs {
 };
 
 hipError_t launch_norm(const NormPlan& p, const NormArgs& a);
+// G' = scale * A A^T alone, as the pair G'hi + G'lo [r x r] at off_ghi and off_glo of ws (16-byte path plans).
+hipError_t launch_norm_gram(const NormPlan& p, const void* A, float scale, void* ws, hipStream_t stream);
 hipError_t launch_norm_strip(const NormPlan& p, const NormArgs& a);
 
 // sq[i] = ||W0_i||^2 in fp32 (vec: in % 8 == 0 and W0 16-byte aligned); grid cdiv(out, 4).

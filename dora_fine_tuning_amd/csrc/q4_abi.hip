@@ -2,6 +2,7 @@
 // Every check runs before the first HIP call, so invalid calls touch no device.
 #include "../../include/dora.h"
 #include "abi_common.hpp"
+#include "norm_kernels.hpp"
 #include "q4_common.hpp"
 
 using namespace dora::abi;
@@ -60,9 +61,10 @@ const dora::Q4Plan& plan_of(int64_t T, int64_t out, int64_t in, bool trans) {
     dora::Q4Plan plan;
   };
   static thread_local Entry table[64];
-  const uint64_t mix = (static_cast<uint64_t>(T) * 0x9e3779b97f4a7c15u ^ static_cast<uint64_t>(out)) * 0x9e3779b97f4a7c15u ^
+  constexpr uint64_t kOdd = 0x9e3779b97f4a7c15u;
+  const uint64_t mix = (static_cast<uint64_t>(T) * kOdd ^ static_cast<uint64_t>(out)) * kOdd ^
                        static_cast<uint64_t>(in) * 2 ^ (trans ? 1u : 0u);
-  Entry& e = table[mix * 0x9e3779b97f4a7c15u >> 58];
+  Entry& e = table[mix * kOdd >> 58];
   if (e.T != T || e.out != out || e.in != in || e.trans != trans)  // (T >= 1)
     e = Entry{T, out, in, trans, dora::q4_plan(T, out, in, trans)};
   return e.plan;
@@ -97,6 +99,25 @@ int gemm_call(const char* fn, const void* x, const void* q, const void* e, int64
                 (long long)T, (long long)out, (long long)in);
   const dora::Q4GemmArgs a{x, q, e, T, out, in, dtype, trans, y, ws, stream};
   return hip_status(dora::launch_q4_gemm(a, plan), fn);
+}
+
+// The norm: ranks whose sums, fp32 [r x out], are small beside the weight in 16 bits, and
+// the Gram kernels' own limit of columns.
+constexpr int64_t kNormMaxRank = 512, kNormMaxCols = int64_t(1) << 21;
+
+bool norm_takes(int64_t out, int64_t in, int64_t r) {
+  return out > 0 && in > 0 && r > 0 && out <= kMaxCols && in < kNormMaxCols && r <= kNormMaxRank && in % 8 == 0 &&
+         r % 8 == 0;
+}
+// Its workspace: the Gram kernels' (their plan), then the product's sums.
+struct NormPlans {
+  dora::NormPlan gram;
+  dora::Q4Plan product;
+  size_t at() const { return (gram.bytes + 255) / 256 * 256; }
+  size_t bytes() const { return at() + product.workspace(); }
+};
+NormPlans norm_plans(int64_t out, int64_t in, int64_t r, int dtype) {
+  return {dora::make_norm_plan(out, in, r, dtype, true), dora::q4_parts_plan(plan_of(r, out, in, false), r)};
 }
 
 }  // namespace
@@ -140,6 +161,45 @@ size_t dora_q4_linear_bwd_workspace_bytes(int64_t T, int64_t out, int64_t in) { 
 int dora_q4_linear_bwd(const void* g, const void* q, const void* e, int64_t T, int64_t out, int64_t in, int dtype,
                        void* dx, void* ws, size_t ws_bytes, hipStream_t stream) {
   return gemm_call("dora_q4_linear_bwd", g, q, e, T, out, in, dtype, true, dx, ws, ws_bytes, stream);
+}
+
+size_t dora_q4_norm_workspace_bytes(int64_t out, int64_t in, int64_t r, int dtype) {
+  return valid_dtype(dtype) && norm_takes(out, in, r) ? norm_plans(out, in, r, dtype).bytes() : 0;
+}
+
+int dora_q4_norm_cached(const void* q, const void* e, const void* A, const void* B, const float* base_sq, int64_t out,
+                        int64_t in, int64_t r, float s, int dtype, float* norm_out, void* ws, size_t ws_bytes,
+                        hipStream_t stream) {
+  const char* fn = "dora_q4_norm_cached";
+  if (int st = check_sizes(fn, dtype, r, out, in)) return st;
+  if (out == 0) return ok();
+  if (!norm_takes(out, in, r))
+    return fail(DORA_UNSUPPORTED, "%s: out=%lld in=%lld r=%lld: in and r are to be multiples of 8, r up to %lld", fn,
+                (long long)out, (long long)in, (long long)r, (long long)kNormMaxRank);
+  if (int st = weight_ptrs(fn, q, e)) return st;
+  if (!A || !B || !aligned16(A) || !aligned16(B))
+    return fail(DORA_INVALID_ARG, "%s: A or B is NULL or not 16-byte aligned", fn);
+  if (!base_sq || !norm_out || !aligned(base_sq, 4) || !aligned(norm_out, 4))
+    return fail(DORA_INVALID_ARG, "%s: base_sq or norm_out is NULL or not 4-byte aligned", fn);
+  const NormPlans p = norm_plans(out, in, r, dtype);
+  if (ws_bytes < p.bytes())
+    return fail(DORA_INVALID_ARG, "%s: workspace of %zu bytes, %zu needed", fn, ws_bytes, p.bytes());
+  if (!ws || !aligned16(ws)) return fail(DORA_INVALID_ARG, "%s: workspace is NULL or not 16-byte aligned", fn);
+  const size_t n4 = static_cast<size_t>(out) * 4;
+  const Range outs[2] = {{norm_out, n4}, {ws, p.bytes()}};
+  const Range ins[5] = {
+      {q, weight_q(out, in)}, {e, weight_e(out, in)}, {A, mat16(r, in)}, {B, mat16(out, r)}, {base_sq, n4}};
+  if (outputs_overlap(outs, ins)) return fail(DORA_INVALID_ARG, "%s: an output overlaps another argument", fn);
+  if (p.product.units() > INT32_MAX || dora::norm_max_grid(p.gram) > INT32_MAX)
+    return fail(DORA_UNSUPPORTED, "%s: out=%lld in=%lld r=%lld needs more workgroups than one launch holds", fn,
+                (long long)out, (long long)in, (long long)r);
+  char* w = static_cast<char*>(ws);
+  if (int st = hip_status(dora::launch_norm_gram(p.gram, A, s * 0.5f, w, stream), fn)) return st;
+  const dora::Q4GemmArgs a{A, q, e, r, out, in, dtype, false, nullptr, w + p.at(), stream};
+  if (int st = hip_status(dora::launch_q4_gemm(a, p.product), fn)) return st;
+  const dora::Q4NormArgs n{B, w + p.gram.off_ghi, w + p.gram.off_glo, base_sq, reinterpret_cast<float*>(w + p.at()),
+                           out, r, dtype, s, norm_out, stream};
+  return hip_status(dora::launch_q4_norm_join(n, dora::q4_parts_of(p.product, r)), fn);
 }
 
 }  // extern "C"

@@ -107,11 +107,36 @@ struct Q4Plan {
   int S = 0, nSplit = 1;         // stages of 64; ranges of them
   int64_t nRB = 0, nTiles = 0, whole = 0, grid = 0;
   size_t pad = 0, bytes = 0;  // of padded rows; of a split's fp32 sums
+  bool parts = false;         // the sums stay in the workspace, for q4_norm.hip
   size_t workspace() const { return pad + bytes; }
   // units of work (tiles in up to 16 ranges) are numbered in 32 bits
   int64_t units() const { return nRB * nTiles * 16 > grid ? nRB * nTiles * 16 : grid; }
 };
 Q4Plan q4_plan(int64_t T, int64_t out, int64_t in, bool trans);
 hipError_t launch_q4_gemm(const Q4GemmArgs& a, const Q4Plan& plan);
+
+// Where a forward product leaves its sums if they stay in the workspace: entries of 64
+// register quads, one of each lane, for 16 rows of x and, with half h, the output columns
+// 32 rt + 8 (lane / 16) + 4 h + register.
+struct Q4Parts {
+  int few, nSplit;
+  int64_t all;  // groups or tiles of a range
+  int R, NT;                                  // few rows: row and token tiles of a group
+  int WM, WN, TMW, TNW, nRB, nTiles, group;   // tiles
+};
+Q4Plan q4_parts_plan(Q4Plan p, int64_t T);  // from q4_plan's
+Q4Parts q4_parts_of(const Q4Plan& p, int64_t T);
+
+// The norm of a packed weight with an adapter (q4_norm.hip).  ghi, glo: (s/2) A A^T.
+struct Q4NormArgs {
+  const void *B, *ghi, *glo;
+  const float *base_sq, *part;
+  int64_t out, r;
+  int dtype;
+  float s;
+  float* norm;
+  hipStream_t stream;
+};
+hipError_t launch_q4_norm_join(const Q4NormArgs& a, const Q4Parts& parts);
 
 }  // namespace dora

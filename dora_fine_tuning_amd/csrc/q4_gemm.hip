@@ -39,7 +39,7 @@ struct GemmArgs : TileGrid {
   int rt, ct;  // row and column tiles of the weight
   void* y;
   int vec;  // 16-byte stores of y
-  float* part;
+  float* part;  // sums of ranges, null where there is none to keep
 };
 
 // Eight consecutive output columns of a row, from column c on.
@@ -210,7 +210,7 @@ __global__ __launch_bounds__(64 * FW::NW) void q4_few(GemmArgs a) {
       f32x4 v = red[0][i];
 #pragma unroll
       for (int w = 1; w < NW; ++w) v += red[w][i];
-      if (a.nSplit > 1) {
+      if (a.part) {
         reinterpret_cast<f32x4*>(a.part)[(static_cast<int64_t>(blockIdx.x) * R + r) * (NT * 2 * 64) + i] = v;
       } else {
         const int l = i & 63, h = (i >> 6) & 1, t = i >> 7;
@@ -778,7 +778,7 @@ __global__ __launch_bounds__(TL::NT, TL::OCC) void q4_gemm_tile(GemmArgs a) {
     int el = static_cast<int>(threadIdx.x) & 63;
     asm volatile("" : "+v"(el));
     const uint32_t er = static_cast<uint32_t>(el & 15);
-    const bool part = cu.tail >= 0 && a.nSplit > 1;
+    const bool part = cu.tail >= 0 && a.part != nullptr;
     // a split's fp32 tile: 16 bytes a lane, in the order the join reads it
     const int64_t tile = static_cast<int64_t>(cu.split) * (a.nRB * a.nTiles - a.whole) + cu.tail;
     f32x4* p = reinterpret_cast<f32x4*>(a.part) + (tile * TL::NW + wave) * (NM * 64) + el;
@@ -918,12 +918,14 @@ double few_us(const Q4Plan& p, int64_t T, int64_t out, int64_t in, bool trans) {
          (p.nSplit > 1 ? 1.50 + 0.156 * p.nSplit + 0.687 * part_mb : 0.0);
 }
 
+constexpr int kTileGroup = 8;  // column tiles of a group of the tile order
+
 struct TileKind {
   Q4Plan::Path path;
   int64_t bm, bn, occ;
   double us[2][3];  // a stage forward and backward, with one to three workgroups on a CU
 };
-constexpr TileKind kTiles[] = {
+constexpr TileKind kTiles[] = {  // in the order of Q4Plan::Path
     {Q4Plan::kLow, 64, 128, 3, {{0.372, 0.490, 0.691}, {0.591, 0.805, 0.959}}},
     {Q4Plan::kThin, 48, 256, 2, {{0.445, 0.602, 0.0}, {0.663, 0.813, 0.0}}},
     {Q4Plan::kFlat, 64, 256, 2, {{0.508, 0.721, 0.0}, {0.703, 0.905, 0.0}}},
@@ -960,7 +962,7 @@ double tile_us(Q4Plan& p, int64_t T, const TileKind& t, bool trans) {
 template <int DT, class TL>
 void launch_tile(const GemmArgs& g, const Q4Plan& p, hipStream_t stream) {
   hipLaunchKernelGGL((q4_gemm_tile<DT, TL>), dim3(static_cast<unsigned>(p.grid)), dim3(TL::NT), 0, stream, g);
-  if (p.nSplit > 1) {
+  if (p.nSplit > 1 && !p.parts) {
     const int64_t waves = (p.nRB * p.nTiles - p.whole) * TL::NW * TL::NM / (TL::TRANS ? TL::TNW : 2);
     hipLaunchKernelGGL((q4_gemm_join<DT, TL>), dim3(static_cast<unsigned>(q4_ceil(waves, 4))), dim3(256), 0, stream, g);
   }
@@ -969,7 +971,7 @@ void launch_tile(const GemmArgs& g, const Q4Plan& p, hipStream_t stream) {
 template <int DT, class FW>
 void launch_few_as(const GemmArgs& g, const Q4Plan& p, hipStream_t stream) {
   hipLaunchKernelGGL((q4_few<DT, FW>), dim3(static_cast<unsigned>(p.grid)), dim3(64 * FW::NW), 0, stream, g);
-  if (p.nSplit > 1) {
+  if (p.nSplit > 1 && !p.parts) {
     const dim3 grid(static_cast<unsigned>(q4_ceil(p.grid / p.nSplit * FW::ENTRIES, 256)));
     hipLaunchKernelGGL((q4_few_join<DT, FW>), grid, dim3(256), 0, stream, g);
   }
@@ -1059,6 +1061,60 @@ Q4Plan q4_plan(int64_t T, int64_t out, int64_t in, bool trans) {
   return best;
 }
 
+// The plan of a forward product whose sums all stay in the workspace: as many ranges as
+// the product's plan has where it splits every tile, else one.
+Q4Plan q4_parts_plan(Q4Plan p, int64_t T) {
+  p.parts = true;
+  if (p.path == Q4Plan::kFew) {
+    p.bytes = static_cast<size_t>(p.grid) * 2 * p.R * 64 * q4_ceil(T, 16) * 16;
+    return p;
+  }
+  const TileKind& t = kTiles[p.path];
+  const int64_t tiles = p.nRB * p.nTiles;
+  if (p.whole > 0) p.nSplit = 1;
+  p.whole = 0;
+  p.grid = std::min<int64_t>(kCUs * t.occ, q4_ceil(tiles * p.nSplit, 8) * 8);
+  p.bytes = static_cast<size_t>(tiles) * p.nSplit * t.bm * t.bn * 4;
+  return p;
+}
+
+Q4Parts q4_parts_of(const Q4Plan& p, int64_t T) {
+  Q4Parts a{};
+  a.nSplit = p.nSplit;
+  a.few = p.path == Q4Plan::kFew;
+  if (a.few) {
+    a.R = p.R;
+    a.NT = static_cast<int>(q4_ceil(T, 16));
+    a.all = p.grid / p.nSplit;
+    return a;
+  }
+  auto of = [&](auto tl) {
+    using TL = decltype(tl);
+    a.WM = TL::WM, a.WN = TL::WN, a.TMW = TL::TMW, a.TNW = TL::TNW;
+  };
+  switch (p.path) {
+    case Q4Plan::kLow:
+      of(LowTile<false>{});
+      break;
+    case Q4Plan::kThin:
+      of(ThinTile<false>{});
+      break;
+    case Q4Plan::kFlat:
+      of(FlatTile<false>{});
+      break;
+    case Q4Plan::kBroad:
+      of(BroadTile<false>{});
+      break;
+    default:
+      of(WideTile<false>{});
+  }
+  a.all = p.nRB * p.nTiles;
+  a.nRB = static_cast<int>(p.nRB);
+  a.nTiles = static_cast<int>(p.nTiles);
+  a.group = kTileGroup;
+  return a;
+}
+
 hipError_t launch_q4_gemm(const Q4GemmArgs& p, const Q4Plan& plan) {
   if (plan.K == 0) {
     const int64_t n = p.T * plan.N;
@@ -1088,10 +1144,10 @@ hipError_t launch_q4_gemm(const Q4GemmArgs& p, const Q4Plan& plan) {
   g.nTiles = static_cast<int>(plan.nTiles);
   g.nSplit = plan.nSplit;
   g.whole = static_cast<int>(plan.whole);
-  g.group = 8;
+  g.group = kTileGroup;
   g.y = p.y;
   g.vec = plan.N % 8 == 0 && (reinterpret_cast<uintptr_t>(p.y) & 15u) == 0;
-  g.part = reinterpret_cast<float*>(static_cast<char*>(p.ws) + plan.pad);
+  g.part = plan.bytes > 0 ? reinterpret_cast<float*>(static_cast<char*>(p.ws) + plan.pad) : nullptr;
   if (p.dtype == 0)
     p.trans ? launch_typed<0, true>(g, plan, p.stream) : launch_typed<0, false>(g, plan, p.stream);
   else

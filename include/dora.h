@@ -54,6 +54,7 @@
  *                              blocks of 32 of e2m1 with a power-of-two scale;
  *   dora_q4_linear_fwd, dora_q4_linear_bwd
  *                              x W0^T and g W0 with 16-bit x and g;
+ *   dora_q4_norm_cached        dora_norm_factored_cached of a packed W0;
  *
  * and, for a batch whose tokens use different adapters over the one W0:
  *
@@ -534,6 +535,21 @@ DORA_API size_t dora_q4_linear_bwd_workspace_bytes(int64_t T, int64_t out, int64
  */
 DORA_API int dora_q4_linear_bwd(const void* g, const void* q, const void* e, int64_t T, int64_t out, int64_t in,
                                 int dtype, void* dx, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* Bytes of device workspace dora_q4_norm_cached needs (0 for sizes that it does not take). */
+DORA_API size_t dora_q4_norm_workspace_bytes(int64_t out, int64_t in, int64_t r, int dtype);
+
+/*
+ * dora_norm_factored_cached of a packed weight: norm_out [out] (fp32) = ||W0 + s * B * A||
+ * per row, with ||W0_i||^2 of the values held from base_sq (fp32).  W0 is not unpacked:
+ * the product W0 A^T keeps its fp32 sums in the workspace.  A [r x in], B [out x r] and
+ * ws are 16-byte aligned, in and r multiples of 8, in below 2^21 and 0 < r <= 512 (else
+ * DORA_UNSUPPORTED: unpack rows and use dora_norm_factored_cached).  No output may
+ * overlap an input or another output.
+ */
+DORA_API int dora_q4_norm_cached(const void* q, const void* e, const void* A, const void* B, const float* base_sq,
+                                 int64_t out, int64_t in, int64_t r, float s, int dtype, float* norm_out, void* ws,
+                                 size_t ws_bytes, hipStream_t stream);
 
 /*
  * ---- Tokens sorted by adapter ---------------------------------------------

@@ -373,6 +373,35 @@ def test_linear_refusals(name):
     assert query(0, 8, 8) == 0 and query(-1, 8, 8) == 0 and query(8, 1 << 24, 8) == 0
 
 
+def test_norm_refusals():
+    def call(q=FAR[0], e=FAR[1], A=FAR[2], B=FAR[3], c=FAR[4], out=256, in_=512, r=16, dt=0, n=FAR[5], ws=FAR[6],
+             wsb=1 << 39):
+        return LIB.dora_q4_norm_cached(q, e, A, B, c, out, in_, r, 1.0, dt, n, ws, wsb, None)
+
+    _status(call(dt=2), UNSUPPORTED, "dtype")
+    _status(call(out=-1), INVALID, "negative")
+    _status(call(r=-8), INVALID, "negative")
+    for sizes in ({"r": 0}, {"r": 12}, {"r": 520}, {"in_": 0}, {"in_": 515}, {"in_": 1 << 21}):
+        _status(call(**sizes), UNSUPPORTED, "multiples of 8")
+        s = {"r": 16, "in_": 512, **sizes}
+        assert LIB.dora_q4_norm_workspace_bytes(256, s["in_"], s["r"], 0) == 0
+    _status(call(out=1 << 22), UNSUPPORTED, "beyond")
+    _status(call(q=None), INVALID, "packed weight")
+    _status(call(e=FAR[1] + 4), INVALID, "alignment")
+    _status(call(A=None), INVALID, "NULL")
+    _status(call(B=FAR[3] + 2), INVALID, "aligned")
+    _status(call(c=None), INVALID, "base_sq")
+    _status(call(n=FAR[5] + 2), INVALID, "norm_out")
+    need = LIB.dora_q4_norm_workspace_bytes(256, 512, 16, 0)
+    _status(call(wsb=need - 1), INVALID, "workspace of")
+    _status(call(ws=None, wsb=need), INVALID, "workspace is NULL")
+    _status(call(ws=FAR[6] + 8), INVALID, "aligned")
+    _status(call(n=FAR[4]), INVALID, "overlaps")
+    _status(call(ws=FAR[0] - need + 16), INVALID, "overlaps")
+    _status(call(n=FAR[6] + 16), INVALID, "overlaps")
+    assert call(out=0, q=None) == OK
+
+
 def test_binding_refuses_other_devices_and_types():
     q, e = F.q4_pack_weight(torch.zeros(4, 200).bfloat16())
     with pytest.raises(ValueError, match="HIP device"):
