@@ -5,12 +5,19 @@
 // c_i = ||W_i||^2.  W A^T is the forward product on the r rows of A, whose fp32 sums
 // stay in the workspace as its kernels leave them (q4_gemm.hip): 17/32 bytes an element
 // of W are read instead of the 5 that unpacking to 16 bits, and reading that, take.
+// Whole calls: 26 us at rank 16 of 8192^2 (168 by unpacked rows), 41 at rank 64 of
+// 27648 x 5120 (590), 83 at rank 384 of 8192^2 (195): of these 48 the product, 27 the join
+// and 12 the Gram matrix.
 // (s/2) A A^T comes as two 16-bit matrices from the 16-bit norm's Gram kernels (norm.hip).
+#include <algorithm>
+
 #include "q4_common.hpp"
 
 namespace dora {
 
 namespace {
+
+constexpr int kMaxWaves = 16;
 
 struct JoinArgs : Q4NormArgs, Q4Parts {};
 
@@ -26,78 +33,113 @@ __device__ inline int64_t entry_of(const Q4Parts& a, int64_t rt, int tt, int h) 
   return (v * a.WM * a.WN + wm * a.WN + wn) * (a.TMW * a.TNW) + i * a.TNW + j % a.TNW + h;
 }
 
-// A workgroup 32 outputs, a wave every fourth 16 rows of A: B's rows times (s/2) A A^T by
-// the matrix instruction in the layout of the entries, these added in the order of their
-// ranges, and the dot with B.
-template <int DT>
-__global__ __launch_bounds__(256) void q4_norm_join(JoinArgs a) {
+// A workgroup 64 outputs, whose rows of B stand in LDS as fragments (KS steps of 32 of the
+// rank); its waves, one for 16 rows of A and 16 at most, take 16 rows of A in turn: B times
+// (s/2) A A^T by the matrix instruction, in the layout of the entries, these added in the
+// order of their ranges, and the dot with B.  The loads bound it: 27 us at rank 384 of 8192
+// outputs and 90 at rank 512 of 27648 (40 and 260 with B from the caches too, workgroups of
+// 32 outputs; 65 and 89 with B in registers and (s/2) A A^T through LDS, in step), 10 at
+// rank 64.
+template <int DT, int KS>
+__global__ __launch_bounds__(64 * kMaxWaves) void q4_norm_join(JoinArgs a) {
   using T16 = typename Dt<DT>::T;
   using V8 = typename Dt<DT>::V8;
-  __shared__ float red[4][32];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l16 = lane & 15, g = lane >> 4;
-  const int64_t rt = blockIdx.x, c0 = rt * 32;
-  const int r = static_cast<int>(a.r);
-  const T16* B = static_cast<const T16*>(a.B);
-  const T16 *ghi = static_cast<const T16*>(a.ghi), *glo = static_cast<const T16*>(a.glo);
+  __shared__ Chunk bs[KS * 4][64];  // step, row tile, half
+  __shared__ float red[kMaxWaves][64];
+  const int lane = threadIdx.x & 63, l16 = lane & 15, g = lane >> 4, waves = blockDim.x >> 6;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t rt = 2 * static_cast<int64_t>(blockIdx.x), c0 = rt * 32;
+  const int r = static_cast<int>(a.r), steps = (r + 31) / 32;
+  const int tiles = c0 + 32 < a.out ? 2 : 1;
   const int64_t stride = a.all * (a.few ? a.R * a.NT * 2 : a.WM * a.WN * a.TMW * a.TNW) * 64;  // of ranges
-  float dot[2][4] = {};
-  for (int tt = wave; tt * 16 < r; tt += 4) {
-    const int j = tt * 16 + l16;
-    f32x4 u[2] = {};
-    for (int k0 = 0; k0 < r; k0 += 32) {
-      const int k = k0 + 8 * g;
-      const bool in = k < r && j < r;
-      const V8 hi = __builtin_bit_cast(V8, in ? *reinterpret_cast<const Chunk*>(ghi + j * r + k) : zero_chunk());
-      const V8 lo = __builtin_bit_cast(V8, in ? *reinterpret_cast<const Chunk*>(glo + j * r + k) : zero_chunk());
+  // eight elements of a row from 32 ks + 8 g on, zeros past its end
+  auto chunk = [&](const T16* row, int ks) {
+    const int k = 32 * ks + 8 * g;
+    const Chunk c = *reinterpret_cast<const Chunk*>(row + min(k, r - 8));
+    return k < r ? c : zero_chunk();
+  };
+  // Row l16 of the product's left operand comes out as register l16 % 4 of lane group
+  // l16 / 4.  Rows past the last are that one again, and not used.
+  for (int f = wave; f < 4 * steps; f += waves) {
+    const int64_t c = c0 + 32 * ((f >> 1) & 1) + 8 * (l16 >> 2) + 4 * (f & 1) + (l16 & 3);
+    bs[f][lane] = chunk(static_cast<const T16*>(a.B) + min(c, a.out - 1) * r, f >> 2);
+  }
+  __syncthreads();
+  float dot[4][4] = {};
+  for (int tt = wave; 16 * tt < r; tt += waves) {
+    const int j = 16 * tt + l16, row = min(j, r - 1) * r;
+    const T16 *hp = static_cast<const T16*>(a.ghi) + row, *lp = static_cast<const T16*>(a.glo) + row;
+    const f32x4* p[4];
+    f32x4 v[4], u[4] = {};
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int64_t c = c0 + 8 * (l16 >> 2) + 4 * h + (l16 & 3);  // row l16 is register l16 % 4 of group l16 / 4
-        const V8 b = __builtin_bit_cast(
-            V8, k < r && c < a.out ? *reinterpret_cast<const Chunk*>(B + c * r + k) : zero_chunk());
-        u[h] = Dt<DT>::mfma16(b, lo, Dt<DT>::mfma16(b, hi, u[h]));
+    for (int x = 0; x < 4; ++x) {
+      p[x] = reinterpret_cast<const f32x4*>(a.part) + entry_of(a, rt + ((x >> 1) & (tiles - 1)), tt, x & 1) * 64 + lane;
+      v[x] = *p[x];
+    }
+    for (int k0 = 0; k0 < steps; k0 += 4) {  // the loads of four steps before their products
+      Chunk hi[4], lo[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) hi[i] = chunk(hp, k0 + i), lo[i] = chunk(lp, k0 + i);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (k0 + i < steps) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const V8 w = __builtin_bit_cast(V8, bs[(k0 + i) * 4 + x][lane]);
+            u[x] = Dt<DT>::mfma16(w, __builtin_bit_cast(V8, hi[i]), u[x]);
+            u[x] = Dt<DT>::mfma16(w, __builtin_bit_cast(V8, lo[i]), u[x]);
+          }
+        }
       }
     }
+    for (int s = 1; s < a.nSplit; ++s)
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const f32x4* p = reinterpret_cast<const f32x4*>(a.part) + entry_of(a, rt, tt, h) * 64 + lane;
-      f32x4 v = p[0];
-      for (int s = 1; s < a.nSplit; ++s) v += p[s * stride];
-      u[h] += v;
+      for (int x = 0; x < 4; ++x) v[x] += p[x][s * stride];
+    // B at output 8 g + 4 h + q and column j, of which bs has eight a lane
+    const T16* bj = reinterpret_cast<const T16*>(&bs[(j >> 5) * 4][16 * ((j >> 3) & 3) + 4 * g]) + (j & 7);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int64_t c = c0 + 8 * g + 4 * h + q;
-        if (j < r && c < a.out) dot[h][q] = __builtin_fmaf(static_cast<float>(B[c * r + j]), u[h][q], dot[h][q]);
-      }
-    }
+    for (int x = 0; x < 4; ++x)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (j < r) dot[x][q] = __builtin_fmaf(static_cast<float>(bj[(x * 64 + q) * 8]), u[x][q] + v[x][q], dot[x][q]);
   }
 #pragma unroll
-  for (int h = 0; h < 2; ++h)
+  for (int x = 0; x < 4; ++x)
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      float v = dot[h][q];
+      float d = dot[x][q];
 #pragma unroll
-      for (int d = 8; d > 0; d >>= 1) v += __shfl_xor(v, d, 64);
-      if (l16 == 0) red[wave][8 * g + 4 * h + q] = v;
+      for (int o = 8; o > 0; o >>= 1) d += __shfl_xor(d, o, 64);
+      if (l16 == 0) red[wave][32 * (x >> 1) + 8 * g + 4 * (x & 1) + q] = d;
     }
   __syncthreads();
   const int64_t c = c0 + threadIdx.x;
-  if (threadIdx.x < 32 && c < a.out) {
-    const int t = threadIdx.x;
-    const double sum = (static_cast<double>(red[0][t]) + red[1][t]) + (static_cast<double>(red[2][t]) + red[3][t]);
+  if (threadIdx.x < 64 && c < a.out) {
+    double sum = 0.0;
+    for (int w = 0; w < waves; ++w) sum += static_cast<double>(red[w][threadIdx.x]);
     const double n2 = static_cast<double>(a.base_sq[c]) + 2.0 * static_cast<double>(a.s) * sum;
     a.norm[c] = static_cast<float>(n2 > 0.0 ? sqrt(n2) : 0.0);
   }
+}
+
+template <int DT>
+void launch_join(const JoinArgs& a) {
+  const dim3 grid(static_cast<unsigned>(q4_ceil(a.out, 64)));
+  const dim3 block(static_cast<unsigned>(64 * std::min<int64_t>(q4_ceil(a.r, 16), kMaxWaves)));
+  if (a.r <= 128)  // less LDS: more workgroups a CU
+    hipLaunchKernelGGL((q4_norm_join<DT, 4>), grid, block, 0, a.stream, a);
+  else  // r <= 512
+    hipLaunchKernelGGL((q4_norm_join<DT, 16>), grid, block, 0, a.stream, a);
 }
 
 }  // namespace
 
 hipError_t launch_q4_norm_join(const Q4NormArgs& n, const Q4Parts& parts) {
   const JoinArgs a{n, parts};
-  const dim3 grid(static_cast<unsigned>(q4_ceil(n.out, 32)));
   if (n.dtype == 0)
-    hipLaunchKernelGGL(q4_norm_join<0>, grid, dim3(256), 0, n.stream, a);
+    launch_join<0>(a);
   else
-    hipLaunchKernelGGL(q4_norm_join<1>, grid, dim3(256), 0, n.stream, a);
+    launch_join<1>(a);
   return hipGetLastError();
 }
 
