@@ -36,7 +36,7 @@ This module registers:
 * the 4-bit weight: ``q4_pack_weight`` / ``q4_unpack_weight`` (e2m1 blocks of 32
   with a power-of-two scale each), ``q4_linear`` (x W0^T from 16-bit x) and
   ``q4_linear_backward`` (g W0), each the other's autograd formula, and
-  ``q4_weight_norm``, the norm of a W0 held so.
+  ``q4_weight_norm``, the norm of a W0 held so, from the packed values.
 * tokens sorted by adapter: ``adapter_sort`` (a batch's slots by adapter),
   ``adapter_gather`` (tokens' rows in that order) and ``adapter_combine`` (rows
   added up per token, with weights; ``adapter_combine_backward`` is its formula).
@@ -1068,7 +1068,8 @@ def _q4_slabs(q, e, out, in_, dtype):
 @torch.library.custom_op("dora_amd::q4_weight_norm", mutates_args=())
 @_without_autocast
 def q4_weight_norm(q: Tensor, e: Tensor, A: Tensor, B: Tensor, base_sq: Tensor, s: float) -> Tensor:
-    """``weight_norm_cached`` of a weight packed in 4 bits."""
+    """``weight_norm_cached`` of a weight packed in 4 bits (by slabs of unpacked rows
+    where the kernel does not take the sizes)."""
     r, in_ = A.shape
     if _kernels_take(A, B) and 0 < r <= 512 and r % 8 == 0 and 0 < in_ < 2**21 and in_ % 8 == 0:
         return binding.dora_q4_norm_cached(q.contiguous(), e.contiguous(), A.contiguous(), B.contiguous(),
