@@ -64,6 +64,32 @@ def test_norm_of_large_weights(b, out, in_, r):
         assert torch.equal(b.dora_q4_norm_cached(q, e, A, B, c, 2.0), got)
 
 
+# sizes at which each kernel of the product is the one taken, whole and in ranges, and one
+# whose product would have whole rounds with ranges behind them (all whole here)
+EVERY = [(512, 512, 8), (1024, 8192, 16), (512, 512, 24), (1024, 8192, 24), (512, 512, 40), (1024, 8192, 48),
+         (12000, 2000, 16), (12000, 2000, 24), (4096, 4096, 32), (12000, 2000, 40), (4096, 4096, 48),
+         (27648, 5120, 16), (8192, 8192, 16), (27648, 5120, 32), (8192, 8192, 32), (27648, 5120, 384),
+         (5120, 27648, 264), (27648, 5120, 200), (8192, 8192, 200), (27648, 5120, 264), (512, 512, 64),
+         (1024, 8192, 128), (8192, 1024, 264), (4096, 4096, 192), (27648, 5120, 512)]
+
+
+@pytest.mark.parametrize("odd", [False, True])
+@pytest.mark.parametrize("out,in_,r", EVERY)
+def test_norm_by_every_kernel(b, out, in_, r, odd):
+    """Against 64 bits on the GPU; |B A| is too small beside W for the terms to cancel."""
+    out -= 5 * odd
+    g = torch.Generator(device=DEV)
+    g.manual_seed(out + r)
+    rand = lambda *s: torch.randn(s, generator=g, device=DEV).bfloat16()
+    q, e = b.dora_q4_pack_weight(rand(out, in_) * 0.02)
+    W = b.dora_q4_unpack_weight(q, e, out, in_, torch.bfloat16)
+    A, B, c = rand(r, in_) * 0.02, rand(out, r) * 0.02, b.dora_row_sqnorm(W)
+    got = b.dora_q4_norm_cached(q, e, A, B, c, 2.0).double()
+    V = B.double() @ A.double()
+    n = (c.double() + (4.0 * W.double() * V + 4.0 * V * V).sum(dim=1)).sqrt()
+    assert bool(((got - n).abs() <= 1e-5 * n).all()), (got / n - 1).abs().max()
+
+
 @pytest.mark.parametrize("r", [16, 64])
 def test_cancelling_rows(b, r):
     """c so small that the sum is negative (0 then), and rows whose terms nearly cancel."""
