@@ -786,11 +786,15 @@ def dora_adapter_combine(rows, weights, place, base=None):
 
 
 def dora_adapter_combine_bwd(dy, rows, weights, place, want_rows: bool = True, want_weights: bool = True):
-    """(d_rows [T k x D], d_weights [T x k] fp32) of the combination, None where not wanted."""
+    """(d_rows [T k x D], d_weights [T x k] fp32) of the combination, None where not wanted (rows: None without
+    the latter)."""
     code = _code(dy)
     (T, D), k, dev = _shape2(dy, "dy"), _shape2(place, "place")[1], dy.device
     _matrix(dy, "dy", (T, D))
-    _matrix(rows, "rows", (T * k, D), dy.dtype, dev)
+    if rows is not None:
+        _matrix(rows, "rows", (T * k, D), dy.dtype, dev)
+    elif want_weights:
+        raise ValueError("the gradient of the weights needs the rows")
     _matrix(place, "place", (T, k), torch.int32, dev)
     if weights is not None:
         _matrix(weights, "weights", (T, k), torch.float32, dev)

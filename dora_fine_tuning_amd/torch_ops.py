@@ -1167,7 +1167,7 @@ def _slot_rows(rows, place):
 
 
 def _check_rows(rows, weights, place, base=None):
-    if rows.dim() != 2 or rows.shape[0] != place.numel():
+    if rows is not None and (rows.dim() != 2 or rows.shape[0] != place.numel()):
         raise ValueError(f"rows are {tuple(rows.shape)}, expected one for each of {place.numel()} slots")
     if weights is not None and weights.shape != place.shape:
         raise ValueError(f"weights are {tuple(weights.shape)}, expected {tuple(place.shape)}")
@@ -1192,6 +1192,8 @@ def _eager_adapter_combine(rows, weights, place, base):
 @_q8_eager
 def _eager_adapter_combine_backward(dy, rows, weights, place, want_rows, want_weights):
     _check_place(place, dy.shape[0], "dy")
+    if rows is None and want_weights:
+        raise ValueError("the gradient of the weights needs the rows")
     _check_rows(rows, weights, place)
     R, (T, k) = place.numel(), place.shape
     d = dy.float()
@@ -1224,9 +1226,11 @@ class _AdapterGather(torch.autograd.Function):
 
 
 class _AdapterCombine(torch.autograd.Function):
+    """The rows, T k x D, are kept only where the gradient of the weights reads them."""
+
     @staticmethod
     def forward(ctx, below, rows, weights, place, base):
-        ctx.save_for_backward(rows, weights, place)
+        ctx.save_for_backward(rows if ctx.needs_input_grad[2] else None, weights, place)
         return below(rows, weights, place, base)
 
     @staticmethod
@@ -1288,22 +1292,22 @@ def _adapter_combine_fake(rows, weights, place, base):
 
 
 @_q8_kernel("adapter_combine_backward")
-def adapter_combine_backward(dy: Tensor, rows: Tensor, weights: Optional[Tensor], place: Tensor, want_rows: bool,
-                             want_weights: bool) -> tuple[Tensor, Tensor]:
+def adapter_combine_backward(dy: Tensor, rows: Optional[Tensor], weights: Optional[Tensor], place: Tensor,
+                             want_rows: bool, want_weights: bool) -> tuple[Tensor, Tensor]:
     """(d_rows, d_weights in fp32) of ``adapter_combine``; an empty tensor stands in
-    for one that is not wanted."""
-    if not _kernels_take(dy, rows):
+    for one that is not wanted.  rows are read for d_weights alone and may be None without."""
+    if not _kernels_take(dy) or not (rows is None or _kernels_take(rows)):
         return _eager_adapter_combine_backward(dy, rows, weights, place, want_rows, want_weights)
     d_rows, d_w = binding.dora_adapter_combine_bwd(
-        dy.contiguous(), rows.contiguous(), None if weights is None else weights.contiguous().float(),
-        place.contiguous(), want_rows, want_weights)
+        dy.contiguous(), None if rows is None else rows.contiguous(),
+        None if weights is None else weights.contiguous().float(), place.contiguous(), want_rows, want_weights)
     return (dy.new_empty((0,)) if d_rows is None else d_rows,
             dy.new_empty((0,), dtype=torch.float32) if d_w is None else d_w)
 
 
 @torch.library.register_fake("dora_amd::adapter_combine_backward")
 def _adapter_combine_backward_fake(dy, rows, weights, place, want_rows, want_weights):
-    return (rows.new_empty(rows.shape if want_rows else (0,)),
+    return (dy.new_empty((place.shape[0] * place.shape[1], dy.shape[1]) if want_rows else (0,)),
             dy.new_empty(place.shape if want_weights else (0,), dtype=torch.float32))
 
 
