@@ -1225,6 +1225,19 @@ class _AdapterGather(torch.autograd.Function):
         return None, adapter_combine(d_rows, None, ctx.saved_tensors[0], None), None
 
 
+class _AdapterCombineGrads(torch.autograd.Function):
+    """``adapter_combine_backward`` as it stands in a graph of gradients (create_graph): its own
+    gradient is refused where it is asked for, as the compose's backward's is."""
+
+    @staticmethod
+    def forward(ctx, *args):
+        return adapter_combine_backward(*args)
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError("adapter_combine_backward has no gradient of its own")
+
+
 class _AdapterCombine(torch.autograd.Function):
     """The rows, T k x D, are kept only where the gradient of the weights reads them."""
 
@@ -1239,7 +1252,7 @@ class _AdapterCombine(torch.autograd.Function):
         need = ctx.needs_input_grad
         d_rows = d_w = None
         if need[1] or need[2]:
-            d_rows, d_w = adapter_combine_backward(dy, rows, weights, place, need[1], need[2])
+            d_rows, d_w = _AdapterCombineGrads.apply(dy, rows, weights, place, need[1], need[2])
         return (None, d_rows if need[1] else None, d_w.to(weights.dtype) if need[2] else None, None,
                 dy if need[4] else None)
 
