@@ -1070,10 +1070,13 @@ def _q4_slabs(q, e, out, in_, dtype):
 def q4_weight_norm(q: Tensor, e: Tensor, A: Tensor, B: Tensor, base_sq: Tensor, s: float) -> Tensor:
     """``weight_norm_cached`` of a weight packed in 4 bits (by slabs of unpacked rows
     where the kernel does not take the sizes)."""
-    r, in_ = A.shape
-    if _kernels_take(A, B) and 0 < r <= 512 and r % 8 == 0 and 0 < in_ < 2**21 and in_ % 8 == 0:
-        return binding.dora_q4_norm_cached(q.contiguous(), e.contiguous(), A.contiguous(), B.contiguous(),
-                                           base_sq.contiguous().float(), s)
+    if _kernels_take(A, B):
+        try:
+            return binding.dora_q4_norm_cached(q.contiguous(), e.contiguous(), A.contiguous(), B.contiguous(),
+                                               base_sq.contiguous().float(), s)
+        except binding.DoraError as err:
+            if not _unsupported(err):
+                raise
     return _norm_of_slabs(_q4_slabs(q, e, B.shape[0], A.shape[1], A.dtype), A, B, base_sq, s)
 
 
