@@ -394,7 +394,7 @@ struct Q4Tile {
   static constexpr bool FIRST = TRANS || TMW < 8;
   static_assert(WM * WN == NW && WQ * NW == WT, "whole DMA instructions per wave");
   static_assert(WT * 16 <= NW * 64, "exponents of a stage in one DMA instruction a wave");
-  static_assert(!TRANS || TNW == 8 || TNW == 4, "a backward lane's columns");
+  static_assert(!TRANS || TNW == 4, "a backward lane's columns");
   static_assert(TNW % 2 == 0 && NS >= 3, "pairs of half tiles; the ring");
   static_assert(WAIT + NST < 64, "vmcnt range");
   static_assert(LDS_BYTES * OCC <= 160 * 1024, "LDS");
@@ -405,13 +405,6 @@ __device__ inline u32x2 lds_read8_at(uint32_t base) {
   static_assert(OFF >= 0 && OFF < 65536, "ds offset field");
   u32x2 v;
   asm volatile("ds_read_b64 %0, %1 offset:%2" : "=v"(v) : "v"(base), "n"(OFF) : "memory");
-  return v;
-}
-template <int OFF>
-__device__ inline uint32_t lds_read4_at(uint32_t base) {
-  static_assert(OFF >= 0 && OFF < 65536, "ds offset field");
-  uint32_t v;
-  asm volatile("ds_read_b32 %0, %1 offset:%2" : "=v"(v) : "v"(base), "n"(OFF) : "memory");
   return v;
 }
 template <int OFF>
@@ -448,7 +441,7 @@ __device__ inline __amdgpu_buffer_rsrc_t rows_of_y(const GemmArgs& a, int64_t m,
 // The fragments of a group of matrix tiles (two forward, TNW backward) of one row of
 // them, as the 16-byte pieces of y they are.  Forward: register q of half tile h is
 // column 8 g + 4 h + q (g = lane / 16).  Backward: register q of fragment f is
-// column TNW * (4 g + q) + f.
+// column 4 * (4 g + q) + f.
 template <int DT, class TL>
 __device__ inline void store_group(__amdgpu_buffer_rsrc_t ry, int vec, uint32_t row, int64_t N, int64_t c0, int lane,
                                    const f32x4* acc) {
@@ -456,12 +449,6 @@ __device__ inline void store_group(__amdgpu_buffer_rsrc_t ry, int vec, uint32_t 
   if constexpr (!TL::TRANS) {
     const float f[8] = {acc[0][0], acc[0][1], acc[0][2], acc[0][3], acc[1][0], acc[1][1], acc[1][2], acc[1][3]};
     store8_to<DT>(ry, vec, row, n, c + 8 * g, f);
-  } else if constexpr (TL::TNW == 8) {
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const float f[8] = {acc[0][q], acc[1][q], acc[2][q], acc[3][q], acc[4][q], acc[5][q], acc[6][q], acc[7][q]};
-      store8_to<DT>(ry, vec, row, n, c + 32 * g + 8 * q, f);
-    }
   } else {
 #pragma unroll
     for (int q = 0; q < 4; q += 2) {
@@ -610,8 +597,6 @@ __global__ __launch_bounds__(TL::NT, TL::OCC) void q4_gemm_tile(GemmArgs a) {
       constexpr int st = s * TL::CT * TL::WSTEP;
       if constexpr (i == 8)
         rawbe = lds_read8_at<s * TL::CT * 64>(ea + so);
-      else if constexpr (TL::TNW == 8)
-        rawb[i] = lds_read4_at<st + 128 * i>(wa[(i >> 1) & 1] + so);
       else
         rawb[i] = lds_read2_at<st + 128 * i>(wa[(i >> 1) & 1] + so);
     } else {
