@@ -54,6 +54,7 @@ EXPORTS = (
     "dora_q4_linear_fwd",
     "dora_q4_linear_bwd_workspace_bytes",
     "dora_q4_linear_bwd",
+    "dora_q4_plan",
     "dora_q4_norm_workspace_bytes",
     "dora_q4_norm_cached",
     "dora_adapter_sort_workspace_bytes",
@@ -131,6 +132,8 @@ def _load() -> ctypes.CDLL:
     for name in ("dora_q4_linear_fwd", "dora_q4_linear_bwd"):
         getattr(lib, name).argtypes = [vp, vp, vp, i64, i64, i64, i32, vp, vp, sz, vp]
         getattr(lib, name).restype = i32
+    lib.dora_q4_plan.argtypes = [i64, i64, i64, i32, vp]
+    lib.dora_q4_plan.restype = i32
     lib.dora_q4_norm_workspace_bytes.argtypes = [i64, i64, i64, i32]
     lib.dora_q4_norm_workspace_bytes.restype = sz
     lib.dora_q4_norm_cached.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, f32, i32, vp, vp, sz, vp]
@@ -708,6 +711,14 @@ def dora_q4_linear_bwd(g, q, e, in_: int):
         _check(LIB.dora_q4_linear_bwd(_ptr(g), _ptr(q), _ptr(e), T, out, in_, code, _ptr(dx), _ptr(ws), need,
                                       _raw_stream(dev)))
     return dx
+
+
+def dora_q4_plan(T: int, out: int, in_: int, product: int) -> tuple[int, ...]:
+    """(tile rows, tile columns, tiles of whole rounds, other tiles, ranges of these, workgroups) of the kernel
+    that the forward (product 0), the backward (1) or the norm's product (2) of these sizes takes."""
+    plan = (ctypes.c_int64 * 6)()
+    _check(LIB.dora_q4_plan(T, out, in_, product, ctypes.addressof(plan)))
+    return tuple(plan)
 
 
 def dora_q4_norm_cached(q, e, A, B, base_sq, s: float):

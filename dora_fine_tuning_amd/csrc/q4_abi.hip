@@ -1,5 +1,7 @@
 // C ABI of the 4-bit weight: argument validation, workspace queries, launch.
 // Every check runs before the first HIP call, so invalid calls touch no device.
+#include <algorithm>
+
 #include "../../include/dora.h"
 #include "abi_common.hpp"
 #include "norm_kernels.hpp"
@@ -161,6 +163,22 @@ size_t dora_q4_linear_bwd_workspace_bytes(int64_t T, int64_t out, int64_t in) { 
 int dora_q4_linear_bwd(const void* g, const void* q, const void* e, int64_t T, int64_t out, int64_t in, int dtype,
                        void* dx, void* ws, size_t ws_bytes, hipStream_t stream) {
   return gemm_call("dora_q4_linear_bwd", g, q, e, T, out, in, dtype, true, dx, ws, ws_bytes, stream);
+}
+
+int dora_q4_plan(int64_t T, int64_t out, int64_t in, int product, int64_t* plan) {
+  const char* fn = "dora_q4_plan";
+  if (int st = check_sizes(fn, 0, T, out, in)) return st;
+  if (!plan) return fail(DORA_INVALID_ARG, "%s: plan is NULL", fn);
+  if (product < 0 || product > 2) return fail(DORA_INVALID_ARG, "%s: unknown product %d", fn, product);
+  if (product == 2 && out > 0 && !norm_takes(out, in, T))
+    return fail(DORA_UNSUPPORTED, "%s: out=%lld in=%lld r=%lld is not taken by the norm", fn, (long long)out,
+                (long long)in, (long long)T);
+  std::fill(plan, plan + 6, 0);
+  if (T == 0 || out == 0 || in == 0) return ok();
+  dora::Q4Plan p = plan_of(T, out, in, product == 1);
+  if (product == 2) p = dora::q4_parts_plan(p, T);
+  dora::q4_plan_numbers(p, product == 1, plan);
+  return ok();
 }
 
 size_t dora_q4_norm_workspace_bytes(int64_t out, int64_t in, int64_t r, int dtype) {

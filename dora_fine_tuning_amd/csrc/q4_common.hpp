@@ -114,6 +114,7 @@ struct Q4Plan {
 };
 Q4Plan q4_plan(int64_t T, int64_t out, int64_t in, bool trans);
 hipError_t launch_q4_gemm(const Q4GemmArgs& a, const Q4Plan& plan);
+void q4_plan_numbers(const Q4Plan& p, bool trans, int64_t* n);  // as dora_q4_plan gives them
 
 // Where a forward product leaves its sums if they stay in the workspace: entries of 64
 // register quads, one of each lane, for 16 rows of x and, with half h, the output columns

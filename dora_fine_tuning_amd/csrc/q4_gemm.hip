@@ -1046,6 +1046,16 @@ Q4Plan q4_plan(int64_t T, int64_t out, int64_t in, bool trans) {
   return best;
 }
 
+void q4_plan_numbers(const Q4Plan& p, bool trans, int64_t* n) {
+  const bool few = p.path == Q4Plan::kFew;
+  n[0] = few ? 0 : kTiles[p.path].bm;
+  n[1] = !few ? kTiles[p.path].bn : trans ? 128 : p.R * kQ4Rows;
+  n[2] = p.whole;
+  n[3] = few ? p.grid / p.nSplit : p.nRB * p.nTiles - p.whole;
+  n[4] = p.nSplit;
+  n[5] = p.grid;
+}
+
 // The plan of a forward product whose sums all stay in the workspace: as many ranges as
 // the product's plan has where it splits every tile, else one.
 Q4Plan q4_parts_plan(Q4Plan p, int64_t T) {

@@ -40,7 +40,8 @@ def main() -> int:
     env["DORA_HIP_LIB"] = lib
     cmd = [sys.executable, "-m", "pytest", "-x", "-q", "-p", "no:cacheprovider",
            *(os.path.join(ROOT, "tests", f) for f in ("test_abi_cpu.py", "test_q8_cpu.py", "test_q8_norm_slabs.py",
-                                                      "test_q4_cpu.py", "test_adapters_cpu.py")),
+                                                      "test_q4_cpu.py", "test_q4_plans_cpu.py",
+                                                      "test_adapters_cpu.py")),
            "-m", "not gpu", "-k", "abi or refus or workspace or valid or bind"]
     print("running:", " ".join(cmd), f"(DORA_HIP_LIB={lib})", flush=True)
     return subprocess.call(cmd, cwd=ROOT, env=env)

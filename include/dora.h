@@ -536,6 +536,21 @@ DORA_API size_t dora_q4_linear_bwd_workspace_bytes(int64_t T, int64_t out, int64
 DORA_API int dora_q4_linear_bwd(const void* g, const void* q, const void* e, int64_t T, int64_t out, int64_t in,
                                 int dtype, void* dx, void* ws, size_t ws_bytes, hipStream_t stream);
 
+/*
+ * The kernel that a call's sizes ask for, on the host: tests name with it what they
+ * run, and sweeps what they time.  product 0: dora_q4_linear_fwd of T rows, 1:
+ * dora_q4_linear_bwd, 2: the product in dora_q4_norm_cached (T: the rank).  plan [6]:
+ *   0  rows of a tile; 0 for the kernels for few rows
+ *   1  columns of a tile; for few rows, of a workgroup's group
+ *   2  tiles that fill whole rounds of workgroups, each with its whole contraction
+ *   3  the other tiles (for few rows: all groups)
+ *   4  ranges of the contraction of these
+ *   5  workgroups
+ * All zeros for an empty product, which a fill kernel takes.  The choice is no part of
+ * the interface: another version may take others.
+ */
+DORA_API int dora_q4_plan(int64_t T, int64_t out, int64_t in, int product, int64_t* plan);
+
 /* Bytes of device workspace dora_q4_norm_cached needs (0 for sizes that it does not take). */
 DORA_API size_t dora_q4_norm_workspace_bytes(int64_t out, int64_t in, int64_t r, int dtype);
 
