@@ -10,10 +10,12 @@
 //   combine      y[t] = base[t] + sum_j w[t, j] rows[place[t, j]]
 //   its backward d_rows[p] = w[t, j] dy[t],  d_w[t, j] = <dy[t], rows[p]>
 //
-// gather's backward is combine without weights or base.  All go by tokens: a
-// token's row is read once and its k rows read or written, so that nothing is
-// fetched twice, no sum needs an atomic, and every row is written, those without
-// an adapter as zeros.
+// gather's backward is combine without weights or base.  All go by tokens: the
+// threads of a token read or write its row and its k rows, so that no sum needs an
+// atomic, and every row is written, those without an adapter as zeros.  Gather and
+// combine read each row once; combine's backward takes the slots in turn and reads
+// the row of dy for each, after the first from the caches (the bytes of the rates
+// below count it once).
 //
 // HBM bounds the rows (8192 tokens of 2 slots, rows of 8192 in bf16: gather 77 us, 5.2
 // TB/s; combine with base and weights 100, 5.3; its backward 135, 5.0; one slot and

@@ -14,7 +14,7 @@
 //   37 rows, 27648 columns into 5120: 27.8, a ring of stages on 240 of the CUs that
 //     waits for memory, and the join of 12 ranges (5.4 of it);
 //   300 rows, backward of 8192^2: 50.5 (0.80 PFLOP/s), 57 % of the cycles in matrix
-//     instructions; 384 rows are multiplied, and the join of 2 ranges takes 8.5;
+//     instructions; 384 rows are multiplied, by 96, and the join of 4 ranges takes 8.5;
 //   8192 rows of 8192^2: 715 to 737 forward (1.5 PFLOP/s); 10240 rows, backward of
 //     27648 x 5120: 1940 to 2000 (1.45 to 1.49).  Matrix instructions are busy for 77 and
 //     80 % of the cycles at 1.69 and 1.75 GHz: the card's power is the limit, so that
@@ -1012,10 +1012,10 @@ void launch_typed(const GemmArgs& g, const Q4Plan& p, hipStream_t stream) {
 }  // namespace
 
 // The kernel, its tile and its ranges are those expected to be fastest.  The times are
-// fitted to 5600 calls (nine weights from 512 x 512 to 27648 x 5120, both directions, 1
-// to 8192 rows, every kind with 1 to 16 ranges, weights out of the caches); over them
-// the plan's call takes 1.1 % more than the fastest measured one on the mean with the
-// tiles (12 % at most) and 2.8 % forward, 1.2 % backward with the kernels for few rows
+// fitted to 15263 calls (nine weights from 512 x 512 to 27648 x 5120, both directions, 1
+// to 8192 rows, every kind with up to 16 ranges, weights out of the caches); over them
+// the plan's call takes 1.0 % more than the fastest measured one on the mean with the
+// tiles (12 % at most) and 3.1 % forward, 1.2 % backward with the kernels for few rows
 // (29 and 20 % at most, both with 32 rows).
 Q4Plan q4_plan(int64_t T, int64_t out, int64_t in, bool trans) {
   Q4Plan p;
