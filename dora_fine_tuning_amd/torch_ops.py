@@ -1069,7 +1069,7 @@ def _q4_slabs(q, e, out, in_, dtype):
 @_without_autocast
 def q4_weight_norm(q: Tensor, e: Tensor, A: Tensor, B: Tensor, base_sq: Tensor, s: float) -> Tensor:
     """``weight_norm_cached`` of a weight packed in 4 bits (by slabs of unpacked rows
-    where the kernel does not take the sizes)."""
+    where the kernel does not take the sizes, or A and B in fp32, under autocast too)."""
     if _kernels_take(A, B):
         try:
             return binding.dora_q4_norm_cached(q.contiguous(), e.contiguous(), A.contiguous(), B.contiguous(),
